@@ -37,6 +37,8 @@ EXPORTED = (
     "dwc_version", "dwc_status_string", "dwc_last_error", "dwc_output_dims",
     "dwc_check", "dwc_plan_describe", "dwc_fwd", "dwc_fwd_fused", "dwc_bwd_data",
     "dwc_bwd_filter_workspace_size", "dwc_bwd_filter", "dwc_bwd_filter_noalloc",
+    "dwc_layer_norm", "dwc_layer_norm_bwd_workspace_size", "dwc_layer_norm_bwd", "dwc_dropout",
+    "dwc_delta_step", "dwc_delta_workspace_size", "dwc_delta_fwd", "dwc_delta_bwd",
 )
 
 
@@ -87,6 +89,7 @@ def lib() -> ctypes.CDLL:
         l.dwc_bwd_filter_workspace_size.argtypes = [P, ctypes.POINTER(ctypes.c_size_t)]
         l.dwc_bwd_filter.argtypes = [P, vp, vp, vp, vp, ctypes.c_size_t, vp]
         l.dwc_bwd_filter_noalloc.argtypes = [P, vp, vp, vp, vp]
+        sequence.bind(l)
         for name in EXPORTED:
             if name not in ("dwc_status_string", "dwc_last_error"):
                 getattr(l, name).restype = ctypes.c_int
@@ -321,3 +324,8 @@ def bwd_filter_noalloc(x: torch.Tensor, dy: torch.Tensor, f_hw: Sequence[int], s
         raise ValueError(f"out must be {(fh, fw, c)}")
     bwd_filter_noalloc_ptr(p, x.data_ptr(), dy.data_ptr(), out.data_ptr(), _stream(stream))
     return out
+
+
+from . import sequence  # noqa: E402  (needs the names above)
+from .sequence import (delta_rule, delta_rule_bwd, delta_rule_step, dropout,  # noqa: E402,F401
+                       layer_norm, layer_norm_bwd)

@@ -57,6 +57,11 @@ def _units():
               ["-mllvm", "-amdgpu-mfma-vgpr-form"]))
     u.append(("hip", "inst_mfma_f32.hip", "inst_mfma_f32.o", ["-mllvm", "-amdgpu-mfma-vgpr-form"]))
     u.append(("hip", "inst_mfma_h4.hip", "inst_mfma_h4.o", ["-mllvm", "-amdgpu-mfma-vgpr-form"]))
+    # layer norm, dropout and the gated delta rule
+    u.append(("hip", "seq/seq_norm.hip", "seq_norm.o", []))
+    u.append(("hip", "seq/seq_dropout.hip", "seq_dropout.o", []))
+    u.append(("hip", "seq/seq_delta_token.hip", "seq_delta_token.o", []))
+    u.append(("hip", "seq/seq_api.cpp", "seq_api.o", ["-x", "hip"]))
     u.append(("hip", "dwc_api.cpp", "dwc_api.o", ["-x", "hip"]))
     u.append(("cxx", "dwc_plan.cpp", "dwc_plan.o", []))
     return u

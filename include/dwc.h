@@ -263,6 +263,137 @@ int dwc_bwd_filter(const dwc_problem* p, const void* x, const void* dy,
 int dwc_bwd_filter_noalloc(const dwc_problem* p, const void* x, const void* dy,
                            void* dw, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators of the sequence layer around a depthwise convolution: layer
+ * norm, dropout and the gated delta rule.  Ownership, threading, streams and
+ * errors are as above: the caller owns every tensor and workspace, nothing
+ * is allocated, nothing synchronises, argument errors are reported before
+ * anything is launched.  Types are DWC_F32, DWC_BF16 and DWC_F16; all sums,
+ * statistics and states are fp32, each output is rounded once.
+ * ------------------------------------------------------------------------ */
+
+/* Layer norm over the last axis of a rows x c matrix:
+ *   m = mean(x), r = 1 / sqrt(mean((x - m)^2) + eps), h = (x - m) r
+ *   y = h w + b
+ * and its gradients, with e = dy w:
+ *   dx = r (e - mean(e) - h mean(e h)), dw = sum_rows dy h, db = sum_rows dy */
+typedef struct {
+    int64_t rows, c;    /* rows >= 0, c >= 1                               */
+    int64_t x_stride;   /* elements between rows of x, >= c                */
+    int64_t dy_stride;  /* elements between rows of dy, >= c (backward)    */
+    int32_t x_dtype;    /* x, dx                                           */
+    int32_t y_dtype;    /* y, dy                                           */
+    int32_t w_dtype;    /* w, b (dw and db are fp32)                       */
+    float eps;          /* >= 0                                            */
+} dwc_norm_problem;
+
+/* y: rows x c, dense; mean, rstd: rows fp32 values, both NULL if not wanted;
+ * w, b: c values each, NULL for 1 and 0. */
+int dwc_layer_norm(const dwc_norm_problem* p, const void* x, const void* w,
+                   const void* b, void* y, float* mean, float* rstd,
+                   void* stream);
+
+/* Bytes of workspace dwc_layer_norm_bwd needs (column partials). */
+int dwc_layer_norm_bwd_workspace_size(const dwc_norm_problem* p, size_t* bytes);
+
+/* dx: rows x c, dense; dw, db: c fp32 values (either may be NULL), summed
+ * over the rows in a fixed order: the same bits on every call. */
+int dwc_layer_norm_bwd(const dwc_norm_problem* p, const void* dy,
+                       const void* x, const float* mean, const float* rstd,
+                       const void* w, void* dx, float* dw, float* db,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Dropout of n elements with a mask that is never stored:
+ *   y = residual + (kept ? x / (1 - p) : 0)
+ * Element i is kept where word i % 4 of Philox4x32 with 7 rounds (counter
+ * offset + i / 4 in the low 64 bits, key seed) is at least round(p 2^32);
+ * p = 1 keeps none.  The backward pass is the same call on dy with the same
+ * p, seed and offset and no residual.  A dropped infinity or NaN gives 0.
+ * Calls that must not share masks take offsets that are (n + 3) / 4 apart. */
+typedef struct {
+    int64_t n;       /* >= 0                                                */
+    double p;        /* 0 <= p <= 1                                         */
+    uint64_t seed;
+    uint64_t offset;
+    int32_t dtype;   /* x, residual, y                                      */
+    int32_t reserved;
+} dwc_dropout_problem;
+
+/* x, y (and residual, if not NULL): n elements, dense. */
+int dwc_dropout(const dwc_dropout_problem* p, const void* x,
+                const void* residual, void* y, void* stream);
+
+/* The gated delta rule.  Per sequence and value head, with a state S of
+ * dk x dv that starts at s0 (or zero), a_t = exp(g_t):
+ *   u_t = beta_t (v_t - (a_t S_{t-1})^T k_t),  S_t = a_t S_{t-1} + k_t u_t^T,
+ *   o_t = scale S_t^T q_t
+ * hv value heads share hk query/key heads: value head h uses query and key
+ * head h / (hv / hk).
+ *   q, k : b x l x hk x dk of dtype     strides in elements (batch, token,
+ *   v    : b x l x hv x dv of dtype     head); the last axis is dense
+ *   g, beta : b x l x hv fp32
+ *   s0, s1  : b x hv x dk x dv fp32, dense; s0 may be NULL (zeros)
+ *   lengths : b int32 in device memory, or NULL: sequence i ends after
+ *             lengths[i] tokens (clamped to 0..l).  What stands in q, k, v,
+ *             g, beta past it is not used, o there is 0, s1 is the state
+ *             after the last token (s0 for an empty sequence)
+ *   o    : b x l x hv x dv of dtype, dense
+ * g = -inf forgets the state; values below -1e5 act as -1e5 (exp of it is
+ * 0).  q, k, v, s0 of live tokens must be finite in the chunked calls: a
+ * matrix product multiplies masked places by zero too, so an infinity or
+ * NaN in a live token may turn outputs of earlier tokens of its chunk of 64
+ * into NaN. */
+typedef struct {
+    int64_t b, l;           /* sequences and tokens, >= 0                   */
+    int64_t q_stride[3], k_stride[3], v_stride[3], g_stride[3],
+        beta_stride[3], do_stride[3]; /* do_stride: gradient of o, bwd only */
+    int32_t hk, hv;         /* >= 1, hv a multiple of hk                    */
+    int32_t dk, dv;         /* 1..256 and 1..4096 (token by token);
+                               dk up to 128 in the chunked calls            */
+    int32_t dtype;
+    float scale;            /* finite; 1 / sqrt(dk) as a rule               */
+} dwc_delta_problem;
+
+/* Token by token, the form for one or a few new tokens of each sequence.
+ * s1 may be s0 itself (the state updated in place). */
+int dwc_delta_step(const dwc_delta_problem* p, const void* q, const void* k,
+                   const void* v, const float* g, const float* beta,
+                   const float* s0, const int32_t* lengths, void* o,
+                   float* s1, void* stream);
+
+#define DWC_DELTA_FWD 0
+#define DWC_DELTA_BWD 1
+/* Bytes of workspace of dwc_delta_fwd or dwc_delta_bwd (may be 0). */
+int dwc_delta_workspace_size(const dwc_delta_problem* p, int op,
+                             size_t* bytes);
+
+/* Whole sequences: chunks of 64 tokens as matrix products, the state carried
+ * from chunk to chunk.  workspace: dwc_delta_workspace_size(p,
+ * DWC_DELTA_FWD) bytes, 256-byte aligned. */
+int dwc_delta_fwd(const dwc_delta_problem* p, const void* q, const void* k,
+                  const void* v, const float* g, const float* beta,
+                  const float* s0, const int32_t* lengths, void* o,
+                  float* s1, void* workspace, size_t workspace_bytes,
+                  void* stream);
+
+/* Gradients of the above from dout (gradient of o, of dtype, do_stride) and
+ * ds1 (gradient of s1, dense fp32, or NULL for zero):
+ *   dq, dk_out : b x l x hk x dk of dtype, dense (summed over the value
+ *                heads that share them)
+ *   dv_out : b x l x hv x dv of dtype, dense
+ *   dg, dbeta : b x l x hv fp32, dense
+ *   ds0 : as s0, or NULL if not wanted
+ * Tokens past a sequence's length get zeros.  Nothing of the forward call
+ * is needed: states are computed again.  The sums' order is fixed: the same
+ * bits on every call. */
+int dwc_delta_bwd(const dwc_delta_problem* p, const void* dout,
+                  const float* ds1, const void* q, const void* k,
+                  const void* v, const float* g, const float* beta,
+                  const float* s0, const int32_t* lengths, void* dq,
+                  void* dk_out, void* dv_out, float* dg, float* dbeta,
+                  float* ds0, void* workspace, size_t workspace_bytes,
+                  void* stream);
+
 #ifdef __cplusplus
 }
 #endif
