@@ -61,6 +61,11 @@ def _units():
     u.append(("hip", "seq/seq_norm.hip", "seq_norm.o", []))
     u.append(("hip", "seq/seq_dropout.hip", "seq_dropout.o", []))
     u.append(("hip", "seq/seq_delta_token.hip", "seq_delta_token.o", []))
+    u.append(("hip", "seq/seq_delta_prep.hip", "seq_delta_prep.o", []))
+    u.append(("hip", "seq/seq_delta_scan.hip", "seq_delta_scan.o",
+              ["-mllvm", "-amdgpu-mfma-vgpr-form"]))
+    u.append(("hip", "seq/seq_delta_grad.hip", "seq_delta_grad.o",
+              ["-mllvm", "-amdgpu-mfma-vgpr-form"]))
     u.append(("hip", "seq/seq_api.cpp", "seq_api.o", ["-x", "hip"]))
     u.append(("hip", "dwc_api.cpp", "dwc_api.o", ["-x", "hip"]))
     u.append(("cxx", "dwc_plan.cpp", "dwc_plan.o", []))

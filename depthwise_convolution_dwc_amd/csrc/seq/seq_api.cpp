@@ -6,6 +6,7 @@
 #include <string>
 
 #include "../dwc_plan.h"
+#include "seq_chunk.h"
 #include "seq_delta.h"
 #include "seq_launch.h"
 
@@ -186,6 +187,39 @@ DeltaArgs delta_args(const dwc_delta_problem* p, const void* q, const void* k, c
   return a;
 }
 
+// The chunked kernels' workspace, laid out from base (null: sizes only).
+size_t delta_layout(const dwc_delta_problem* p, bool bwd, char* base, ChunkArgs* c) {
+  const int64_t np = p->dtype == DWC_F32 ? 2 : 1, op = p->dtype == DWC_BF16 ? 1 : 2;
+  const int64_t dp = p->dk <= 64 ? 64 : 128;
+  c->nc = (int)((p->l + kChunk - 1) / kChunk);
+  c->dvp = (p->dv + 15) / 16 * 16;
+  const int64_t nk = p->b * c->nc * p->hk, nv = p->b * c->nc * p->hv;
+  const int64_t frags = nk * np * (dp / 8) * 64, tri = nv * kTri * 64;
+  size_t at = 0;
+  const auto take = [&](auto** field, int64_t bytes) {
+    *field = reinterpret_cast<std::remove_reference_t<decltype(*field)>>(base + at);
+    at += ((size_t)bytes + 255) & ~(size_t)255;
+  };
+  take(&c->ka, frags * 16);
+  take(&c->kt, frags * 16);
+  take(&c->xa, tri * 2 * 16);
+  take(&c->kq_inv, nk * 8);
+  take(&c->gate, nv * (int64_t)sizeof(Gate));
+  if (!bwd) {
+    take(&c->qa, frags * 16);
+    take(&c->pa, tri * op * 16);
+  } else {
+    take(&c->qt, frags * 16);
+    take(&c->xt, tri * 2 * 16);
+    take(&c->pt, tri * 2 * 16);
+    take(&c->states, nv * dp * c->dvp * 4);
+    take(&c->dstates, nv * dp * c->dvp * 4);
+    take(&c->e, nv * kChunk * c->dvp * 4);
+    take(&c->dw, nv * kChunk * c->dvp * 4);
+  }
+  return at;
+}
+
 }  // namespace
 
 extern "C" {
@@ -326,17 +360,41 @@ int dwc_delta_workspace_size(const dwc_delta_problem* p, int op, size_t* bytes) 
   if (op != DWC_DELTA_FWD && op != DWC_DELTA_BWD)
     return fail(DWC_ERR_BAD_PARAM, "op must be DWC_DELTA_FWD or DWC_DELTA_BWD");
   if (!bytes) return fail(DWC_ERR_BAD_PARAM, "bytes pointer is NULL");
-  *bytes = 0;
+  ChunkArgs c{};
+  *bytes = p->b > 0 && p->l > 0 ? delta_layout(p, op == DWC_DELTA_BWD, nullptr, &c) : 0;
   return DWC_OK;
 }
 
 int dwc_delta_fwd(const dwc_delta_problem* p, const void* q, const void* k, const void* v,
                   const float* g, const float* beta, const float* s0, const int32_t* lengths,
                   void* o, float* s1, void* workspace, size_t workspace_bytes, void* stream) {
-  int st = check_delta(p, 128);
+  size_t need = 0;
+  int st = dwc_delta_workspace_size(p, DWC_DELTA_FWD, &need);
   if (st != DWC_OK) return st;
-  if (s1 && s1 == s0) return fail(DWC_ERR_ALIAS, "output overlaps an input");
-  return dwc_delta_step(p, q, k, v, g, beta, s0, lengths, o, s1, stream);
+  DeltaSpans n{};
+  st = delta_spans(p, false, &n);
+  if (st != DWC_OK) return st;
+  if (p->b == 0) return DWC_OK;
+  if (!s1 || (p->l > 0 && (!q || !k || !v || !g || !beta || !o)))
+    return fail(DWC_ERR_BAD_PARAM, "a tensor's pointer is NULL");
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(DWC_ERR_WORKSPACE, "workspace missing or smaller than required");
+  const int64_t e = bytes_of(p->dtype);
+  const Span in[] = {{q, n.q, e},       {k, n.k, e},  {v, n.v, e}, {g, n.g, 4},
+                     {beta, n.beta, 4}, {s0, n.s, 4}, {lengths, lengths ? p->b * 4 : 0, 4}};
+  const Span out[] = {{o, n.o, e}, {s1, n.s, 4}, {workspace, (int64_t)need, 256}};
+  st = check_spans(in, out);
+  if (st != DWC_OK) return st;
+  ChunkArgs c{};
+  c.a = delta_args(p, q, k, v, g, beta, s0, lengths);
+  c.a.o = o;
+  c.a.s1 = s1;
+  const hipStream_t hs = (hipStream_t)stream;
+  if (p->l == 0) return hip_result(launch_delta_token(c.a, hs), "dwc_delta_fwd launch");
+  delta_layout(p, false, (char*)workspace, &c);
+  hipError_t err = launch_delta_prep(c, false, hs);
+  if (err == hipSuccess) err = launch_delta_scan(c, false, hs);
+  return hip_result(err, "dwc_delta_fwd launch");
 }
 
 int dwc_delta_bwd(const dwc_delta_problem* p, const void* dout, const float* ds1, const void* q,
@@ -344,7 +402,51 @@ int dwc_delta_bwd(const dwc_delta_problem* p, const void* dout, const float* ds1
                   const float* s0, const int32_t* lengths, void* dq, void* dk_out, void* dv_out,
                   float* dg, float* dbeta, float* ds0, void* workspace, size_t workspace_bytes,
                   void* stream) {
-  return fail(DWC_ERR_UNSUPPORTED, "the delta rule's gradient is not built");
+  size_t need = 0;
+  int st = dwc_delta_workspace_size(p, DWC_DELTA_BWD, &need);
+  if (st != DWC_OK) return st;
+  DeltaSpans n{};
+  st = delta_spans(p, true, &n);
+  if (st != DWC_OK) return st;
+  if (p->b == 0) return DWC_OK;
+  if (p->l > 0 && (!dout || !q || !k || !v || !g || !beta || !dq || !dk_out || !dv_out || !dg ||
+                   !dbeta))
+    return fail(DWC_ERR_BAD_PARAM, "a tensor's pointer is NULL");
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(DWC_ERR_WORKSPACE, "workspace missing or smaller than required");
+  const int64_t e = bytes_of(p->dtype);
+  const Span in[] = {{q, n.q, e},       {k, n.k, e},
+                     {v, n.v, e},       {g, n.g, 4},
+                     {beta, n.beta, 4}, {s0, n.s, 4},
+                     {dout, n.dout, e}, {ds1, n.s, 4},
+                     {lengths, lengths ? p->b * 4 : 0, 4}};
+  const Span out[] = {{dq, n.qk_dense, e}, {dk_out, n.qk_dense, e}, {dv_out, n.o, e},
+                      {dg, n.heads, 4},    {dbeta, n.heads, 4},     {ds0, n.s, 4},
+                      {workspace, (int64_t)need, 256}};
+  st = check_spans(in, out);
+  if (st != DWC_OK) return st;
+  ChunkArgs c{};
+  c.a = delta_args(p, q, k, v, g, beta, s0, lengths);
+  c.a.dout = dout;
+  c.a.ds1 = ds1;
+  c.a.dq = dq;
+  c.a.dk_out = dk_out;
+  c.a.dv_out = dv_out;
+  c.a.dg = dg;
+  c.a.dbeta = dbeta;
+  c.a.ds0 = ds0;
+  const hipStream_t hs = (hipStream_t)stream;
+  hipError_t err = hipSuccess;
+  delta_layout(p, true, (char*)workspace, &c);
+  if (p->l == 0) {  // the state passes through, and its gradient
+    if (ds0) err = launch_delta_scan_bwd(c, hs);
+    return hip_result(err, "dwc_delta_bwd launch");
+  }
+  err = launch_delta_prep(c, true, hs);
+  if (err == hipSuccess) err = launch_delta_scan(c, true, hs);
+  if (err == hipSuccess) err = launch_delta_scan_bwd(c, hs);
+  if (err == hipSuccess) err = launch_delta_grad(c, hs);
+  return hip_result(err, "dwc_delta_bwd launch");
 }
 
 }  // extern "C"

@@ -1,0 +1,468 @@
+// seq_delta_grad.hip -- the gradients of q, k, g and beta in each chunk of
+// the gated delta rule, from the states around it, E and W = dL/dU (see
+// seq_chunk.h and seq_delta_scan.hip).  With S the state before the chunk,
+// dS the gradient of the state after it, dV = beta o W:
+//   Ph = scale D o (dO U^T) (lower),  B = -D o (dV U^T) (strictly lower)
+//   dQ = scale exp(G) o (dO S^T) + Ph K
+//   dK = -exp(G) o (dV S^T) + exp(G_64 - G) o (U dS^T) + Ph^T Q + (B + B^T) K
+//   dbeta_t = E_t . W_t
+// and, since S_t exp(-G_t) depends on g through v exp(-G) and o exp(G) alone,
+//   dG_t = q_t . dq_t - v_t . dv_t  for each token,
+//   dg_t = sum of dG_s over s >= t in the chunk + <dS, S after the chunk>,
+//   <dS, S after> = exp(G_64) <dS, S> + sum_t k_t . (exp(G_64 - G) o U dS^T)_t.
+//
+// One workgroup of DP / 16 waves a (sequence, chunk, key head), the value
+// heads that share the key head one after another, dv in blocks of 64
+// columns.  A wave owns 16 key dimensions of dQ and dK, so the states go from
+// memory to exactly one wave's registers; the operands that all waves share
+// lie in LDS.
+#include "seq_chunk.h"
+
+namespace dwc {
+namespace seq {
+namespace grad {
+
+constexpr int kPitch = 72;             // halves a row: 144 bytes, 16-byte aligned
+constexpr int kTile = kChunk * kPitch;  // halves a 64x64 tile
+
+// 8 consecutive halves at column 32 ks + 8 q.
+__device__ __forceinline__ half8 frag8(const _Float16* tile, int row, int ks, int q) {
+  return *(const half8*)(tile + row * kPitch + 32 * ks + 8 * q);
+}
+
+// 8 halves in the order of the packed K and Q fragments.
+__device__ __forceinline__ half8 frag44(const _Float16* tile, int row, int ks, int q) {
+  const half4 u = *(const half4*)(tile + row * kPitch + 32 * ks + 4 * q);
+  const half4 v = *(const half4*)(tile + row * kPitch + 32 * ks + 16 + 4 * q);
+  return half8{u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
+}
+
+__device__ __forceinline__ float wave_max(float m) {
+#pragma unroll
+  for (int i = 1; i < 64; i <<= 1) m = fmaxf(m, __shfl_xor(m, i, 64));
+  return m;
+}
+
+// Pieces of N consecutive values to a row of a tile.
+template <int P, int N>
+__device__ __forceinline__ void put(_Float16* tile, int row, int col, const float* v, float s) {
+#pragma unroll
+  for (int i = 0; i < N; i += 8) {
+    half8 hi, lo;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      _Float16 h, l;
+      split(v[i + j] * s, &h, &l);
+      hi[j] = h;
+      lo[j] = l;
+    }
+    *(half8*)(tile + row * kPitch + col + i) = hi;
+    if constexpr (P == 2) *(half8*)(tile + kTile + row * kPitch + col + i) = lo;
+  }
+}
+
+// LDS tiles: dO, dV, U per block of dv, then Ph, Ph^T, B + B^T, two pieces
+// each.
+constexpr int kLds = 6 * kTile * 2;
+
+template <int V>
+struct Int {
+  static constexpr int value = V;
+};
+
+template <int T, int DP>
+__global__ void __launch_bounds__(DP * 4) delta_grad(ChunkArgs c) {
+  constexpr int NP = T == T_F32 ? 2 : 1;  // pieces of an input
+  // pieces of what only dk (or only the rounded part of dq) sums: a bf16
+  // output needs one, 2^-12 against its own 2^-9
+  constexpr int OP = T == T_BF16 ? 1 : 2;
+  constexpr int NW = DP / 16;   // waves
+  constexpr int CPT = 64 / NW;  // columns of a 64-wide tile a thread loads
+  extern __shared__ __align__(16) char lds_raw[];
+  __shared__ float red[4][NW];
+  __shared__ float sdot[NW][kChunk], sbeta[kChunk], svdv[kChunk];
+  __shared__ double sg[kChunk];
+  _Float16* lds = (_Float16*)lds_raw;
+  _Float16 *tdo = lds, *tdv = lds + 2 * kTile, *tu = lds + 4 * kTile;
+  _Float16 *tph = lds, *tpt = lds + 2 * kTile, *tb = lds + 4 * kTile;
+  const DeltaArgs& a = c.a;
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, m0 = lane & 15, q0 = lane >> 4;
+  const int row0 = tid / NW, part0 = tid % NW;  // for whole-tile loads
+  const int64_t id = blockIdx.x;
+  const int hk = (int)(id % a.hk);
+  const int64_t bc = id / a.hk;
+  const int chunk = (int)(bc % c.nc);
+  const int64_t b = bc / c.nc;
+  const int64_t len = live_tokens(a, b), t0 = (int64_t)chunk * kChunk;
+  const int n = (int)(len - t0 < 0 ? 0 : (len - t0 < kChunk ? len - t0 : kChunk));
+  const int per = a.hv / a.hk;
+  f32x4 dq[4], dk[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) dq[i] = dk[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const float kinv = n ? c.kq_inv[2 * id] : 0.f, qinv = n ? c.kq_inv[2 * id + 1] : 0.f;
+  // this wave's key dimension: 16 w + lane % 16
+  const Frag* kt = c.kt + (id * NP * (DP / 16 * 2) + w * 2) * 64 + lane;
+  const Frag* qt = c.qt + (id * NP * (DP / 16 * 2) + w * 2) * 64 + lane;
+  constexpr int PIECE = DP / 16 * 2 * 64;
+
+  for (int r = 0; r < per; ++r) {
+    const int h = hk * per + r;
+    const int64_t hid = bc * a.hv + h;
+    // opaque copies, so that addresses made of them are made again for each
+    // head instead of held through the loop (they would not fit)
+    int m = m0, q = q0, row = row0, part = part0;
+    asm volatile("" : "+v"(m), "+v"(q), "+v"(row), "+v"(part));
+    if (n == 0) {  // past the sequence: zeros
+      if (tid < kChunk && t0 + tid < a.l) {
+        a.dg[(b * a.l + t0 + tid) * a.hv + h] = 0.f;
+        a.dbeta[(b * a.l + t0 + tid) * a.hv + h] = 0.f;
+      }
+      continue;
+    }
+    const Gate* gate = c.gate + hid;
+    const float beta = gate->beta[row];
+    float ew = 0.f, vdv = 0.f, sds = 0.f, kdk = 0.f;
+    // rows 16 wr.., columns 16 j.. of dO U^T and dV U^T: with 8 waves four
+    // of them take the one and four the other, with 4 waves each takes both
+    constexpr int BOTH = NW == 4 ? 2 : 1;
+    const int wr = w & 3;
+    f32x4 dp[BOTH][4];
+    float qdot[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int x = 0; x < BOTH; ++x) dp[x][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) qdot[i][x] = 0.f;
+    }
+    for (int v0 = 0; v0 < c.dvp; v0 += 64) {
+      __syncthreads();  // the tiles' readers are done
+      asm volatile("" : "+v"(m), "+v"(q), "+v"(row), "+v"(part));
+      float xd[CPT], xv[CPT], xu[CPT];
+      float md = 0.f, mv = 0.f, mu = 0.f;
+      {
+        const int col = v0 + CPT * part;
+        const int64_t t = t0 + row;
+        const float* ep = c.e + (hid * kChunk + row) * c.dvp + col;
+        const float* wp = c.dw + (hid * kChunk + row) * c.dvp + col;
+        const int64_t vb = b * a.v_stride[0] + t * a.v_stride[1] + h * a.v_stride[2] + col;
+        const int64_t ob = b * a.do_stride[0] + t * a.do_stride[1] + h * a.do_stride[2] + col;
+#pragma unroll
+        for (int i = 0; i < CPT; i += 4) {
+          f32x4 ee = {0.f, 0.f, 0.f, 0.f}, ww = ee;
+          if (col < c.dvp) {
+            ee = *(const f32x4*)(ep + i);
+            ww = *(const f32x4*)(wp + i);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const bool in = row < n && col + i + j < a.dv;
+            xd[i + j] = in ? load1<T>(a.dout, ob + i + j) : 0.f;
+            const float v = in ? load1<T>(a.v, vb + i + j) : 0.f;
+            xv[i + j] = beta * ww[j];
+            xu[i + j] = beta * ee[j];
+            ew = fmaf(ee[j], ww[j], ew);
+            vdv = fmaf(v, xv[i + j], vdv);
+            md = fmaxf(md, fabsf(xd[i + j]));
+            mv = fmaxf(mv, fabsf(xv[i + j]));
+            mu = fmaxf(mu, fabsf(xu[i + j]));
+          }
+        }
+      }
+      md = wave_max(md);
+      mv = wave_max(mv);
+      mu = wave_max(mu);
+      if (lane == 0) {
+        red[0][w] = md;
+        red[1][w] = mv;
+        red[2][w] = mu;
+      }
+      __syncthreads();
+      md = mv = mu = 0.f;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        md = fmaxf(md, red[0][i]);
+        mv = fmaxf(mv, red[1][i]);
+        mu = fmaxf(mu, red[2][i]);
+      }
+      const Scale sd = scale_of(md), sv = scale_of(mv), su = scale_of(mu);
+      put<NP, CPT>(tdo, row, CPT * part, xd, sd.mul);
+      put<2, CPT>(tdv, row, CPT * part, xv, sv.mul);
+      put<2, CPT>(tu, row, CPT * part, xu, su.mul);
+      __syncthreads();
+      // dO U^T and dV U^T
+      const auto lower = [&](auto pieces, const _Float16* tile, float inv, f32x4(&acc)[4]) {
+        constexpr int P = decltype(pieces)::value;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j > wr) break;
+          __builtin_amdgcn_sched_barrier(0);
+          f32x4 p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) {
+            half8 f[P], fu[2];
+#pragma unroll
+            for (int y = 0; y < P; ++y) f[y] = frag8(tile + y * kTile, 16 * wr + m, ks, q);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) fu[y] = frag8(tu + y * kTile, 16 * j + m, ks, q);
+            p = mfma_pieces<P, 2>(f, fu, p);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[j][i] = fmaf(inv, p[i], acc[j][i]);
+        }
+      };
+      if (BOTH == 2 || w < 4) lower(Int<NP>{}, tdo, sd.inv * su.inv, dp[0]);
+      if (BOTH == 2 || w >= 4) lower(Int<2>{}, tdv, sv.inv * su.inv, dp[BOTH - 1]);
+      // dO S^T, dV S^T and U dS^T
+      asm volatile("" : "+v"(m), "+v"(q), "+v"(row), "+v"(part));
+      {
+        const int64_t at = (hid * DP + 16 * w + m) * c.dvp + v0 + 8 * q;
+        f32x4 s[4], g[4];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const bool in = v0 + 32 * ks + 8 * q < c.dvp;
+            s[2 * ks + x] = in ? *(const f32x4*)(c.states + at + 32 * ks + 4 * x)
+                               : f32x4{0.f, 0.f, 0.f, 0.f};
+            g[2 * ks + x] = in ? *(const f32x4*)(c.dstates + at + 32 * ks + 4 * x)
+                               : f32x4{0.f, 0.f, 0.f, 0.f};
+          }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) sds = fmaf(s[i][x], g[i][x], sds);
+        const Scale ss = scale_of(column_max(abs_max(s)));
+        const Scale sgr = scale_of(column_max(abs_max(g)));
+        half8 fs[2][2], fg[2][2];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          to_frag<2>(s[2 * ks], s[2 * ks + 1], ss.mul, fs[ks]);
+          to_frag<2>(g[2 * ks], g[2 * ks + 1], sgr.mul, fg[ks]);
+        }
+        half8 fq[2][NP], fk[2][NP];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+          for (int y = 0; y < NP; ++y) {
+            fq[ks][y] = qt[y * PIECE + ks * 64];
+            fk[ks][y] = kt[y * PIECE + ks * 64];
+          }
+        const float cq = a.scale * sd.inv * ss.inv, ck = -sv.inv * ss.inv,
+                    cu = su.inv * sgr.inv;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // loads of later rows are not pulled ahead of this one's products:
+          // all at once they would not fit the registers
+          __builtin_amdgcn_sched_barrier(0);
+          f32x4 xq = {0.f, 0.f, 0.f, 0.f}, xk = xq, xs = xq;
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) {
+            half8 fo[NP], fv[2], fu[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              if (y < NP) fo[y] = frag8(tdo + y * kTile, 16 * i + m, ks, q);
+              if (y < OP) fv[y] = frag8(tdv + y * kTile, 16 * i + m, ks, q);
+              fu[y] = frag8(tu + y * kTile, 16 * i + m, ks, q);
+            }
+            xq = mfma_pieces<NP, 2>(fo, fs[ks], xq);
+            xk = mfma_pieces<OP, OP>(fv, fs[ks], xk);
+            xs = mfma_pieces<2, 2>(fu, fg[ks], xs);
+          }
+          const f32x4 into = *(const f32x4*)(gate->into + 16 * i + 4 * q);
+          const f32x4 out = *(const f32x4*)(gate->out + 16 * i + 4 * q);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            // q and k at this result's place, from their fragments
+            const int slot = (i & 1) * 4 + x;
+            float qv = (float)fq[i >> 1][0][slot], kv = (float)fk[i >> 1][0][slot];
+            if constexpr (NP == 2) {
+              qv += (float)fq[i >> 1][1][slot];
+              kv += (float)fk[i >> 1][1][slot];
+            }
+            const float u = cq * into[x] * xq[x], v = cu * out[x] * xs[x];
+            qdot[i][x] = fmaf(qv * qinv, u, qdot[i][x]);
+            kdk = fmaf(kv * kinv, v, kdk);
+            dq[i][x] += u;
+            dk[i][x] += fmaf(ck * into[x], xk[x], v);
+          }
+        }
+      }
+    }
+    // Ph, Ph^T and B + B^T to LDS
+    asm volatile("" : "+v"(m), "+v"(q), "+v"(row), "+v"(part));
+    if (tid < kChunk) sg[tid] = gate->g[tid];
+    __syncthreads();
+    float mx[2] = {0.f, 0.f};
+#pragma unroll
+    for (int x = 0; x < BOTH; ++x) {
+      const bool ph = BOTH == 2 ? x == 0 : w < 4;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = 16 * wr + 4 * q + i, cc = 16 * j + m;
+          const float d = cc <= rr ? expf((float)(sg[rr] - sg[cc])) : 0.f;
+          const float v = ph ? a.scale * d * dp[x][j][i] : -d * dp[x][j][i];
+          dp[x][j][i] = cc < rr || (ph && cc == rr) ? v : 0.f;
+          mx[x] = fmaxf(mx[x], fabsf(dp[x][j][i]));
+        }
+    }
+    if (BOTH == 1 && w >= 4) {
+      mx[1] = mx[0];
+      mx[0] = 0.f;
+    }
+    mx[0] = wave_max(mx[0]);
+    mx[1] = wave_max(mx[1]);
+    if (lane == 0) {
+      red[0][w] = mx[0];
+      red[1][w] = mx[1];
+    }
+    __syncthreads();
+    mx[0] = mx[1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      mx[0] = fmaxf(mx[0], red[0][i]);
+      mx[1] = fmaxf(mx[1], red[1][i]);
+    }
+    const Scale sp = scale_of(mx[0]), sb = scale_of(mx[1]);
+#pragma unroll
+    for (int y = 0; y < BOTH; ++y) {
+      const bool ph = BOTH == 2 ? y == 0 : w < 4;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = 16 * wr + 4 * q + i, cc = 16 * j + m;
+          _Float16 hi, lo;
+          split(dp[y][j][i] * (ph ? sp.mul : sb.mul), &hi, &lo);
+          if (ph) {
+            tph[rr * kPitch + cc] = hi;
+            tph[kTile + rr * kPitch + cc] = lo;
+            tpt[cc * kPitch + rr] = hi;
+            if constexpr (OP == 2) tpt[kTile + cc * kPitch + rr] = lo;
+          } else if (cc <= rr) {
+            tb[rr * kPitch + cc] = hi;
+            tb[cc * kPitch + rr] = hi;
+            if constexpr (OP == 2) {
+              tb[kTile + rr * kPitch + cc] = lo;
+              tb[kTile + cc * kPitch + rr] = lo;
+            }
+          }
+        }
+      }
+    }
+    __syncthreads();
+    asm volatile("" : "+v"(m), "+v"(q), "+v"(row), "+v"(part));
+    {
+      half8 fq[2][NP], fk[2][NP];
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int y = 0; y < NP; ++y) {
+          fq[ks][y] = qt[y * PIECE + ks * 64];
+          fk[ks][y] = kt[y * PIECE + ks * 64];
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
+        f32x4 xq = {0.f, 0.f, 0.f, 0.f}, xp = xq, xb = xq;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          if (ks == 0 || i >= 2) {
+            const half8 f[2] = {frag44(tph, 16 * i + m, ks, q),
+                                frag44(tph + kTile, 16 * i + m, ks, q)};
+            xq = mfma_pieces<2, NP>(f, fk[ks], xq);
+          }
+          half8 f[OP], g[OP];
+#pragma unroll
+          for (int y = 0; y < OP; ++y) {
+            f[y] = frag44(tpt + y * kTile, 16 * i + m, ks, q);
+            g[y] = frag44(tb + y * kTile, 16 * i + m, ks, q);
+          }
+          if (ks == 1 || i < 2) xp = mfma_pieces<OP, NP>(f, fq[ks], xp);
+          xb = mfma_pieces<OP, NP>(g, fk[ks], xb);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int slot = (i & 1) * 4 + x;
+          float qv = (float)fq[i >> 1][0][slot];
+          if constexpr (NP == 2) qv += (float)fq[i >> 1][1][slot];
+          const float u = sp.inv * kinv * xq[x];
+          qdot[i][x] = fmaf(qv * qinv, u, qdot[i][x]);
+          dq[i][x] += u;
+          dk[i][x] += fmaf(sp.inv * qinv, xp[x], sb.inv * kinv * xb[x]);
+        }
+      }
+    }
+    // dbeta and dg
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float d = lane_sum<16>(qdot[i][x]);
+        if (m == 0) sdot[w][16 * i + 4 * q + x] = d;
+      }
+    ew = lane_sum<NW>(ew);
+    vdv = lane_sum<NW>(vdv);
+    if (part == 0) {
+      sbeta[row] = ew;
+      svdv[row] = vdv;
+    }
+    sds = lane_sum<64>(sds);
+    kdk = lane_sum<64>(kdk);
+    if (lane == 0) {
+      red[2][w] = sds;
+      red[3][w] = kdk;
+    }
+    __syncthreads();
+    if (w == 0) {
+      float d = -svdv[lane], far = 0.f, ends = 0.f;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        d += sdot[i][lane];
+        far += red[2][i];
+        ends += red[3][i];
+      }
+#pragma unroll
+      for (int i = 1; i < 64; i <<= 1) {
+        const float o = __shfl_down(d, i, 64);
+        if (lane + i < 64) d += o;
+      }
+      d += gate->total * far + ends;
+      if (t0 + lane < a.l) {
+        a.dg[(b * a.l + t0 + lane) * a.hv + h] = lane < n ? d : 0.f;
+        a.dbeta[(b * a.l + t0 + lane) * a.hv + h] = lane < n ? sbeta[lane] : 0.f;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const int t = 16 * i + 4 * q0 + x, col = 16 * w + m0;
+        if (t0 + t >= a.l || col >= a.dk) continue;
+        const int64_t at = ((b * a.l + t0 + t) * a.hk + hk) * a.dk + col;
+        store1<T>(a.dq, at, t < n ? dq[i][x] : 0.f);
+        store1<T>(a.dk_out, at, t < n ? dk[i][x] : 0.f);
+      }
+}
+
+template <int T>
+void go(const ChunkArgs& c, hipStream_t st) {
+  const dim3 grid((uint32_t)(c.a.b * c.nc * c.a.hk));
+  if (c.a.dk <= 64) hipLaunchKernelGGL((delta_grad<T, 64>), grid, dim3(256), kLds, st, c);
+  else hipLaunchKernelGGL((delta_grad<T, 128>), grid, dim3(512), kLds, st, c);
+}
+
+}  // namespace grad
+
+hipError_t launch_delta_grad(const ChunkArgs& c, hipStream_t st) {
+  if (c.a.type == T_F32) grad::go<T_F32>(c, st);
+  else if (c.a.type == T_BF16) grad::go<T_BF16>(c, st);
+  else grad::go<T_F16>(c, st);
+  return hipGetLastError();
+}
+
+}  // namespace seq
+}  // namespace dwc

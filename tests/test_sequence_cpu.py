@@ -164,3 +164,37 @@ def test_tensor_calls_refuse_host_tensors_and_wrong_types():
     q = torch.zeros(1, 2, 1, 4)
     with pytest.raises(ValueError):
         dwc.delta_rule(q, q, q, q[..., 0], q[..., 0])
+
+
+def test_delta_chunked_pointers_refused():
+    p, need = delta(), ctypes.c_size_t()
+    lib = dwc.lib()
+    for op in (0, 1):
+        assert lib.dwc_delta_workspace_size(ctypes.byref(p), op, ctypes.byref(need)) == 0
+        assert need.value > 0
+        names = (["q", "k", "v", "g", "beta", "s0", "lengths", "o", "s1"] if op == 0 else
+                 ["dout", "ds1", "q", "k", "v", "g", "beta", "s0", "lengths", "dq", "dk", "dv",
+                  "dg", "dbeta", "ds0"])
+        f = lib.dwc_delta_fwd if op == 0 else lib.dwc_delta_bwd
+
+        def call(p=p, ws=at(40), n=need.value, **ch):
+            a = {name: at(i) for i, name in enumerate(names)}
+            a["lengths"] = None
+            a.update(ch)
+            return f(ctypes.byref(p) if p else None, *a.values(), ws, n, None)
+
+        assert call(p=None) == BAD
+        assert call(n=need.value - 1) == WORKSPACE and call(ws=None) == WORKSPACE
+        assert call(ws=at(40, 64)) == MISALIGNED
+        for name in names:
+            if name not in ("lengths", "s0", "ds1", "ds0"):
+                assert call(**{name: None}) == BAD, name
+            if name != "lengths":
+                assert call(**{name: at(30, 1)}) == MISALIGNED, name
+        out = names[7] if op == 0 else "dq"
+        assert call(**{out: at(names.index("v"))}) == ALIAS
+        assert call(ws=at(names.index("q"))) == ALIAS
+        if op == 0:
+            assert call(s1=at(names.index("s0"))) == ALIAS
+        assert call(p=delta(q=(-4, 1, 1))) == BAD
+        assert call(p=delta(b=0)) == 0
