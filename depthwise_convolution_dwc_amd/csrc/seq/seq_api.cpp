@@ -203,7 +203,6 @@ size_t delta_layout(const dwc_delta_problem* p, bool bwd, char* base, ChunkArgs*
   take(&c->ka, frags * 16);
   take(&c->kt, frags * 16);
   take(&c->xa, tri * 2 * 16);
-  take(&c->kq_inv, nk * 8);
   take(&c->gate, nv * (int64_t)sizeof(Gate));
   if (!bwd) {
     take(&c->qa, frags * 16);

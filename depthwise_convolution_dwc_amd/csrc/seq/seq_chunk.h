@@ -40,8 +40,9 @@ struct Gate {
   float out[kChunk];   // exp(G_64 - G_t)
   float beta[kChunk];
   float total;         // exp(G_64)
-  float xinv, pinv;    // the values of X and P times these are the true ones
-  float pad;
+  // the packed values of X, P, K and Q times these are the true ones
+  float xinv, pinv, kinv, qinv;
+  float pad[3];
   double g[kChunk];    // G_t
 };
 
@@ -68,7 +69,6 @@ struct ChunkArgs {
   int dvp;       // dv rounded up to 16
   Frag *ka, *qa, *kt, *qt;   // per (b, chunk, hk): [piece][block][64]
   Frag *xa, *pa, *xt, *pt;   // per (b, chunk, hv): [piece][kTri][64]
-  float* kq_inv;             // per (b, chunk, hk): 2
   Gate* gate;                // per (b, chunk, hv)
   float *states, *dstates;   // per (b, chunk, hv): dp x dvp, before the chunk / after it
   float *e, *dw;             // per (b, chunk, hv): 64 x dvp
@@ -103,10 +103,18 @@ __device__ __forceinline__ void split(float v, _Float16* hi, _Float16* lo) {
   *lo = (_Float16)(v - (float)*hi);
 }
 
-// Largest magnitude over the lanes that share a column (lane % 16).
+// Largest magnitude over the lanes that share a column (lane % 16).  The
+// swap exchanges the odd halves (then rows of 16 lanes) of its first register
+// with the even ones of its second: of a register and its copy, one is left
+// with either half's values in all lanes, so a maximum joins them.  (The
+// compiler's builtin returns its first result twice.)
 __device__ __forceinline__ float column_max(float m) {
-  m = fmaxf(m, __shfl_xor(m, 16, 64));
-  return fmaxf(m, __shfl_xor(m, 32, 64));
+  float o = m;
+  asm("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(m), "+v"(o));
+  m = fmaxf(m, o);
+  o = m;
+  asm("s_nop 1\n\tv_permlane16_swap_b32 %0, %1" : "+v"(m), "+v"(o));
+  return fmaxf(m, o);
 }
 
 // acc += A B from pieces: PA of A, PB of B, the products that matter.

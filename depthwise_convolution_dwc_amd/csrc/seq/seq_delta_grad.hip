@@ -99,7 +99,6 @@ __global__ void __launch_bounds__(DP * 4) delta_grad(ChunkArgs c) {
   f32x4 dq[4], dk[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) dq[i] = dk[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const float kinv = n ? c.kq_inv[2 * id] : 0.f, qinv = n ? c.kq_inv[2 * id + 1] : 0.f;
   // this wave's key dimension: 16 w + lane % 16
   const Frag* kt = c.kt + (id * NP * (DP / 16 * 2) + w * 2) * 64 + lane;
   const Frag* qt = c.qt + (id * NP * (DP / 16 * 2) + w * 2) * 64 + lane;
@@ -120,7 +119,7 @@ __global__ void __launch_bounds__(DP * 4) delta_grad(ChunkArgs c) {
       continue;
     }
     const Gate* gate = c.gate + hid;
-    const float beta = gate->beta[row];
+    const float beta = gate->beta[row], kinv = gate->kinv, qinv = gate->qinv;
     float ew = 0.f, vdv = 0.f, sds = 0.f, kdk = 0.f;
     // rows 16 wr.., columns 16 j.. of dO U^T and dV U^T: with 8 waves four
     // of them take the one and four the other, with 4 waves each takes both

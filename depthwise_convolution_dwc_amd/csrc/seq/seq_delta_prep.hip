@@ -135,11 +135,6 @@ __global__ void __launch_bounds__(256) delta_prep(ChunkArgs c) {
     }
     __syncthreads();
   }
-  if (tid == 0) {
-    c.kq_inv[2 * id] = kinv;
-    c.kq_inv[2 * id + 1] = qinv;
-  }
-
   // fragments of K and Q (rows are tokens), and this wave's rows of K K^T
   // and Q K^T
   f32x4 kk[4], qk[4];
@@ -239,7 +234,6 @@ __global__ void __launch_bounds__(256) delta_prep(ChunkArgs c) {
     __syncthreads();
     // X = N - N beta X, 16 rows at a time: what the rows above give, by all
     // waves (a lane a column), then the 16 rows among themselves
-    const float bl = sbeta[lane];
     for (int i = 0; i < 4; ++i) {
       float acc[4];
 #pragma unroll
@@ -266,7 +260,6 @@ __global__ void __launch_bounds__(256) delta_prep(ChunkArgs c) {
       }
       __syncthreads();
     }
-    (void)bl;
     float xmax = 0.f;
 #pragma unroll
     for (int t = 0; t < 16; ++t) xmax = fmaxf(xmax, fabsf(tx[(16 * w + t) * kPitch + lane]));
@@ -279,6 +272,8 @@ __global__ void __launch_bounds__(256) delta_prep(ChunkArgs c) {
     if (tid == 0) {
       gate->xinv = xs.inv;
       gate->pinv = ps.inv;
+      gate->kinv = kinv;
+      gate->qinv = qinv;
     }
     write_tri<2, false>(tx, xs.mul, c.xa + hid * 2 * kTri * 64);
     if constexpr (BWD) {

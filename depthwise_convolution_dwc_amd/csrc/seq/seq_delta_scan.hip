@@ -1,12 +1,20 @@
 // seq_delta_scan.hip -- the serial part of the chunked gated delta rule, and
 // of its gradient (formulas in seq_chunk.h).
 //
-// A column of the state depends on no other, so a wave owns 16 columns for
-// the whole sequence and holds them in fp32 as 16x16 results of the matrix
-// cores (MT tiles of 4 registers).  Every product of the recurrence has the
-// state or something made of it on the right and a shared fragment on the
-// left, and each result is the next operand without leaving its lane: waves
-// share nothing and never wait for each other.
+// A column of the state depends on no other, so a workgroup owns 16 NT
+// columns of one head for the whole sequence.  Its two waves share them by
+// rows: each holds half of the state (fp32, as 16x16 results of the matrix
+// cores) and makes the results of half of a chunk's tokens.  Every product
+// has the state, or something made of it, on the right; its rows are 32-row
+// blocks that one wave owns whole, so a block's scale needs no other wave,
+// and the blocks go through LDS (three exchanges a chunk).  The fragments on
+// the left are each wave's own: they go from memory to registers, each
+// refilled for the next chunk as soon as this chunk is done with it, so that
+// no exchange waits for memory.
+//
+// Bound: the chain of products and exchanges of a chunk, about 3000 cycles,
+// times the chunks of the longest sequence.
+#include "../dwc_device.h"
 #include "seq_chunk.h"
 
 namespace dwc {
@@ -18,204 +26,351 @@ __device__ __forceinline__ f32x4 row4(const float* p, int i, int q) {
   return *(const f32x4*)(p + 16 * i + 4 * q);
 }
 
-// The wave's part in one (sequence, value head) and its 16 columns.
-struct Place {
-  int64_t b, head;
-  int h, hk, col, groups;
-  bool ok, any;
+// LDS written before is visible to both waves after; loads from memory stay
+// in flight (__syncthreads may wait for them).
+__device__ __forceinline__ void exchange() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+template <int T>
+struct Raw {
+  typedef uint16_t type;
+  static __device__ __forceinline__ float value(uint16_t x) { return from16<T>(x); }
+};
+template <>
+struct Raw<T_F32> {
+  typedef float type;
+  static __device__ __forceinline__ float value(float x) { return x; }
 };
 
+// This wave's rows of a chunk's gates.
+struct Gates {
+  f32x4 into[2], out[2], beta[2];
+  float total, xinv, pinv, kinv, qinv;
+  __device__ __forceinline__ void load(const Gate* g, int hf, int q) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      into[x] = row4(g->into, 2 * hf + x, q);
+      out[x] = row4(g->out, 2 * hf + x, q);
+      beta[x] = row4(g->beta, 2 * hf + x, q);
+    }
+    total = g->total;
+    xinv = g->xinv;
+    pinv = g->pinv;
+    kinv = g->kinv;
+    qinv = g->qinv;
+  }
+};
+
+// A block of 32 rows of an operand in LDS: both pieces, and what its columns'
+// values are to be multiplied by.
+struct Block {
+  half8 f[2][64];
+  float inv[16];
+};
+
+template <int P>
+__device__ __forceinline__ void publish(Block* blk, const f32x4& t0, const f32x4& t1,
+                                        const Scale& s, int lane) {
+  half8 f[2];
+  to_frag<P>(t0, t1, s.mul, f);
+  blk->f[0][lane] = f[0];
+  if constexpr (P == 2) blk->f[1][lane] = f[1];
+  if (lane < 16) blk->inv[lane] = s.inv;
+}
+
+__device__ __forceinline__ float abs_max2(const f32x4 (&v)[2]) { return abs_max(v); }
+
+// What both kernels know of their place.
+struct Place {
+  int64_t b, head;
+  int h, hk, col0;
+};
+
+template <int NT>
 __device__ __forceinline__ Place place_of(const ChunkArgs& c) {
   Place p;
   const DeltaArgs& a = c.a;
-  const int groups = c.dvp / 16;
-  const int64_t wave = (int64_t)blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6);
-  p.any = wave < a.b * a.hv * groups;
-  p.head = wave / groups;
-  p.col = (int)(wave - p.head * groups) * 16 + (threadIdx.x & 15);
+  const int groups = (c.dvp / 16 + NT - 1) / NT;
+  // the workgroups of one head read the same fragments: on one XCD's L2
+  const int id = xcd_logical_block((int)blockIdx.x, (int)gridDim.x);
+  p.head = id / groups;
+  p.col0 = (int)(id - p.head * groups) * 16 * NT + (threadIdx.x & 15);
   p.b = p.head / a.hv;
   p.h = (int)(p.head - p.b * a.hv);
   p.hk = p.h / (a.hv / a.hk);
-  p.ok = p.col < a.dv;
-  p.groups = groups;
   return p;
 }
 
-template <int T, int DP, bool BWD>
-__global__ void __launch_bounds__(256) delta_scan(ChunkArgs c) {
+template <int T, int DP, int NT, bool BWD>
+__global__ void __launch_bounds__(128) delta_scan(ChunkArgs c) {
   constexpr int NP = T == T_F32 ? 2 : 1, OP = T == T_BF16 ? 1 : 2;
-  constexpr int KS = DP / 32, MT = DP / 16;
+  constexpr int KS = DP / 32, MT = DP / 16, MW = MT / 2;
+  typedef Raw<T> R;
+  __shared__ Block bs[NT][KS], by[NT][2], bu[NT][2], bo[BWD ? 1 : NT][2];
   const DeltaArgs& a = c.a;
-  const Place p = place_of(c);
-  if (!p.any) return;
-  const int lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
+  const Place p = place_of<NT>(c);
+  const int lane = threadIdx.x & 63, hf = uniform((int)threadIdx.x >> 6);
+  const int m = lane & 15, q = lane >> 4;
   const int64_t len = live_tokens(a, p.b);
   const int chunks = (int)((len + kChunk - 1) / kChunk);
-  f32x4 s[MT];
+  bool ok[NT], in[NT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+  for (int nt = 0; nt < NT; ++nt) {
+    ok[nt] = p.col0 + 16 * nt < a.dv;
+    in[nt] = p.col0 + 16 * nt < c.dvp;
+  }
+
+  f32x4 s[NT][MW];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 16 * i + 4 * q + r;
-      s[i][r] = a.s0 && p.ok && row < a.dk
-                    ? a.s0[(p.head * a.dk + row) * a.dv + p.col] : 0.f;
-    }
-  for (int chunk = 0; chunk < chunks; ++chunk) {
-    const int64_t bc = p.b * c.nc + chunk, kid = bc * a.hk + p.hk, hid = bc * a.hv + p.h;
-    const int64_t t0 = (int64_t)chunk * kChunk;
-    const int n = (int)(len - t0 < kChunk ? len - t0 : kChunk);
-    const Gate* gate = c.gate + hid;
-    const float kinv = c.kq_inv[2 * kid], qinv = c.kq_inv[2 * kid + 1];
-    const Frag* ka = c.ka + kid * NP * 4 * KS * 64 + lane;
-    const Frag* kt = c.kt + kid * NP * MT * 2 * 64 + lane;
-    const Frag* xa = c.xa + hid * 2 * kTri * 64 + lane;
-    if constexpr (BWD) {
-      float* st = c.states + hid * DP * c.dvp + p.col;
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) st[(int64_t)(16 * i + 4 * q + r) * c.dvp] = s[i][r];
-    }
-    f32x4 e[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < MW; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int t = 16 * i + 4 * q + r;
-        e[i][r] = p.ok && t < n ? load1<T>(a.v, p.b * a.v_stride[0] + (t0 + t) * a.v_stride[1] +
-                                                    p.h * a.v_stride[2] + p.col)
-                                : 0.f;
+        const int row = 16 * (hf * MW + i) + 4 * q + r;
+        s[nt][i][r] = a.s0 && ok[nt] && row < a.dk
+                          ? a.s0[(p.head * a.dk + row) * a.dv + p.col0 + 16 * nt] : 0.f;
       }
-    half8 fs[KS][2];
-    const Scale ss = scale_of(column_max(abs_max(s)));
+
+  // this wave's fragments and values of one chunk
+  half8 ka[2][KS][NP], kt[MW][2][NP], xa[2][2][2], qa[2][KS][NP], pa[2][2][OP];
+  typename R::type vr[NT][2][4];
+  Gates gt, gn;
+  const auto kid_of = [&](int chunk) { return (p.b * c.nc + chunk) * a.hk + p.hk; };
+  const auto hid_of = [&](int chunk) { return (p.b * c.nc + chunk) * a.hv + p.h; };
+  const auto load_rows = [&](half8(&f)[2][KS][NP], const Frag* base, int chunk) {
+    const Frag* src = base + kid_of(chunk) * NP * 4 * KS * 64 + lane;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) to_frag<2>(s[2 * ks], s[2 * ks + 1], ss.mul, fs[ks]);
-    // e = V - exp(G) o (K S)
-    const float cks = kinv * ss.inv;
+    for (int x = 0; x < 2; ++x)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+      for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        half8 f[NP];
+        for (int y = 0; y < NP; ++y) f[x][ks][y] = src[((y * 4 + 2 * hf + x) * KS + ks) * 64];
+  };
+  const auto load_kt = [&](int chunk) {
+    const Frag* src = c.kt + kid_of(chunk) * NP * MT * 2 * 64 + lane;
 #pragma unroll
-        for (int x = 0; x < NP; ++x) f[x] = ka[((x * 4 + i) * KS + ks) * 64];
-        acc = mfma_pieces<NP, 2>(f, fs[ks], acc);
-      }
-      const f32x4 into = row4(gate->into, i, q);
+    for (int i = 0; i < MW; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) e[i][r] -= into[r] * (cks * acc[r]);
-    }
-    // E = e - X (beta o e)
-    f32x4 u[4];
+      for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const f32x4 beta = row4(gate->beta, i, q);
+        for (int y = 0; y < NP; ++y)
+          kt[i][ks][y] = src[((y * MT + hf * MW + i) * 2 + ks) * 64];
+  };
+  // rows 0..31 of a lower triangular operand have their first block only
+  const auto load_tri = [&](auto& f, const Frag* base, int pieces, int chunk) {
+    const Frag* src = base + hid_of(chunk) * pieces * kTri * 64 + lane;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) u[i][r] = beta[r] * e[i][r];
-    }
-    half8 fu[2][2];
-    Scale us = scale_of(column_max(abs_max(u)));
-    to_frag<2>(u[0], u[1], us.mul, fu[0]);
-    to_frag<2>(u[2], u[3], us.mul, fu[1]);
-    const float cx = gate->xinv * us.inv;
+    for (int x = 0; x < 2; ++x)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+      for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-      for (int ks = 0; ks < (i < 2 ? 1 : 2); ++ks) {
-        const half8 f[2] = {xa[tri_block(i, ks) * 64], xa[(kTri + tri_block(i, ks)) * 64]};
-        acc = mfma_pieces<2, 2>(f, fu[ks], acc);
-      }
+        for (int y = 0; y < (int)(sizeof(f[0][0]) / sizeof(half8)); ++y)
+          if (ks == 0 || hf) f[x][ks][y] = src[(y * kTri + (hf ? 2 + 2 * x + ks : x)) * 64];
+  };
+  const auto load_v = [&](int chunk) {
+    const int64_t t0 = (int64_t)chunk * kChunk;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) e[i][r] -= cx * acc[r];
-    }
-    if constexpr (BWD) {
-      float* ep = c.e + hid * kChunk * c.dvp + p.col;
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) ep[(int64_t)(16 * i + 4 * q + r) * c.dvp] = e[i][r];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const f32x4 beta = row4(gate->beta, i, q);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) u[i][r] = beta[r] * e[i][r];
-    }
-    if constexpr (!BWD) {
-      // O = scale exp(G) o (Q S) + P U; an output of 16 bits takes fewer
-      // pieces: bf16 one of each (2^-12 against its 2^-9), fp16 two
-      const Frag* qa = c.qa + kid * NP * 4 * KS * 64 + lane;
-      const Frag* pa = c.pa + hid * OP * kTri * 64 + lane;
-      us = scale_of(column_max(abs_max(u)));
-      to_frag<OP>(u[0], u[1], us.mul, fu[0]);
-      to_frag<OP>(u[2], u[3], us.mul, fu[1]);
-      const float cq = a.scale * qinv * ss.inv, cp = gate->pinv * us.inv;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f}, acc2 = acc;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          half8 f[NP];
-#pragma unroll
-          for (int x = 0; x < NP; ++x) f[x] = qa[((x * 4 + i) * KS + ks) * 64];
-          acc = mfma_pieces<NP, OP>(f, fs[ks], acc);
-        }
-#pragma unroll
-        for (int ks = 0; ks < (i < 2 ? 1 : 2); ++ks) {
-          half8 f[OP];
-#pragma unroll
-          for (int x = 0; x < OP; ++x) f[x] = pa[(x * kTri + tri_block(i, ks)) * 64];
-          acc2 = mfma_pieces<OP, OP>(f, fu[ks], acc2);
-        }
-        const f32x4 into = row4(gate->into, i, q);
+      for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int64_t t = t0 + 16 * i + 4 * q + r;
-          if (p.ok && t < a.l)
-            store1<T>(a.o, ((p.b * a.l + t) * a.hv + p.h) * a.dv + p.col,
-                      t < len ? fmaf(cq * into[r], acc[r], cp * acc2[r]) : 0.f);
+          const int64_t t = t0 + 16 * (2 * hf + x) + 4 * q + r;
+          vr[nt][x][r] = 0;
+          if (ok[nt] && t < len)
+            vr[nt][x][r] = ((const typename R::type*)a.v)[p.b * a.v_stride[0] + t * a.v_stride[1] +
+                                                          p.h * a.v_stride[2] + p.col0 + 16 * nt];
         }
+  };
+  if (chunks > 0) {
+    gt.load(c.gate + hid_of(0), hf, q);
+    load_rows(ka, c.ka, 0);
+    load_v(0);
+    if constexpr (!BWD) load_rows(qa, c.qa, 0);
+    load_tri(xa, c.xa, 2, 0);
+    load_kt(0);
+    if constexpr (!BWD) load_tri(pa, c.pa, OP, 0);
+  }
+  for (int chunk = 0; chunk < chunks; ++chunk) {
+    const int next = chunk + 1 < chunks ? chunk + 1 : chunk;
+    const int64_t t0 = (int64_t)chunk * kChunk, hid = hid_of(chunk);
+    gn.load(c.gate + hid_of(next), hf, q);
+    // the state's blocks of this wave
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const Scale ss = scale_of(column_max(abs_max(s[nt])));
+#pragma unroll
+      for (int i = 0; i < MW; i += 2)
+        publish<2>(&bs[nt][(hf * MW + i) / 2], s[nt][i], s[nt][i + 1], ss, lane);
+    }
+    exchange();
+    // e = V - exp(G) o (K S)
+    f32x4 e[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      f32x4 acc[2][2] = {};
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const half8 f[2] = {bs[nt][ks].f[0][lane], bs[nt][ks].f[1][lane]};
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          acc[x][ks / (KS / 2)] = mfma_pieces<NP, 2>(ka[x][ks], f, acc[x][ks / (KS / 2)]);
       }
+      const float i0 = gt.kinv * bs[nt][0].inv[m], i1 = gt.kinv * bs[nt][KS - 1].inv[m];
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          e[nt][x][r] = R::value(vr[nt][x][r]) -
+                        gt.into[x][r] * fmaf(i0, acc[x][0][r], i1 * acc[x][1][r]);
     }
-    // S <- exp(G_64) S + K^T (exp(G_64 - G) o U)
+    load_rows(ka, c.ka, next);
+    load_v(next);
+    f32x4 u[NT][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const f32x4 out = row4(gate->out, i, q);
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) u[i][r] *= out[r];
+      for (int x = 0; x < 2; ++x) u[nt][x] = gt.beta[x] * e[nt][x];
+      publish<2>(&by[nt][hf], u[nt][0], u[nt][1], scale_of(column_max(abs_max2(u[nt]))), lane);
     }
-    us = scale_of(column_max(abs_max(u)));
-    to_frag<2>(u[0], u[1], us.mul, fu[0]);
-    to_frag<2>(u[2], u[3], us.mul, fu[1]);
-    const float ck = kinv * us.inv, total = gate->total;
+    // Q S, while the other wave's block is on its way; an output of 16 bits
+    // takes fewer pieces: bf16 one of each operand (2^-12 against its 2^-9)
+    f32x4 o[BWD ? 1 : NT][2];
+    if constexpr (!BWD) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+      for (int nt = 0; nt < NT; ++nt) {
+        f32x4 acc[2][2] = {};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          half8 f[OP];
+#pragma unroll
+          for (int y = 0; y < OP; ++y) f[y] = bs[nt][ks].f[y][lane];
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            acc[x][ks / (KS / 2)] = mfma_pieces<NP, OP>(qa[x][ks], f, acc[x][ks / (KS / 2)]);
+        }
+        const float sc = a.scale * gt.qinv;
+        const float i0 = sc * bs[nt][0].inv[m], i1 = sc * bs[nt][KS - 1].inv[m];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            o[nt][x][r] = gt.into[x][r] * fmaf(i0, acc[x][0][r], i1 * acc[x][1][r]);
+      }
+      load_rows(qa, c.qa, next);
+    }
+    exchange();
+    // E = e - X (beta o e), U = beta o E
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      f32x4 acc[2][2] = {};
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        half8 f[NP];
+        if (ks > hf) break;
+        const half8 f[2] = {by[nt][ks].f[0][lane], by[nt][ks].f[1][lane]};
 #pragma unroll
-        for (int x = 0; x < NP; ++x) f[x] = kt[((x * MT + i) * 2 + ks) * 64];
-        acc = mfma_pieces<NP, 2>(f, fu[ks], acc);
+        for (int x = 0; x < 2; ++x) acc[x][ks] = mfma_pieces<2, 2>(xa[x][ks], f, acc[x][ks]);
       }
+      const float i0 = gt.xinv * by[nt][0].inv[m], i1 = gt.xinv * by[nt][1].inv[m];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) s[i][r] = fmaf(ck, acc[r], total * s[i][r]);
+      for (int x = 0; x < 2; ++x) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) e[nt][x][r] -= fmaf(i0, acc[x][0][r], i1 * acc[x][1][r]);
+        u[nt][x] = gt.beta[x] * e[nt][x];
+      }
+      if constexpr (!BWD)
+        publish<OP>(&bo[nt][hf], u[nt][0], u[nt][1], scale_of(column_max(abs_max2(u[nt]))), lane);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) u[nt][x] *= gt.out[x];
+      publish<2>(&bu[nt][hf], u[nt][0], u[nt][1], scale_of(column_max(abs_max2(u[nt]))), lane);
     }
+    load_tri(xa, c.xa, 2, next);
+    if constexpr (BWD) {
+      // what the gradient needs of this chunk
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if (!in[nt]) continue;
+        float* st = c.states + hid * DP * c.dvp + p.col0 + 16 * nt;
+        float* ep = c.e + hid * kChunk * c.dvp + p.col0 + 16 * nt;
+#pragma unroll
+        for (int i = 0; i < MW; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            st[(int64_t)(16 * (hf * MW + i) + 4 * q + r) * c.dvp] = s[nt][i][r];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            ep[(int64_t)(16 * (2 * hf + x) + 4 * q + r) * c.dvp] = e[nt][x][r];
+      }
+    }
+    exchange();
+    // S <- exp(G_64) S + K^T (exp(G_64 - G) o U)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      half8 f[2][2];
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) f[ks][y] = bu[nt][ks].f[y][lane];
+      const float i0 = gt.kinv * bu[nt][0].inv[m], i1 = gt.kinv * bu[nt][1].inv[m];
+#pragma unroll
+      for (int i = 0; i < MW; ++i) {
+        f32x4 acc[2] = {};
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) acc[ks] = mfma_pieces<NP, 2>(kt[i][ks], f[ks], acc[ks]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          s[nt][i][r] = fmaf(gt.total, s[nt][i][r], fmaf(i0, acc[0][r], i1 * acc[1][r]));
+      }
+    }
+    load_kt(next);
+    if constexpr (!BWD) {
+      // O = scale exp(G) o (Q S) + P U
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        f32x4 acc[2][2] = {};
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          if (ks > hf) break;
+          half8 f[OP];
+#pragma unroll
+          for (int y = 0; y < OP; ++y) f[y] = bo[nt][ks].f[y][lane];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) acc[x][ks] = mfma_pieces<OP, OP>(pa[x][ks], f, acc[x][ks]);
+        }
+        const float i0 = gt.pinv * bo[nt][0].inv[m], i1 = gt.pinv * bo[nt][1].inv[m];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int64_t t = t0 + 16 * (2 * hf + x) + 4 * q + r;
+            if (ok[nt] && t < a.l)
+              store1<T>(a.o, ((p.b * a.l + t) * a.hv + p.h) * a.dv + p.col0 + 16 * nt,
+                        t < len ? o[nt][x][r] + fmaf(i0, acc[x][0][r], i1 * acc[x][1][r]) : 0.f);
+          }
+      }
+      load_tri(pa, c.pa, OP, next);
+    }
+    gt = gn;
   }
   if constexpr (!BWD) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int nt = 0; nt < NT; ++nt) {
+      if (!ok[nt]) continue;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * i + 4 * q + r;
-        if (p.ok && row < a.dk) a.s1[(p.head * a.dk + row) * a.dv + p.col] = s[i][r];
-      }
-    // outputs past the last live chunk
-    if (p.ok)
-      for (int64_t t = (int64_t)chunks * kChunk + q; t < a.l; t += 4)
-        store1<T>(a.o, ((p.b * a.l + t) * a.hv + p.h) * a.dv + p.col, 0.f);
+      for (int i = 0; i < MW; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 16 * (hf * MW + i) + 4 * q + r;
+          if (row < a.dk) a.s1[(p.head * a.dk + row) * a.dv + p.col0 + 16 * nt] = s[nt][i][r];
+        }
+      // outputs past the last live chunk
+      for (int64_t t = (int64_t)chunks * kChunk + 4 * hf + q; t < a.l; t += 8)
+        store1<T>(a.o, ((p.b * a.l + t) * a.hv + p.h) * a.dv + p.col0 + 16 * nt, 0.f);
+    }
   }
 }
 
@@ -223,171 +378,261 @@ __global__ void __launch_bounds__(256) delta_scan(ChunkArgs c) {
 //   dU = P^T dO + exp(G_64 - G) o (K dS),   W = dU - X^T (beta o dU),
 //   dV = beta o W,
 //   dS <- exp(G_64) dS + Q^T (scale exp(G) o dO) - K^T (exp(G) o dV).
-template <int T, int DP>
-__global__ void __launch_bounds__(256) delta_scan_bwd(ChunkArgs c) {
+template <int T, int DP, int NT>
+__global__ void __launch_bounds__(128) delta_scan_bwd(ChunkArgs c) {
   constexpr int NP = T == T_F32 ? 2 : 1;
-  constexpr int KS = DP / 32, MT = DP / 16;
+  constexpr int KS = DP / 32, MT = DP / 16, MW = MT / 2;
+  typedef Raw<T> R;
+  __shared__ Block bs[NT][KS], by[NT][2], bu[NT][2], bo[NT][2], bd[NT][2];
   const DeltaArgs& a = c.a;
-  const Place p = place_of(c);
-  if (!p.any) return;
-  const int lane = threadIdx.x & 63, q = lane >> 4;
+  const Place p = place_of<NT>(c);
+  const int lane = threadIdx.x & 63, hf = uniform((int)threadIdx.x >> 6);
+  const int m = lane & 15, q = lane >> 4;
   const int64_t len = live_tokens(a, p.b);
   const int chunks = (int)((len + kChunk - 1) / kChunk);
-  f32x4 s[MT];
+  bool ok[NT], in[NT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+  for (int nt = 0; nt < NT; ++nt) {
+    ok[nt] = p.col0 + 16 * nt < a.dv;
+    in[nt] = p.col0 + 16 * nt < c.dvp;
+  }
+  f32x4 s[NT][MW];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 16 * i + 4 * q + r;
-      s[i][r] = a.ds1 && p.ok && row < a.dk
-                    ? a.ds1[(p.head * a.dk + row) * a.dv + p.col] : 0.f;
-    }
-  for (int chunk = chunks - 1; chunk >= 0; --chunk) {
-    const int64_t bc = p.b * c.nc + chunk, kid = bc * a.hk + p.hk, hid = bc * a.hv + p.h;
-    const int64_t t0 = (int64_t)chunk * kChunk;
-    const int n = (int)(len - t0 < kChunk ? len - t0 : kChunk);
-    const Gate* gate = c.gate + hid;
-    const float kinv = c.kq_inv[2 * kid], qinv = c.kq_inv[2 * kid + 1];
-    const Frag* ka = c.ka + kid * NP * 4 * KS * 64 + lane;
-    const Frag* kt = c.kt + kid * NP * MT * 2 * 64 + lane;
-    const Frag* qt = c.qt + kid * NP * MT * 2 * 64 + lane;
-    const Frag* xt = c.xt + hid * 2 * kTri * 64 + lane;
-    const Frag* pt = c.pt + hid * 2 * kTri * 64 + lane;
-    float* st = c.dstates + hid * DP * c.dvp + p.col;
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) st[(int64_t)(16 * i + 4 * q + r) * c.dvp] = s[i][r];
-    f32x4 d[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < MW; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int t = 16 * i + 4 * q + r;
-        d[i][r] = p.ok && t < n
-                      ? load1<T>(a.dout, p.b * a.do_stride[0] + (t0 + t) * a.do_stride[1] +
-                                             p.h * a.do_stride[2] + p.col)
-                      : 0.f;
+        const int row = 16 * (hf * MW + i) + 4 * q + r;
+        s[nt][i][r] = a.ds1 && ok[nt] && row < a.dk
+                          ? a.ds1[(p.head * a.dk + row) * a.dv + p.col0 + 16 * nt] : 0.f;
       }
-    half8 fd[2][NP];
-    const Scale ds = scale_of(column_max(abs_max(d)));
-    to_frag<NP>(d[0], d[1], ds.mul, fd[0]);
-    to_frag<NP>(d[2], d[3], ds.mul, fd[1]);
-    half8 fs[KS][2];
-    const Scale ss = scale_of(column_max(abs_max(s)));
+
+  half8 ka[2][KS][NP], kt[MW][2][NP], qt[MW][2][NP], xt[2][2][2], pt[2][2][2];
+  typename R::type dr[NT][2][4];
+  Gates gt, gn;
+  const auto kid_of = [&](int chunk) { return (p.b * c.nc + chunk) * a.hk + p.hk; };
+  const auto hid_of = [&](int chunk) { return (p.b * c.nc + chunk) * a.hv + p.h; };
+  const auto load_ka = [&](int chunk) {
+    const Frag* src = c.ka + kid_of(chunk) * NP * 4 * KS * 64 + lane;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) to_frag<2>(s[2 * ks], s[2 * ks + 1], ss.mul, fs[ks]);
-    const float cks = kinv * ss.inv, cp = gate->pinv * ds.inv;
-    f32x4 w[4], y[4];
+    for (int x = 0; x < 2; ++x)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f}, acc2 = acc;
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int y = 0; y < NP; ++y) ka[x][ks][y] = src[((y * 4 + 2 * hf + x) * KS + ks) * 64];
+  };
+  const auto load_t = [&](half8(&f)[MW][2][NP], const Frag* base, int chunk) {
+    const Frag* src = base + kid_of(chunk) * NP * MT * 2 * 64 + lane;
+#pragma unroll
+    for (int i = 0; i < MW; ++i)
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int y = 0; y < NP; ++y)
+          f[i][ks][y] = src[((y * MT + hf * MW + i) * 2 + ks) * 64];
+  };
+  // rows 32..63 of an upper triangular operand have their second block only
+  const auto load_tri = [&](half8(&f)[2][2][2], const Frag* base, int chunk) {
+    const Frag* src = base + hid_of(chunk) * 2 * kTri * 64 + lane;
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          if (ks == 1 || !hf) f[x][ks][y] = src[(y * kTri + (hf ? 4 + x : 2 * x + ks)) * 64];
+  };
+  const auto load_d = [&](int chunk) {
+    const int64_t t0 = (int64_t)chunk * kChunk;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int64_t t = t0 + 16 * (2 * hf + x) + 4 * q + r;
+          dr[nt][x][r] = 0;
+          if (ok[nt] && t < len)
+            dr[nt][x][r] =
+                ((const typename R::type*)a.dout)[p.b * a.do_stride[0] + t * a.do_stride[1] +
+                                                  p.h * a.do_stride[2] + p.col0 + 16 * nt];
+        }
+  };
+  if (chunks > 0) {
+    const int last = chunks - 1;
+    gt.load(c.gate + hid_of(last), hf, q);
+    load_d(last);
+    load_ka(last);
+    load_tri(pt, c.pt, last);
+    load_tri(xt, c.xt, last);
+    load_t(kt, c.kt, last);
+    load_t(qt, c.qt, last);
+  }
+  for (int chunk = chunks - 1; chunk >= 0; --chunk) {
+    const int next = chunk > 0 ? chunk - 1 : 0;
+    const int64_t t0 = (int64_t)chunk * kChunk, hid = hid_of(chunk);
+    gn.load(c.gate + hid_of(next), hf, q);
+    f32x4 d[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const Scale ss = scale_of(column_max(abs_max(s[nt])));
+#pragma unroll
+      for (int i = 0; i < MW; i += 2)
+        publish<2>(&bs[nt][(hf * MW + i) / 2], s[nt][i], s[nt][i + 1], ss, lane);
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) d[nt][x][r] = R::value(dr[nt][x][r]);
+      publish<NP>(&bd[nt][hf], d[nt][0], d[nt][1], scale_of(column_max(abs_max2(d[nt]))), lane);
+    }
+    load_d(next);
+    exchange();
+    f32x4 w[NT][2], y[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      f32x4 acc[2][2] = {}, acp[2][2] = {};
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        half8 f[NP];
+        const half8 f[2] = {bs[nt][ks].f[0][lane], bs[nt][ks].f[1][lane]};
 #pragma unroll
-        for (int x = 0; x < NP; ++x) f[x] = ka[((x * 4 + i) * KS + ks) * 64];
-        acc = mfma_pieces<NP, 2>(f, fs[ks], acc);
+        for (int x = 0; x < 2; ++x)
+          acc[x][ks / (KS / 2)] = mfma_pieces<NP, 2>(ka[x][ks], f, acc[x][ks / (KS / 2)]);
       }
-#pragma unroll
-      for (int ks = (i < 2 ? 0 : 1); ks < 2; ++ks) {
-        const half8 f[2] = {pt[tri_block_t(i, ks) * 64], pt[(kTri + tri_block_t(i, ks)) * 64]};
-        acc2 = mfma_pieces<2, NP>(f, fd[ks], acc2);
-      }
-      const f32x4 out = row4(gate->out, i, q), beta = row4(gate->beta, i, q);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        w[i][r] = fmaf(cks * out[r], acc[r], cp * acc2[r]);
-        y[i][r] = beta[r] * w[i][r];
-      }
-    }
-    half8 fy[2][2];
-    Scale ys = scale_of(column_max(abs_max(y)));
-    to_frag<2>(y[0], y[1], ys.mul, fy[0]);
-    to_frag<2>(y[2], y[3], ys.mul, fy[1]);
-    const float cx = gate->xinv * ys.inv;
-    float* wp = c.dw + hid * kChunk * c.dvp + p.col;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int ks = (i < 2 ? 0 : 1); ks < 2; ++ks) {
-        const half8 f[2] = {xt[tri_block_t(i, ks) * 64], xt[(kTri + tri_block_t(i, ks)) * 64]};
-        acc = mfma_pieces<2, 2>(f, fy[ks], acc);
-      }
-      const f32x4 beta = row4(gate->beta, i, q), into = row4(gate->into, i, q);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int64_t t = t0 + 16 * i + 4 * q + r;
-        w[i][r] -= cx * acc[r];
-        wp[(int64_t)(16 * i + 4 * q + r) * c.dvp] = w[i][r];
-        const float dv = beta[r] * w[i][r];
-        if (p.ok && t < a.l)
-          store1<T>(a.dv_out, ((p.b * a.l + t) * a.hv + p.h) * a.dv + p.col, t < len ? dv : 0.f);
-        y[i][r] = -into[r] * dv * kinv;
-        d[i][r] *= a.scale * into[r] * qinv;
-      }
-    }
-    // one scale for both operands, so that one sum takes both products
-    half8 fq[2][2];
-    ys = scale_of(column_max(fmaxf(abs_max(y), abs_max(d))));
-    to_frag<2>(y[0], y[1], ys.mul, fy[0]);
-    to_frag<2>(y[2], y[3], ys.mul, fy[1]);
-    to_frag<2>(d[0], d[1], ys.mul, fq[0]);
-    to_frag<2>(d[2], d[3], ys.mul, fq[1]);
-    const float total = gate->total;
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        half8 f[NP], g[NP];
+        if (ks < hf) continue;
+        half8 f[NP];
 #pragma unroll
-        for (int x = 0; x < NP; ++x) {
-          f[x] = kt[((x * MT + i) * 2 + ks) * 64];
-          g[x] = qt[((x * MT + i) * 2 + ks) * 64];
-        }
-        acc = mfma_pieces<NP, 2>(f, fy[ks], acc);
-        acc = mfma_pieces<NP, 2>(g, fq[ks], acc);
+        for (int z = 0; z < NP; ++z) f[z] = bd[nt][ks].f[z][lane];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) acp[x][ks] = mfma_pieces<2, NP>(pt[x][ks], f, acp[x][ks]);
       }
+      const float i0 = gt.kinv * bs[nt][0].inv[m], i1 = gt.kinv * bs[nt][KS - 1].inv[m];
+      const float p0 = gt.pinv * bd[nt][0].inv[m], p1 = gt.pinv * bd[nt][1].inv[m];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) s[i][r] = fmaf(ys.inv, acc[r], total * s[i][r]);
+      for (int x = 0; x < 2; ++x) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          w[nt][x][r] = fmaf(gt.out[x][r], fmaf(i0, acc[x][0][r], i1 * acc[x][1][r]),
+                             fmaf(p0, acp[x][0][r], p1 * acp[x][1][r]));
+        y[nt][x] = gt.beta[x] * w[nt][x];
+      }
+      publish<2>(&by[nt][hf], y[nt][0], y[nt][1], scale_of(column_max(abs_max2(y[nt]))), lane);
     }
-  }
-  if (a.ds0) {
+    load_ka(next);
+    load_tri(pt, c.pt, next);
+    // the state's gradient after this chunk, while the exchange is under way
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int nt = 0; nt < NT; ++nt) {
+      if (!in[nt]) continue;
+      float* st = c.dstates + hid * DP * c.dvp + p.col0 + 16 * nt;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * i + 4 * q + r;
-        if (p.ok && row < a.dk) a.ds0[(p.head * a.dk + row) * a.dv + p.col] = s[i][r];
+      for (int i = 0; i < MW; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          st[(int64_t)(16 * (hf * MW + i) + 4 * q + r) * c.dvp] = s[nt][i][r];
+    }
+    exchange();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      f32x4 acc[2][2] = {};
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        if (ks < hf) continue;
+        const half8 f[2] = {by[nt][ks].f[0][lane], by[nt][ks].f[1][lane]};
+#pragma unroll
+        for (int x = 0; x < 2; ++x) acc[x][ks] = mfma_pieces<2, 2>(xt[x][ks], f, acc[x][ks]);
       }
+      const float i0 = gt.xinv * by[nt][0].inv[m], i1 = gt.xinv * by[nt][1].inv[m];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) w[nt][x][r] -= fmaf(i0, acc[x][0][r], i1 * acc[x][1][r]);
+        y[nt][x] = gt.beta[x] * w[nt][x];
+        const f32x4 dv = y[nt][x];
+        y[nt][x] *= -gt.kinv * gt.into[x];
+        d[nt][x] *= a.scale * gt.qinv * gt.into[x];
+        const int64_t row0 = 16 * (2 * hf + x) + 4 * q;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int64_t t = t0 + row0 + r;
+          if (in[nt]) c.dw[(hid * kChunk + row0 + r) * c.dvp + p.col0 + 16 * nt] = w[nt][x][r];
+          if (ok[nt] && t < a.l)
+            store1<T>(a.dv_out, ((p.b * a.l + t) * a.hv + p.h) * a.dv + p.col0 + 16 * nt,
+                      t < len ? dv[r] : 0.f);
+        }
+      }
+      // one scale for both operands, so that one sum takes both products
+      const Scale ys = scale_of(column_max(fmaxf(abs_max2(y[nt]), abs_max2(d[nt]))));
+      publish<2>(&bu[nt][hf], y[nt][0], y[nt][1], ys, lane);
+      publish<2>(&bo[nt][hf], d[nt][0], d[nt][1], ys, lane);
+    }
+    load_tri(xt, c.xt, next);
+    exchange();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      half8 f[2][2], g[2][2];
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          f[ks][z] = bu[nt][ks].f[z][lane];
+          g[ks][z] = bo[nt][ks].f[z][lane];
+        }
+      const float i0 = bu[nt][0].inv[m], i1 = bu[nt][1].inv[m];
+#pragma unroll
+      for (int i = 0; i < MW; ++i) {
+        f32x4 acc[2] = {};
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          acc[ks] = mfma_pieces<NP, 2>(kt[i][ks], f[ks], acc[ks]);
+          acc[ks] = mfma_pieces<NP, 2>(qt[i][ks], g[ks], acc[ks]);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          s[nt][i][r] = fmaf(gt.total, s[nt][i][r], fmaf(i0, acc[0][r], i1 * acc[1][r]));
+      }
+    }
+    load_t(kt, c.kt, next);
+    load_t(qt, c.qt, next);
+    gt = gn;
   }
-  if (p.ok)
-    for (int64_t t = (int64_t)chunks * kChunk + q; t < a.l; t += 4)
-      store1<T>(a.dv_out, ((p.b * a.l + t) * a.hv + p.h) * a.dv + p.col, 0.f);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    if (!ok[nt]) continue;
+    if (a.ds0) {
+#pragma unroll
+      for (int i = 0; i < MW; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 16 * (hf * MW + i) + 4 * q + r;
+          if (row < a.dk) a.ds0[(p.head * a.dk + row) * a.dv + p.col0 + 16 * nt] = s[nt][i][r];
+        }
+    }
+    for (int64_t t = (int64_t)chunks * kChunk + 4 * hf + q; t < a.l; t += 8)
+      store1<T>(a.dv_out, ((p.b * a.l + t) * a.hv + p.h) * a.dv + p.col0 + 16 * nt, 0.f);
+  }
 }
 
-inline dim3 grid_of(const ChunkArgs& c, int waves) {
-  const int64_t n = c.a.b * c.a.hv * (c.dvp / 16);
-  return dim3((uint32_t)((n + waves - 1) / waves));
-}
-
-// Waves of a workgroup share fragments through the L1; with few columns one
-// wave a workgroup spreads them over more compute units.
-inline int waves_of(const ChunkArgs& c) {
-  return c.a.b * c.a.hv * (c.dvp / 16) >= 1024 ? 4 : 1;
+template <int T, int DP, int NT>
+void go_nt(const ChunkArgs& c, int what, hipStream_t st) {
+  const int groups = (c.dvp / 16 + NT - 1) / NT;
+  const dim3 grid((uint32_t)(c.a.b * c.a.hv * groups)), block(128);
+  if (what == 0) hipLaunchKernelGGL((delta_scan<T, DP, NT, false>), grid, block, 0, st, c);
+  else if (what == 1) hipLaunchKernelGGL((delta_scan<T, DP, NT, true>), grid, block, 0, st, c);
+  else hipLaunchKernelGGL((delta_scan_bwd<T, DP, NT>), grid, block, 0, st, c);
 }
 
 template <int T, int DP>
 void go(const ChunkArgs& c, int what, hipStream_t st) {
-  const int waves = waves_of(c);
-  if (what == 0)
-    hipLaunchKernelGGL((delta_scan<T, DP, false>), grid_of(c, waves), dim3(64 * waves), 0, st, c);
-  else if (what == 1)
-    hipLaunchKernelGGL((delta_scan<T, DP, true>), grid_of(c, waves), dim3(64 * waves), 0, st, c);
-  else
-    hipLaunchKernelGGL((delta_scan_bwd<T, DP>), grid_of(c, waves), dim3(64 * waves), 0, st, c);
+  // 32 columns a workgroup read each fragment half as often; 16 columns give
+  // twice the workgroups, which few heads need to reach the compute units
+  // (and fp32 fragments of 128 dimensions leave no registers for 32)
+  if constexpr (T != T_F32 || DP == 64) {
+    if (c.a.b * c.a.hv * (c.dvp / 16) > 512) return go_nt<T, DP, 2>(c, what, st);
+  }
+  go_nt<T, DP, 1>(c, what, st);
 }
 
 template <int T>
