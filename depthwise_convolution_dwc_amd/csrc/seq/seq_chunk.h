@@ -30,6 +30,7 @@ namespace dwc {
 namespace seq {
 
 constexpr int kChunk = 64;
+constexpr double kLog2e = 1.4426950408889634074;  // sums of g are kept for exp2
 
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef _Float16 half4 __attribute__((ext_vector_type(4)));
@@ -43,7 +44,7 @@ struct Gate {
   // the packed values of X, P, K and Q times these are the true ones
   float xinv, pinv, kinv, qinv;
   float pad[3];
-  double g[kChunk];    // G_t
+  double g[kChunk];    // G_t log2(e)
 };
 
 // Fragment blocks of 64 lanes x 16 bytes.  Inside a block of 32 along the
@@ -115,6 +116,20 @@ __device__ __forceinline__ float column_max(float m) {
   o = m;
   asm("s_nop 1\n\tv_permlane16_swap_b32 %0, %1" : "+v"(m), "+v"(o));
   return fmaxf(m, o);
+}
+
+// Largest magnitude over a wave: over each 16 lanes by rotations of a row,
+// then over the rows.
+__device__ __forceinline__ float wave_max(float m) {
+#define DWC_ROTATE(v, n) \
+  __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), \
+                                                        0x120 + n, 0xf, 0xf, false))
+  m = fmaxf(m, DWC_ROTATE(m, 8));
+  m = fmaxf(m, DWC_ROTATE(m, 4));
+  m = fmaxf(m, DWC_ROTATE(m, 2));
+  m = fmaxf(m, DWC_ROTATE(m, 1));
+#undef DWC_ROTATE
+  return column_max(m);
 }
 
 // acc += A B from pieces: PA of A, PB of B, the products that matter.

@@ -37,12 +37,6 @@ __device__ __forceinline__ half8 frag44(const _Float16* tile, int row, int ks, i
   return half8{u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
 }
 
-__device__ __forceinline__ float wave_max(float m) {
-#pragma unroll
-  for (int i = 1; i < 64; i <<= 1) m = fmaxf(m, __shfl_xor(m, i, 64));
-  return m;
-}
-
 // Pieces of N consecutive values to a row of a tile.
 template <int P, int N>
 __device__ __forceinline__ void put(_Float16* tile, int row, int col, const float* v, float s) {
@@ -301,7 +295,7 @@ __global__ void __launch_bounds__(DP * 4) delta_grad(ChunkArgs c) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int rr = 16 * wr + 4 * q + i, cc = 16 * j + m;
-          const float d = cc <= rr ? expf((float)(sg[rr] - sg[cc])) : 0.f;
+          const float d = cc <= rr ? __builtin_amdgcn_exp2f((float)(sg[rr] - sg[cc])) : 0.f;
           const float v = ph ? a.scale * d * dp[x][j][i] : -d * dp[x][j][i];
           dp[x][j][i] = cc < rr || (ph && cc == rr) ? v : 0.f;
           mx[x] = fmaxf(mx[x], fabsf(dp[x][j][i]));

@@ -4,21 +4,37 @@
 //
 // One workgroup of 4 waves a (sequence, chunk, key head); the value heads
 // that share the key head reuse K K^T and Q K^T from registers.
+#include "../dwc_device.h"
 #include "seq_chunk.h"
 
 namespace dwc {
 namespace seq {
 namespace prep {
 
-constexpr int kPitch = 65;  // of the 64x64 fp32 tiles in LDS: no two rows on one bank
+// Of the 64x64 fp32 tiles in LDS: rows stay 16-byte aligned, and 16 rows read
+// 16 bytes each at one column cover all 64 banks.
+constexpr int kPitch = 68;
 
-__device__ __forceinline__ float block_max(float m, float* red) {
+// The largest of each of two values over the workgroup.
+__device__ __forceinline__ f32x2 block_max2(float u, float v, float (*red)[4]) {
+  u = wave_max(u);
+  v = wave_max(v);
+  if ((threadIdx.x & 63) == 0) {
+    red[0][threadIdx.x >> 6] = u;
+    red[1][threadIdx.x >> 6] = v;
+  }
+  __syncthreads();
+  return f32x2{fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3])),
+               fmaxf(fmaxf(red[1][0], red[1][1]), fmaxf(red[1][2], red[1][3]))};
+}
+
+// acc += A B for 16x16 fp32 blocks: a holds A's row lane % 16, columns
+// 4 q .. 4 q + 3 (q = lane / 16); b is a result of an earlier product.  Step
+// r sums the columns 4 q + r, which is where register r of a result lies.
+__device__ __forceinline__ f32x4 mul16(const f32x4& a, const f32x4& b, f32x4 acc) {
 #pragma unroll
-  for (int i = 1; i < 64; i <<= 1) m = fmaxf(m, __shfl_xor(m, i, 64));
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
-  __syncthreads();
-  return fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  for (int r = 0; r < 4; ++r) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], b[r], acc, 0, 0, 0);
+  return acc;
 }
 
 template <int P>
@@ -49,12 +65,16 @@ __device__ __forceinline__ void write_tri(const float* tile, float s, Frag* dst)
       ks = blk < 4 ? blk % 2 : 1;
     }
     half8 hi, lo;
+    f32x4 rows[2] = {};
+    if constexpr (!TRANSPOSED) {
+      rows[0] = *(const f32x4*)(tile + (16 * mt + m) * kPitch + 32 * ks + 4 * q);
+      rows[1] = *(const f32x4*)(tile + (16 * mt + m) * kPitch + 32 * ks + 16 + 4 * q);
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int r = 16 * mt + m, c = 32 * ks + (j < 4 ? 4 * q + j : 12 + 4 * q + j);
-      const float v = (TRANSPOSED ? tile[c * kPitch + r] : tile[r * kPitch + c]) * s;
       _Float16 h, l;
-      split(v, &h, &l);
+      split((TRANSPOSED ? tile[c * kPitch + r] : rows[j / 4][j % 4]) * s, &h, &l);
       hi[j] = h;
       lo[j] = l;
     }
@@ -70,14 +90,15 @@ __global__ void __launch_bounds__(256) delta_prep(ChunkArgs c) {
   constexpr int NP = T == T_F32 ? 2 : 1, OP = T == T_BF16 ? 1 : 2;
   constexpr int KS = DP / 32, PITCH = DP + 8, PER = DP / 4;
   extern __shared__ __align__(16) char lds[];
-  __shared__ float red[4];
-  __shared__ double sg[kChunk];
-  __shared__ float sbeta[kChunk];
+  __shared__ float red[4][4];
+  __shared__ __align__(16) double sg[4][kChunk];
+  __shared__ __align__(16) float sbeta[4][kChunk];
   _Float16* rows = (_Float16*)lds;  // [k, q][piece][64][PITCH]
   float* tn = (float*)lds;          // N, then P
   float* tx = tn + kChunk * kPitch;
   const DeltaArgs& a = c.a;
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, m = lane & 15, q = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, q = lane >> 4;
+  const int w = uniform(tid >> 6);
   const int64_t id = blockIdx.x;
   const int hk = (int)(id % a.hk);
   const int64_t bc = id / a.hk;
@@ -87,50 +108,88 @@ __global__ void __launch_bounds__(256) delta_prep(ChunkArgs c) {
   if (t0 >= len) return;
   const int n = (int)(len - t0 < kChunk ? len - t0 : kChunk);
 
+  const int per = a.hv / a.hk;
+  // Wave w makes the gates of the w-th of the next four heads.
+  const auto gates = [&](int first) {
+    if (first + w >= per) return;
+    const int h = hk * per + first + w;
+    Gate* gate = c.gate + bc * a.hv + h;
+    double g = 0.0;
+    float beta = 0.f;
+    if (lane < n) {
+      // below -1e5 the decay is 0 anyway, and sums of it stay finite
+      const float x = a.g[b * a.g_stride[0] + (t0 + lane) * a.g_stride[1] + h * a.g_stride[2]];
+      g = (x < -1e5f ? -1e5 : (double)x) * kLog2e;
+      beta = a.beta[b * a.beta_stride[0] + (t0 + lane) * a.beta_stride[1] + h * a.beta_stride[2]];
+    }
+    // sums in 64 bits: differences of far sums are what decays are made of
+#pragma unroll
+    for (int i = 1; i < 64; i <<= 1) {
+      const double o = __shfl_up(g, i, 64);
+      if (lane >= i) g += o;
+    }
+    const double all = __shfl(g, 63, 64);
+    sg[w][lane] = g;
+    sbeta[w][lane] = beta;
+    gate->into[lane] = __builtin_amdgcn_exp2f((float)g);
+    gate->out[lane] = __builtin_amdgcn_exp2f((float)(all - g));
+    gate->beta[lane] = beta;
+    gate->g[lane] = g;
+    if (lane == 0) gate->total = __builtin_amdgcn_exp2f((float)all);
+  };
+
   // K and Q to LDS as scaled pieces; places past the sequence or the head
   // size are zero whatever memory holds there
   float kinv, qinv;
   {
+    // a thread takes every fourth 8 values of a row
     const int row = tid >> 2, part = tid & 3;
-    float v[2][PER];
+    float v[2][PER], mx[2] = {0.f, 0.f};
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const void* p = x ? a.q : a.k;
       const int64_t* st = x ? a.q_stride : a.k_stride;
-      const int64_t base = b * st[0] + (t0 + row) * st[1] + hk * st[2] + part * PER;
-      float mx = 0.f;
-      if constexpr (WIDE) {
+      const int64_t base = b * st[0] + (t0 + row) * st[1] + hk * st[2];
 #pragma unroll
-        for (int i = 0; i < PER; i += 8) {
-          if (row < n && part * PER + i < a.dk) {
-            load_vec<T, 8>(p, base + i, &v[x][i]);
+      for (int i = 0; i < PER; i += 8) {
+        const int col = 4 * i + 8 * part;
+        if constexpr (WIDE) {
+          if (row < n && col < a.dk) {
+            load_vec<T, 8>(p, base + col, &v[x][i]);
           } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[x][i + j] = 0.f;
           }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            v[x][i + j] = row < n && col + j < a.dk ? load1<T>(p, base + col + j) : 0.f;
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-          v[x][i] = row < n && part * PER + i < a.dk ? load1<T>(p, base + i) : 0.f;
       }
+    }
+    gates(0);
 #pragma unroll
-      for (int i = 0; i < PER; ++i) mx = fmaxf(mx, fabsf(v[x][i]));
-      const Scale s = scale_of(block_max(mx, red));
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int i = 0; i < PER; ++i) mx[x] = fmaxf(mx[x], fabsf(v[x][i]));
+    const f32x2 top = block_max2(mx[0], mx[1], red);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const Scale s = scale_of(top[x]);
       (x ? qinv : kinv) = s.inv;
 #pragma unroll
-      for (int i = 0; i < PER; i += 4) {
-        half4 hi, lo;
+      for (int i = 0; i < PER; i += 8) {
+        half8 hi, lo;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 8; ++j) {
           _Float16 h, l;
           split(v[x][i + j] * s.mul, &h, &l);
           hi[j] = h;
           lo[j] = l;
         }
-        _Float16* dst = rows + ((x * NP) * kChunk + row) * PITCH + part * PER + i;
-        *(half4*)dst = hi;
-        if constexpr (NP == 2) *(half4*)(dst + kChunk * PITCH) = lo;
+        _Float16* dst = rows + ((x * NP) * kChunk + row) * PITCH + 4 * i + 8 * part;
+        *(half8*)dst = hi;
+        if constexpr (NP == 2) *(half8*)(dst + kChunk * PITCH) = lo;
       }
     }
     __syncthreads();
@@ -180,90 +239,98 @@ __global__ void __launch_bounds__(256) delta_prep(ChunkArgs c) {
     }
   }
 
-  const int per = a.hv / a.hk;
   for (int r = 0; r < per; ++r) {
     const int h = hk * per + r;
     const int64_t hid = bc * a.hv + h;
     Gate* gate = c.gate + hid;
     __syncthreads();  // the rows, or the last head's tiles, are read
-    if (w == 0) {
-      double g = 0.0;
-      float beta = 0.f;
-      if (lane < n) {
-        // below -1e5 the decay is 0 anyway, and sums of it stay finite
-        const float x =
-            a.g[b * a.g_stride[0] + (t0 + lane) * a.g_stride[1] + h * a.g_stride[2]];
-        g = x < -1e5f ? -1e5 : (double)x;
-        beta = a.beta[b * a.beta_stride[0] + (t0 + lane) * a.beta_stride[1] +
-                      h * a.beta_stride[2]];
-      }
-      // sums in 64 bits: differences of far sums are what decays are made of
-#pragma unroll
-      for (int i = 1; i < 64; i <<= 1) {
-        const double o = __shfl_up(g, i, 64);
-        if (lane >= i) g += o;
-      }
-      const double all = __shfl(g, 63, 64);
-      sg[lane] = g;
-      sbeta[lane] = beta;
-      gate->into[lane] = expf((float)g);
-      gate->out[lane] = expf((float)(all - g));
-      gate->beta[lane] = beta;
-      gate->g[lane] = g;
-      if (lane == 0) gate->total = expf((float)all);
+    if (r && r % 4 == 0) {
+      gates(r);
+      __syncthreads();
     }
-    __syncthreads();
+    const double* g = sg[r % 4];
+    const float* beta = sbeta[r % 4];
     f32x4 pv[4];
     float pmax = 0.f;
+    double grow[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) grow[i] = g[16 * w + 4 * q + i];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      pv[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      f32x4 nv = pv[j];
+      if (j <= w) {
+        const double gcol = g[16 * j + m];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = 16 * w + 4 * q + i, col = 16 * j + m;
+          const float d =
+              col <= row ? __builtin_amdgcn_exp2f((float)(grow[i] - gcol)) : 0.f;
+          nv[i] = col < row ? d * (kk[j][i] * kinv * kinv) : 0.f;
+          pv[j][i] = a.scale * d * (qk[j][i] * kinv * qinv);
+          pmax = fmaxf(pmax, fabsf(pv[j][i]));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tn[(16 * w + 4 * q + i) * kPitch + 16 * j + m] = nv[i];
+    }
+    __syncthreads();
+    // X = N - N beta X in 16x16 blocks, wave w the block column w.  On the
+    // diagonal by substitution (a lane a column, four lanes the same one) ...
+    f32x4 x[4];
+    {
+      float y[16];
+#pragma unroll
+      for (int t = 0; t < 16; ++t) {
+        const float* row = tn + (16 * w + t) * kPitch + 16 * w;
+        y[t] = row[m];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (4 * k >= t) continue;
+          const f32x4 nb = *(const f32x4*)(row + 4 * k) * *(const f32x4*)(beta + 16 * w + 4 * k);
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+            if (4 * k + z < t) y[t] = fmaf(-nb[z], y[4 * k + z], y[t]);
+        }
+      }
+      f32x4 d;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        d[i] = q < 2 ? (q == 0 ? y[i] : y[4 + i]) : (q == 2 ? y[8 + i] : y[12 + i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = i == w ? d : f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int row = 16 * w + 4 * q + i, col = 16 * j + m;
-        float nv = 0.f;
-        pv[j][i] = 0.f;
-        if (col <= row) {
-          const float d = expf((float)(sg[row] - sg[col]));
-          if (col < row) nv = d * (kk[j][i] * kinv * kinv);
-          pv[j][i] = a.scale * d * (qk[j][i] * kinv * qinv);
-        }
-        pmax = fmaxf(pmax, fabsf(pv[j][i]));
-        tn[row * kPitch + col] = nv;
+        if (i > w) break;
+#pragma unroll
+        for (int z = 0; z < 4; ++z) tx[(16 * i + 4 * q + z) * kPitch + 16 * w + m] = x[i][z];
       }
     }
     __syncthreads();
-    // X = N - N beta X, 16 rows at a time: what the rows above give, by all
-    // waves (a lane a column), then the 16 rows among themselves
-    for (int i = 0; i < 4; ++i) {
-      float acc[4];
+    // ... and below it, with (1 + N_ii beta)^-1 = 1 - X_ii beta:
+    // X_iw = R - X_ii beta R,  R = N_iw - sum over k of N_ik beta X_kw
 #pragma unroll
-      for (int x = 0; x < 4; ++x) acc[x] = tn[(16 * i + 4 * w + x) * kPitch + lane];
-      for (int j = 0; j < 16 * i; ++j) {
-        const float y = sbeta[j] * tx[j * kPitch + lane];
+    for (int i = 1; i < 4; ++i) {
+      if (i <= w) continue;
+      f32x4 acc = {0.f, 0.f, 0.f, 0.f}, nw;
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          acc[x] = fmaf(-tn[(16 * i + 4 * w + x) * kPitch + j], y, acc[x]);
+      for (int k = 0; k < 3; ++k) {
+        if (k >= i || k < w) continue;
+        const f32x4 nb = *(const f32x4*)(tn + (16 * i + m) * kPitch + 16 * k + 4 * q) *
+                         *(const f32x4*)(beta + 16 * k + 4 * q);
+        acc = mul16(nb, x[k], acc);
       }
 #pragma unroll
-      for (int x = 0; x < 4; ++x) tx[(16 * i + 4 * w + x) * kPitch + lane] = acc[x];
-      __syncthreads();
-      if (w == 0) {
-        float x[16];
+      for (int z = 0; z < 4; ++z)
+        nw[z] = tn[(16 * i + 4 * q + z) * kPitch + 16 * w + m] - acc[z];
+      const f32x4 xb = *(const f32x4*)(tx + (16 * i + m) * kPitch + 16 * i + 4 * q) *
+                       *(const f32x4*)(beta + 16 * i + 4 * q);
+      x[i] = nw - mul16(xb, nw, f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-        for (int t = 0; t < 16; ++t) {
-          x[t] = tx[(16 * i + t) * kPitch + lane];
-#pragma unroll
-          for (int s = 0; s < t; ++s)
-            x[t] = fmaf(-tn[(16 * i + t) * kPitch + 16 * i + s] * sbeta[16 * i + s], x[s], x[t]);
-          tx[(16 * i + t) * kPitch + lane] = x[t];
-        }
-      }
-      __syncthreads();
+      for (int z = 0; z < 4; ++z) tx[(16 * i + 4 * q + z) * kPitch + 16 * w + m] = x[i][z];
     }
-    float xmax = 0.f;
-#pragma unroll
-    for (int t = 0; t < 16; ++t) xmax = fmaxf(xmax, fabsf(tx[(16 * w + t) * kPitch + lane]));
-    const Scale xs = scale_of(block_max(xmax, red)), ps = scale_of(block_max(pmax, red));
+    const f32x2 top = block_max2(abs_max(x), pmax, red + 2);
+    const Scale xs = scale_of(top[0]), ps = scale_of(top[1]);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
