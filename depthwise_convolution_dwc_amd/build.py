@@ -61,7 +61,8 @@ def _units():
     u.append(("hip", "seq/seq_norm.hip", "seq_norm.o", []))
     u.append(("hip", "seq/seq_dropout.hip", "seq_dropout.o", []))
     u.append(("hip", "seq/seq_delta_token.hip", "seq_delta_token.o", []))
-    u.append(("hip", "seq/seq_delta_prep.hip", "seq_delta_prep.o", []))
+    u.append(("hip", "seq/seq_delta_prep.hip", "seq_delta_prep.o",
+              ["-mllvm", "-amdgpu-mfma-vgpr-form"]))
     u.append(("hip", "seq/seq_delta_scan.hip", "seq_delta_scan.o",
               ["-mllvm", "-amdgpu-mfma-vgpr-form"]))
     u.append(("hip", "seq/seq_delta_grad.hip", "seq_delta_grad.o",

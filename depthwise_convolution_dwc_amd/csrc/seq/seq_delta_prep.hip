@@ -86,7 +86,7 @@ __device__ __forceinline__ void write_tri(const float* tile, float s, Frag* dst)
 // T: type of q and k.  DP: head size padded.  NP: pieces of an input.  OP:
 // pieces of P in the forward pass.  BWD: also the transposes.
 template <int T, int DP, bool WIDE, bool BWD>
-__global__ void __launch_bounds__(256) delta_prep(ChunkArgs c) {
+__global__ void __launch_bounds__(256, BWD ? 3 : 4) delta_prep(ChunkArgs c) {
   constexpr int NP = T == T_F32 ? 2 : 1, OP = T == T_BF16 ? 1 : 2;
   constexpr int KS = DP / 32, PITCH = DP + 8, PER = DP / 4;
   extern __shared__ __align__(16) char lds[];

@@ -10,8 +10,10 @@ on that stream, so that the allocator does not hand them out too early.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -20,7 +22,9 @@ from . import _DTYPE_CODE, _raise, lib
 
 DELTA_FWD, DELTA_BWD = 0, 1
 _TYPES = (torch.float32, torch.bfloat16, torch.float16)
+_F32, _I32 = (torch.float32,), (torch.int32,)
 _I3 = ctypes.c_int64 * 3
+_DENSE = torch.contiguous_format
 
 
 class NormProblem(ctypes.Structure):
@@ -49,65 +53,62 @@ class DeltaProblem(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+# The problems as the calls below pass them: the structures' bytes, packed in
+# one step (a small call costs the host about as long as the kernel runs).
+_NORM = struct.Struct("4q3if").pack
+_DROPOUT = struct.Struct("qdQQ2i").pack
+_DELTA = struct.Struct("20q5if").pack
+
+
 def bind(l: ctypes.CDLL) -> None:
-    """Argument types of the sequence-layer entry points."""
+    """Argument types of the sequence-layer entry points; a problem may be
+    passed by reference or as the structure's bytes."""
     vp, sz = ctypes.c_void_p, ctypes.c_size_t
-    n, d, r = (ctypes.POINTER(t) for t in (NormProblem, DropoutProblem, DeltaProblem))
-    l.dwc_layer_norm.argtypes = [n] + [vp] * 7
-    l.dwc_layer_norm_bwd_workspace_size.argtypes = [n, ctypes.POINTER(sz)]
-    l.dwc_layer_norm_bwd.argtypes = [n] + [vp] * 9 + [sz, vp]
-    l.dwc_dropout.argtypes = [d] + [vp] * 4
-    l.dwc_delta_step.argtypes = [r] + [vp] * 10
-    l.dwc_delta_workspace_size.argtypes = [r, ctypes.c_int, ctypes.POINTER(sz)]
-    l.dwc_delta_fwd.argtypes = [r] + [vp] * 10 + [sz, vp]
-    l.dwc_delta_bwd.argtypes = [r] + [vp] * 16 + [sz, vp]
+    l.dwc_layer_norm.argtypes = [vp] * 8
+    l.dwc_layer_norm_bwd_workspace_size.argtypes = [vp, ctypes.POINTER(sz)]
+    l.dwc_layer_norm_bwd.argtypes = [vp] * 10 + [sz, vp]
+    l.dwc_dropout.argtypes = [vp] * 5
+    l.dwc_delta_step.argtypes = [vp] * 11
+    l.dwc_delta_workspace_size.argtypes = [vp, ctypes.c_int, ctypes.POINTER(sz)]
+    l.dwc_delta_fwd.argtypes = [vp] * 11 + [sz, vp]
+    l.dwc_delta_bwd.argtypes = [vp] * 17 + [sz, vp]
 
 
-class _On:
-    """The device of ``t`` made current, and the stream to launch on."""
-
-    def __init__(self, t: torch.Tensor, stream):
-        self._guard = torch.cuda.device(t.device) \
-            if t.device.index != torch.cuda.current_device() else None
-        self._stream = stream
-        self._given = stream is not None
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        s = self._stream
-        if s is None:
-            return torch.cuda.current_stream().cuda_stream
-        return s.cuda_stream if hasattr(s, "cuda_stream") else int(s)
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
-
-    def made(self, *ts):
-        """Marks tensors allocated here as used on the stream given."""
-        if self._given:
-            s = self._stream
-            if not hasattr(s, "cuda_stream"):
-                s = torch.cuda.ExternalStream(int(s))
-            for t in ts:
-                if t is not None:
-                    t.record_stream(s)
+_HERE = contextlib.nullcontext()
 
 
-def _device_tensor(t, name, dtypes=None, device=None):
+def _on(index):
+    """The device made current, if it is not."""
+    return _HERE if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
+
+
+def _raw(stream, index, *made):
+    """The stream to launch on; tensors allocated here are marked as used on
+    a stream given."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+    for t in made:
+        if t is not None:
+            t.record_stream(s)
+    return s.cuda_stream
+
+
+def _device_tensor(t, name, dtypes, index=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
+    at = t.get_device()
+    if at < 0 or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if dtypes is not None and t.dtype not in dtypes:
+    if index is not None and at != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {dtypes}, got {t.dtype}")
+    return at
 
 
 def _dense(t, name, shape):
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous of shape {tuple(shape)}, "
                          f"got {tuple(t.shape)}")
 
@@ -120,7 +121,7 @@ def _row_stride(t, name):
     """Elements between the rows of (..., c) seen as rows x c; raises where
     the leading axes do not form one stride or the last is not dense."""
     c = t.shape[-1]
-    if t.numel() == 0:
+    if t.is_contiguous() or t.numel() == 0:
         return c
     if c > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}'s last axis must be dense")
@@ -139,10 +140,10 @@ def _row_stride(t, name):
     return stride
 
 
-def _weights(w, b, c, device):
+def _weights(w, b, c, index):
     for t, name in ((w, "w"), (b, "b")):
         if t is not None:
-            _device_tensor(t, name, _TYPES, device)
+            _device_tensor(t, name, _TYPES, index)
             _dense(t, name, (c,))
     if w is not None and b is not None and w.dtype != b.dtype:
         raise TypeError("w and b must have one dtype")
@@ -156,63 +157,62 @@ def layer_norm(x: torch.Tensor, w: Optional[torch.Tensor] = None,
                stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """Layer norm over the last axis: (y, mean, rstd), y of ``out_dtype``
     (x's by default), mean and 1 / sqrt(var + eps) fp32, one a row."""
-    _device_tensor(x, "x", _TYPES)
-    if x.dim() < 1 or x.shape[-1] < 1:
+    index = _device_tensor(x, "x", _TYPES)
+    shape = x.shape
+    if len(shape) < 1 or shape[-1] < 1:
         raise ValueError("x needs a last axis of at least one element")
-    c, lead = x.shape[-1], x.shape[:-1]
-    rows = x.numel() // c
-    wt = _weights(w, b, c, x.device)
+    c, lead = shape[-1], shape[:-1]
+    wt = _weights(w, b, c, index)
     if out is not None:
-        _device_tensor(out, "out", _TYPES if out_dtype is None else (out_dtype,), x.device)
-        _dense(out, "out", x.shape)
+        _device_tensor(out, "out", _TYPES if out_dtype is None else (out_dtype,), index)
+        _dense(out, "out", shape)
         out_dtype = out.dtype
     out_dtype = out_dtype or x.dtype
     if out_dtype not in _TYPES:
         raise TypeError(f"out_dtype must be one of {_TYPES}, got {out_dtype}")
-    p = NormProblem(rows, c, _row_stride(x, "x"), c, _DTYPE_CODE[x.dtype],
-                    _DTYPE_CODE[out_dtype], wt, eps)
-    on = _On(x, stream)
-    with on as s:
-        made = out is None
-        if made:
-            out = torch.empty(x.shape, dtype=out_dtype, device=x.device)
-        mean = torch.empty(lead, dtype=torch.float32, device=x.device)
-        rstd = torch.empty(lead, dtype=torch.float32, device=x.device)
-        on.made(out if made else None, mean, rstd)
-        _raise(lib().dwc_layer_norm(ctypes.byref(p), _ptr(x), _ptr(w), _ptr(b), _ptr(out),
-                                    _ptr(mean), _ptr(rstd), s))
-    return out, mean, rstd
+    p = _NORM(x.numel() // c, c, _row_stride(x, "x"), c, _DTYPE_CODE[x.dtype],
+              _DTYPE_CODE[out_dtype], wt, eps)
+    with _on(index):
+        y = out
+        if y is None:
+            y = torch.empty_like(x, dtype=out_dtype, memory_format=_DENSE)
+        mean = x.new_empty(lead, dtype=torch.float32)
+        rstd = torch.empty_like(mean)
+        s = _raw(stream, index, y if out is None else None, mean, rstd)
+        _raise(lib().dwc_layer_norm(p, x.data_ptr(), _ptr(w), _ptr(b), y.data_ptr(),
+                                    mean.data_ptr(), rstd.data_ptr(), s))
+    return y, mean, rstd
 
 
 def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
                    w: Optional[torch.Tensor] = None, stream=None
                    ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """Gradients of ``layer_norm``: (dx of x's dtype, dw, db fp32)."""
-    _device_tensor(x, "x", _TYPES)
-    _device_tensor(dy, "dy", _TYPES, x.device)
-    if dy.shape != x.shape:
+    index = _device_tensor(x, "x", _TYPES)
+    _device_tensor(dy, "dy", _TYPES, index)
+    shape = x.shape
+    if dy.shape != shape:
         raise ValueError("dy and x disagree in shape")
-    if x.dim() < 1 or x.shape[-1] < 1:
+    if len(shape) < 1 or shape[-1] < 1:
         raise ValueError("x needs a last axis of at least one element")
-    c, lead = x.shape[-1], x.shape[:-1]
+    c, lead = shape[-1], shape[:-1]
     for t, name in ((mean, "mean"), (rstd, "rstd")):
-        _device_tensor(t, name, (torch.float32,), x.device)
+        _device_tensor(t, name, _F32, index)
         _dense(t, name, lead)
-    wt = _weights(w, None, c, x.device)
-    p = NormProblem(x.numel() // c, c, _row_stride(x, "x"), _row_stride(dy, "dy"),
-                    _DTYPE_CODE[x.dtype], _DTYPE_CODE[dy.dtype], wt, 0.0)
-    on = _On(x, stream)
-    with on as s:
+    wt = _weights(w, None, c, index)
+    p = _NORM(x.numel() // c, c, _row_stride(x, "x"), _row_stride(dy, "dy"),
+              _DTYPE_CODE[x.dtype], _DTYPE_CODE[dy.dtype], wt, 0.0)
+    with _on(index):
         need = ctypes.c_size_t()
-        _raise(lib().dwc_layer_norm_bwd_workspace_size(ctypes.byref(p), ctypes.byref(need)))
-        ws = torch.empty(need.value, dtype=torch.uint8, device=x.device)
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dw = torch.empty(c, dtype=torch.float32, device=x.device)
-        db = torch.empty(c, dtype=torch.float32, device=x.device)
-        on.made(ws, dx, dw, db)
-        _raise(lib().dwc_layer_norm_bwd(ctypes.byref(p), _ptr(dy), _ptr(x), _ptr(mean),
-                                        _ptr(rstd), _ptr(w), _ptr(dx), _ptr(dw), _ptr(db),
-                                        _ptr(ws), need.value, s))
+        _raise(lib().dwc_layer_norm_bwd_workspace_size(p, ctypes.byref(need)))
+        ws = x.new_empty(need.value, dtype=torch.uint8)
+        dx = torch.empty_like(x, memory_format=_DENSE)
+        dw = x.new_empty(c, dtype=torch.float32)
+        db = torch.empty_like(dw)
+        s = _raw(stream, index, ws, dx, dw, db)
+        _raise(lib().dwc_layer_norm_bwd(p, dy.data_ptr(), x.data_ptr(), mean.data_ptr(),
+                                        rstd.data_ptr(), _ptr(w), dx.data_ptr(), dw.data_ptr(),
+                                        db.data_ptr(), ws.data_ptr(), need.value, s))
     return dx, dw, db
 
 
@@ -223,72 +223,76 @@ def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0,
     offset, element index).  The gradient of x is this call on dy with the
     same p, seed and offset; elements of later calls that must not share a
     mask take an offset at least (numel + 3) // 4 further."""
-    _device_tensor(x, "x", _TYPES)
+    index = _device_tensor(x, "x", _TYPES)
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
     if residual is not None:
-        _device_tensor(residual, "residual", (x.dtype,), x.device)
+        _device_tensor(residual, "residual", (x.dtype,), index)
         _dense(residual, "residual", x.shape)
     if not 0 <= int(seed) < 1 << 64 or not 0 <= int(offset) < 1 << 64:
         raise ValueError("seed and offset must be in 0 .. 2^64 - 1")
     if out is not None:
-        _device_tensor(out, "out", (x.dtype,), x.device)
+        _device_tensor(out, "out", (x.dtype,), index)
         _dense(out, "out", x.shape)
-    d = DropoutProblem(x.numel(), p, int(seed), int(offset), _DTYPE_CODE[x.dtype], 0)
-    on = _On(x, stream)
-    with on as s:
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-            on.made(out)
-        _raise(lib().dwc_dropout(ctypes.byref(d), _ptr(x), _ptr(residual), _ptr(out), s))
-    return out
+    d = _DROPOUT(x.numel(), p, int(seed), int(offset), _DTYPE_CODE[x.dtype], 0)
+    with _on(index):
+        y = out
+        if y is None:
+            y = torch.empty_like(x, memory_format=_DENSE)
+        s = _raw(stream, index, y if out is None else None)
+        _raise(lib().dwc_dropout(d, x.data_ptr(), _ptr(residual), y.data_ptr(), s))
+    return y
 
 
-def _strides(t, name, heads, last):
-    """(batch, token, head) strides of a b x l x h (x d) tensor."""
-    if last and t.shape[-1] > 1 and t.numel() and t.stride(-1) != 1:
+def _strides(t, name):
+    """(batch, token, head) strides of a b x l x h x d tensor."""
+    s = t.stride()
+    if s[3] != 1 and t.shape[3] > 1 and t.numel():
         raise ValueError(f"{name}'s last axis must be dense")
-    return _I3(*t.stride()[:3])
+    return s[:3]
 
 
 def _delta(q, k, v, g, beta, s0, lengths, scale, dout=None):
-    _device_tensor(q, "q", _TYPES)
-    dev, dt = q.device, (q.dtype,)
-    _device_tensor(k, "k", dt, dev)
-    _device_tensor(v, "v", dt, dev)
-    _device_tensor(g, "g", (torch.float32,), dev)
-    _device_tensor(beta, "beta", (torch.float32,), dev)
-    if q.dim() != 4 or v.dim() != 4:
+    """(the problem's bytes, device index, shape of the states)"""
+    index = _device_tensor(q, "q", _TYPES)
+    dt = (q.dtype,)
+    _device_tensor(k, "k", dt, index)
+    _device_tensor(v, "v", dt, index)
+    _device_tensor(g, "g", _F32, index)
+    _device_tensor(beta, "beta", _F32, index)
+    shape = q.shape
+    if len(shape) != 4 or v.dim() != 4:
         raise ValueError("q, k and v must be b x l x heads x head size")
-    b, n, hk, dk = q.shape
-    hv, dv = v.shape[2:]
-    if k.shape != q.shape or v.shape[:2] != q.shape[:2]:
+    b, n, hk, dk = shape
+    vb, vn, hv, dv = v.shape
+    if k.shape != shape or vb != b or vn != n:
         raise ValueError("q, k and v disagree in shape")
     if g.shape != (b, n, hv) or beta.shape != (b, n, hv):
         raise ValueError(f"g and beta must be {(b, n, hv)}")
+    states = (b, hv, dk, dv)
     if s0 is not None:
-        _device_tensor(s0, "s0", (torch.float32,), dev)
-        _dense(s0, "s0", (b, hv, dk, dv))
+        _device_tensor(s0, "s0", _F32, index)
+        _dense(s0, "s0", states)
     if lengths is not None:
-        _device_tensor(lengths, "lengths", (torch.int32,), dev)
+        _device_tensor(lengths, "lengths", _I32, index)
         _dense(lengths, "lengths", (b,))
+    do = (0, 0, 0)
     if dout is not None:
-        _device_tensor(dout, "dout", dt, dev)
+        _device_tensor(dout, "dout", dt, index)
         if dout.shape != v.shape:
             raise ValueError("dout and v disagree in shape")
+        do = _strides(dout, "dout")
     if scale is None:
         scale = 1.0 / math.sqrt(dk) if dk else 1.0
-    return DeltaProblem(b, n, _strides(q, "q", hk, True), _strides(k, "k", hk, True),
-                        _strides(v, "v", hv, True), _strides(g, "g", hv, False),
-                        _strides(beta, "beta", hv, False),
-                        _strides(dout, "dout", hv, True) if dout is not None else _I3(0, 0, 0),
-                        hk, hv, dk, dv, _DTYPE_CODE[q.dtype], scale)
+    p = _DELTA(b, n, *_strides(q, "q"), *_strides(k, "k"), *_strides(v, "v"), *g.stride(),
+               *beta.stride(), *do, hk, hv, dk, dv, _DTYPE_CODE[q.dtype], scale)
+    return p, index, states
 
 
-def _workspace(p, op, device):
+def _workspace(p, op, like):
     need = ctypes.c_size_t()
-    _raise(lib().dwc_delta_workspace_size(ctypes.byref(p), op, ctypes.byref(need)))
-    return torch.empty(need.value, dtype=torch.uint8, device=device), need.value
+    _raise(lib().dwc_delta_workspace_size(p, op, ctypes.byref(need)))
+    return like.new_empty(need.value, dtype=torch.uint8), need.value
 
 
 def delta_rule_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
@@ -299,22 +303,20 @@ def delta_rule_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.
     """The gated delta rule token by token: (o, s1).  The form for one or a
     few new tokens of each sequence; shapes as ``delta_rule``.  out_state
     may be s0: the state is then updated in place."""
-    p = _delta(q, k, v, g, beta, s0, lengths, scale)
-    shape = (p.b, p.hv, p.dk, p.dv)
+    p, index, states = _delta(q, k, v, g, beta, s0, lengths, scale)
     if out_state is not None:
-        _device_tensor(out_state, "out_state", (torch.float32,), q.device)
-        _dense(out_state, "out_state", shape)
-    on = _On(q, stream)
-    with on as s:
-        o = torch.empty(v.shape, dtype=v.dtype, device=q.device)
-        on.made(o)
-        if out_state is None:
-            out_state = torch.empty(shape, dtype=torch.float32, device=q.device)
-            on.made(out_state)
-        _raise(lib().dwc_delta_step(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
-                                    _ptr(beta), _ptr(s0), _ptr(lengths), _ptr(o),
-                                    _ptr(out_state), s))
-    return o, out_state
+        _device_tensor(out_state, "out_state", _F32, index)
+        _dense(out_state, "out_state", states)
+    with _on(index):
+        o = torch.empty_like(v, memory_format=_DENSE)
+        s1 = out_state
+        if s1 is None:
+            s1 = g.new_empty(states)
+        s = _raw(stream, index, o, s1 if out_state is None else None)
+        _raise(lib().dwc_delta_step(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                                    beta.data_ptr(), _ptr(s0), _ptr(lengths), o.data_ptr(),
+                                    s1.data_ptr(), s))
+    return o, s1
 
 
 def delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
@@ -328,16 +330,15 @@ def delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
     b x l x hv fp32; s0: b x hv x dk x dv fp32 or None; lengths: b int32 or
     None.  o: b x l x hv x dv of v's dtype; s1: the states after the last
     token.  scale defaults to 1 / sqrt(dk)."""
-    p = _delta(q, k, v, g, beta, s0, lengths, scale)
-    on = _On(q, stream)
-    with on as s:
-        ws, need = _workspace(p, DELTA_FWD, q.device)
-        o = torch.empty(v.shape, dtype=v.dtype, device=q.device)
-        s1 = torch.empty((p.b, p.hv, p.dk, p.dv), dtype=torch.float32, device=q.device)
-        on.made(ws, o, s1)
-        _raise(lib().dwc_delta_fwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
-                                   _ptr(beta), _ptr(s0), _ptr(lengths), _ptr(o), _ptr(s1),
-                                   _ptr(ws), need, s))
+    p, index, states = _delta(q, k, v, g, beta, s0, lengths, scale)
+    with _on(index):
+        ws, need = _workspace(p, DELTA_FWD, q)
+        o = torch.empty_like(v, memory_format=_DENSE)
+        s1 = g.new_empty(states)
+        s = _raw(stream, index, ws, o, s1)
+        _raise(lib().dwc_delta_fwd(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                                   beta.data_ptr(), _ptr(s0), _ptr(lengths), o.data_ptr(),
+                                   s1.data_ptr(), ws.data_ptr(), need, s))
     return o, s1
 
 
@@ -347,24 +348,24 @@ def delta_rule_bwd(dout: torch.Tensor, ds1: Optional[torch.Tensor], q: torch.Ten
                    scale: Optional[float] = None, stream=None):
     """Gradients of ``delta_rule`` from those of o and s1 (None: zero):
     (dq, dk, dv, dg, dbeta, ds0), ds0 None where s0 is."""
-    p = _delta(q, k, v, g, beta, s0, lengths, scale, dout)
+    p, index, states = _delta(q, k, v, g, beta, s0, lengths, scale, dout)
     if ds1 is not None:
-        _device_tensor(ds1, "ds1", (torch.float32,), q.device)
-        _dense(ds1, "ds1", (p.b, p.hv, p.dk, p.dv))
-    on = _On(q, stream)
-    with on as s:
-        ws, need = _workspace(p, DELTA_BWD, q.device)
-        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        dk = torch.empty(k.shape, dtype=k.dtype, device=q.device)
-        dv = torch.empty(v.shape, dtype=v.dtype, device=q.device)
-        dg = torch.empty(g.shape, dtype=torch.float32, device=q.device)
-        dbeta = torch.empty(g.shape, dtype=torch.float32, device=q.device)
+        _device_tensor(ds1, "ds1", _F32, index)
+        _dense(ds1, "ds1", states)
+    with _on(index):
+        ws, need = _workspace(p, DELTA_BWD, q)
+        dq = torch.empty_like(q, memory_format=_DENSE)
+        dk = torch.empty_like(q, memory_format=_DENSE)
+        dv = torch.empty_like(v, memory_format=_DENSE)
+        dg = torch.empty_like(g, memory_format=_DENSE)
+        dbeta = torch.empty_like(g, memory_format=_DENSE)
         ds0 = torch.empty_like(s0) if s0 is not None else None
-        on.made(ws, dq, dk, dv, dg, dbeta, ds0)
-        _raise(lib().dwc_delta_bwd(ctypes.byref(p), _ptr(dout), _ptr(ds1), _ptr(q), _ptr(k),
-                                   _ptr(v), _ptr(g), _ptr(beta), _ptr(s0), _ptr(lengths),
-                                   _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dbeta),
-                                   _ptr(ds0), _ptr(ws), need, s))
+        s = _raw(stream, index, ws, dq, dk, dv, dg, dbeta, ds0)
+        _raise(lib().dwc_delta_bwd(p, dout.data_ptr(), _ptr(ds1), q.data_ptr(), k.data_ptr(),
+                                   v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(s0),
+                                   _ptr(lengths), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                   dg.data_ptr(), dbeta.data_ptr(), _ptr(ds0), ws.data_ptr(),
+                                   need, s))
     return dq, dk, dv, dg, dbeta, ds0
 
 
