@@ -17,16 +17,21 @@ Outputs and gradients are computed in fp32 (the library's output type).  For
 bf16/fp16 operands the forward returns fp32; the backward rounds the
 incoming gradient to the operand dtype (the library takes X, W and dY in one
 dtype) and returns dX and dW in the dtypes of X and W.
+
+Layer norm, dropout and the gated delta rule have autograd wrappers here too,
+and ``GatedDeltaMixer`` is the sequence layer that runs them together with a
+causal depthwise convolution.
 """
 
 from __future__ import annotations
 
 import math
-from typing import Tuple, Union
+from typing import NamedTuple, Optional, Tuple, Union
 
 import torch
+import torch.nn.functional as F
 
-from . import bwd_data, bwd_filter, fwd
+from . import bwd_data, bwd_filter, fwd, sequence
 
 IntPair = Union[int, Tuple[int, int]]
 
@@ -162,3 +167,229 @@ class DepthwiseConv2d(torch.nn.Module):
     def extra_repr(self) -> str:
         return (f"{self.channels}, kernel_size={self.kernel_size}, stride={self.stride}, "
                 f"padding={self.padding}, layout={self.layout!r}")
+
+
+class LayerNormFunction(torch.autograd.Function):
+    """``sequence.layer_norm`` and its gradients; mean and rstd are kept, the
+    normalised rows are computed again."""
+
+    @staticmethod
+    def forward(ctx, x, w, b, eps, out_dtype):
+        y, mean, rstd = sequence.layer_norm(x, w, b, eps, out_dtype)
+        ctx.save_for_backward(x, w, mean, rstd)
+        ctx.b_dtype = b.dtype if b is not None else None
+        return y
+
+    @staticmethod
+    def backward(ctx, gy):
+        x, w, mean, rstd = ctx.saved_tensors
+        dx, dw, db = sequence.layer_norm_bwd(gy.contiguous(), x, mean, rstd, w)
+        return (dx, dw.to(w.dtype) if w is not None else None,
+                db.to(ctx.b_dtype) if ctx.b_dtype is not None else None, None, None)
+
+
+def layer_norm(x: torch.Tensor, w: Optional[torch.Tensor] = None,
+               b: Optional[torch.Tensor] = None, eps: float = 1e-5,
+               out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """Layer norm over the last axis with autograd; y is of ``out_dtype`` (x's
+    by default).  A matrix with a row stride is read in place; other views
+    are made contiguous first (one copy)."""
+    if x.dim() != 2 or x.stride(1) != 1 or x.stride(0) < x.shape[1]:
+        x = x.contiguous()
+    return LayerNormFunction.apply(x, w, b, eps, out_dtype)
+
+
+class LayerNorm(torch.nn.Module):
+    """Layer norm over the last axis; weight and bias fp32 unless ``dtype``
+    says otherwise."""
+
+    def __init__(self, channels: int, eps: float = 1e-5, bias: bool = True, device=None,
+                 dtype=torch.float32):
+        super().__init__()
+        self.channels, self.eps = int(channels), float(eps)
+        self.weight = torch.nn.Parameter(torch.ones(self.channels, device=device, dtype=dtype))
+        self.bias = torch.nn.Parameter(
+            torch.zeros(self.channels, device=device, dtype=dtype)) if bias else None
+
+    def forward(self, x: torch.Tensor, out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+        return layer_norm(x, self.weight, self.bias, self.eps, out_dtype)
+
+    def extra_repr(self) -> str:
+        return f"{self.channels}, eps={self.eps}, bias={self.bias is not None}"
+
+
+class DropoutFunction(torch.autograd.Function):
+    """``sequence.dropout``: the mask is made again from (seed, offset) in the
+    backward pass, nothing is saved."""
+
+    @staticmethod
+    def forward(ctx, x, p, seed, offset, residual):
+        ctx.key = (p, seed, offset)
+        ctx.residual = residual is not None
+        return sequence.dropout(x, p, seed, offset, residual=residual)
+
+    @staticmethod
+    def backward(ctx, gy):
+        gx = None
+        if ctx.needs_input_grad[0]:
+            gx = sequence.dropout(gy.contiguous(), *ctx.key)
+        return gx, None, None, None, gy if ctx.residual else None
+
+
+def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0,
+            residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """residual + (kept ? x / (1 - p) : 0) with autograd; the mask is a
+    function of (seed, offset, element index)."""
+    return DropoutFunction.apply(x.contiguous(), p, seed, offset,
+                                 residual.contiguous() if residual is not None else None)
+
+
+class DeltaRuleFunction(torch.autograd.Function):
+    """``sequence.delta_rule`` and its gradients; only the inputs are saved."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, g, beta, s0, lengths, scale):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(q, k, v, g, beta, s0, lengths)
+        ctx.scale = scale
+        return sequence.delta_rule(q, k, v, g, beta, s0, lengths, scale)
+
+    @staticmethod
+    def backward(ctx, do, ds1):
+        q, k, v, g, beta, s0, lengths = ctx.saved_tensors
+        do = torch.zeros_like(v, memory_format=torch.contiguous_format) if do is None \
+            else do.contiguous()
+        ds1 = ds1.contiguous() if ds1 is not None else None
+        return sequence.delta_rule_bwd(do, ds1, q, k, v, g, beta, s0, lengths,
+                                       ctx.scale) + (None, None)
+
+
+def delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
+               beta: torch.Tensor, s0: Optional[torch.Tensor] = None,
+               lengths: Optional[torch.Tensor] = None, scale: Optional[float] = None
+               ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The gated delta rule over whole sequences with autograd: (o, s1).
+    Shapes as ``sequence.delta_rule``; g, beta and the states are fp32."""
+    return DeltaRuleFunction.apply(q, k, v, g, beta, s0, lengths, scale)
+
+
+class MixerState(NamedTuple):
+    """What a ``GatedDeltaMixer`` carries from token to token: the last
+    kernel_size - 1 tokens of its convolution's input (b x taps x channels)
+    and the states of the delta rule (b x value heads x dk x dv, fp32)."""
+
+    taps: torch.Tensor
+    states: torch.Tensor
+
+
+class GatedDeltaMixer(torch.nn.Module):
+    """A residual sequence layer on b x l x channels:
+
+      h = layer_norm(x);  q, k, v = SiLU(causal depthwise convolution(h W_in))
+      q, k normalised to length 1;  beta = sigmoid(h W_beta),
+      g = -exp(a) softplus(h W_g + bias)
+      o, state = delta_rule(q, k, v, g, beta, state)
+      y = x + dropout(layer_norm(o) per head, times SiLU(h W_gate), times W_out)
+
+    ``forward`` takes whole sequences (``lengths`` where they are unequal: y
+    past a length is x) and returns (y, MixerState); ``step`` takes one token
+    of each sequence and updates the state in place.  Dropout is active in
+    training; its masks are a function of ``seed`` and of how many elements
+    earlier calls covered."""
+
+    def __init__(self, channels: int, heads: int, key_heads: Optional[int] = None,
+                 key_dim: int = 128, value_dim: int = 128, kernel_size: int = 4,
+                 p: float = 0.0, seed: int = 0, eps: float = 1e-5, device=None,
+                 dtype=torch.float32):
+        super().__init__()
+        key_heads = heads if key_heads is None else key_heads
+        if key_heads < 1 or heads % key_heads:
+            raise ValueError("heads must be a multiple of key_heads")
+        if not 1 <= key_dim <= 128:
+            raise ValueError("key_dim must be 1..128")
+        if kernel_size < 1:
+            raise ValueError("kernel_size must be at least 1")
+        if not 0.0 <= p <= 1.0:
+            raise ValueError("p must be 0..1")
+        self.heads, self.key_heads = int(heads), int(key_heads)
+        self.key_dim, self.value_dim = int(key_dim), int(value_dim)
+        self.kernel_size, self.p, self.seed = int(kernel_size), float(p), int(seed)
+        self.offset = 0
+        nk, nv = self.key_heads * self.key_dim, self.heads * self.value_dim
+        self.mixed = 2 * nk + nv
+        kw = dict(device=device, dtype=dtype)
+        self.norm = LayerNorm(channels, eps, device=device)
+        self.w_in = torch.nn.Linear(channels, self.mixed, bias=False, **kw)
+        self.w_rate = torch.nn.Linear(channels, 2 * self.heads, bias=False, **kw)
+        self.w_gate = torch.nn.Linear(channels, nv, bias=False, **kw)
+        self.w_out = torch.nn.Linear(nv, channels, bias=False, **kw)
+        self.conv = DepthwiseConv2d(self.mixed, (1, self.kernel_size),
+                                    padding=(0, self.kernel_size - 1), layout="nhwc", **kw)
+        self.out_norm = LayerNorm(self.value_dim, eps, device=device)
+        f32 = dict(device=device, dtype=torch.float32)
+        self.a = torch.nn.Parameter(torch.zeros(self.heads, **f32))
+        self.g_bias = torch.nn.Parameter(torch.zeros(self.heads, **f32))
+
+    def _rates(self, h):
+        r = self.w_rate(h).float()
+        g = -torch.exp(self.a) * F.softplus(r[..., :self.heads] + self.g_bias)
+        return g, torch.sigmoid(r[..., self.heads:])
+
+    def _heads(self, c):
+        """q, k, v as heads, from the convolution's fp32 output."""
+        dt = self.w_in.weight.dtype
+        nk = self.key_heads * self.key_dim
+        c = F.silu(c)
+        qk = c[..., :2 * nk].unflatten(-1, (2 * self.key_heads, self.key_dim))
+        qk = (qk * torch.rsqrt((qk * qk).sum(-1, keepdim=True) + 1e-6)).to(dt)
+        v = c[..., 2 * nk:].unflatten(-1, (self.heads, self.value_dim)).to(dt)
+        return qk[..., :self.key_heads, :], qk[..., self.key_heads:, :], v
+
+    def _out(self, x, h, o):
+        y = self.w_out(self.out_norm(o).flatten(-2) * F.silu(self.w_gate(h)))
+        y = y.to(x.dtype)
+        if not self.training or self.p == 0.0:
+            return x + y
+        offset = self.offset
+        self.offset += (y.numel() + 3) // 4
+        return dropout(y, self.p, self.seed, offset, residual=x)
+
+    def forward(self, x: torch.Tensor, state: Optional[MixerState] = None,
+                lengths: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, MixerState]:
+        b, n, _ = x.shape
+        h = self.norm(x, self.w_in.weight.dtype)
+        m, taps = self.w_in(h), self.kernel_size - 1
+        past = state.taps if state is not None else m.new_zeros(b, taps, self.mixed)
+        m = torch.cat([past, m], 1)
+        # of the outputs of a padded row, those that see no token past their own
+        c = self.conv(m.unsqueeze(1))[:, 0, taps:taps + n]
+        g, beta = self._rates(h)
+        o, s1 = delta_rule(*self._heads(c), g, beta, state.states if state is not None else None,
+                           lengths)
+        y = self._out(x, h, o)
+        if lengths is None:
+            return y, MixerState(m[:, n:].contiguous(), s1)
+        ends = lengths.clamp(0, n).long()
+        live = (torch.arange(n, device=x.device) < ends[:, None])[..., None]
+        at = ends[:, None] + torch.arange(taps, device=x.device)
+        kept = m.gather(1, at[..., None].expand(-1, -1, self.mixed))
+        return torch.where(live, y, x), MixerState(kept, s1)
+
+    @torch.no_grad()
+    def step(self, x: torch.Tensor, state: MixerState) -> torch.Tensor:
+        """One token of each sequence (b x 1 x channels); ``state`` is updated
+        in place."""
+        if x.dim() != 3 or x.shape[1] != 1:
+            raise ValueError(f"x must be b x 1 x channels, got {tuple(x.shape)}")
+        h = self.norm(x, self.w_in.weight.dtype)
+        m = torch.cat([state.taps, self.w_in(h)], 1)
+        c = fwd(m.unsqueeze(1), self.conv.weight, 1, 0, algo=self.conv.algo)[:, 0]
+        g, beta = self._rates(h)
+        o, _ = sequence.delta_rule_step(*self._heads(c), g, beta, state.states,
+                                        out_state=state.states)
+        state.taps.copy_(m[:, 1:])
+        return self._out(x, h, o)
+
+    def extra_repr(self) -> str:
+        return (f"heads={self.heads}, key_heads={self.key_heads}, key_dim={self.key_dim}, "
+                f"value_dim={self.value_dim}, kernel_size={self.kernel_size}, p={self.p}")
