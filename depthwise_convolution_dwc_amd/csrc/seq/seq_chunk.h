@@ -73,6 +73,7 @@ struct ChunkArgs {
   Gate* gate;                // per (b, chunk, hv)
   float *states, *dstates;   // per (b, chunk, hv): dp x dvp, before the chunk / after it
   float *e, *dw;             // per (b, chunk, hv): 64 x dvp
+  bool wide;  // v and dout can be read 16 bytes at a time, dv is a multiple of 8
 };
 
 __device__ __forceinline__ int64_t live_tokens(const DeltaArgs& a, int64_t b) {
@@ -104,32 +105,30 @@ __device__ __forceinline__ void split(float v, _Float16* hi, _Float16* lo) {
   *lo = (_Float16)(v - (float)*hi);
 }
 
-// Largest magnitude over the lanes that share a column (lane % 16).  The
-// swap exchanges the odd halves (then rows of 16 lanes) of its first register
-// with the even ones of its second: of a register and its copy, one is left
-// with either half's values in all lanes, so a maximum joins them.  (The
-// compiler's builtin returns its first result twice.)
+// Largest magnitude over the lanes that share a column (lane % 16).
 __device__ __forceinline__ float column_max(float m) {
-  float o = m;
-  asm("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(m), "+v"(o));
+  float o;
+  halves(m, o);
   m = fmaxf(m, o);
-  o = m;
-  asm("s_nop 1\n\tv_permlane16_swap_b32 %0, %1" : "+v"(m), "+v"(o));
+  rows16(m, o);
   return fmaxf(m, o);
 }
 
 // Largest magnitude over a wave: over each 16 lanes by rotations of a row,
 // then over the rows.
 __device__ __forceinline__ float wave_max(float m) {
-#define DWC_ROTATE(v, n) \
-  __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), \
-                                                        0x120 + n, 0xf, 0xf, false))
-  m = fmaxf(m, DWC_ROTATE(m, 8));
-  m = fmaxf(m, DWC_ROTATE(m, 4));
-  m = fmaxf(m, DWC_ROTATE(m, 2));
-  m = fmaxf(m, DWC_ROTATE(m, 1));
-#undef DWC_ROTATE
+  m = fmaxf(m, row_move<0x128>(m));
+  m = fmaxf(m, row_move<0x124>(m));
+  m = fmaxf(m, row_move<0x122>(m));
+  m = fmaxf(m, row_move<0x121>(m));
   return column_max(m);
+}
+
+// Element lane of a block at a uniform address: the address stays in scalar
+// registers, the lane's part is one 32-bit offset.
+template <typename V>
+__device__ __forceinline__ V at_lane(const V* block, uint32_t offset) {
+  return *(const V*)((const char*)block + offset);
 }
 
 // acc += A B from pieces: PA of A, PB of B, the products that matter.

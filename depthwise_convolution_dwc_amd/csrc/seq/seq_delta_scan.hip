@@ -84,7 +84,7 @@ __device__ __forceinline__ float abs_max2(const f32x4 (&v)[2]) { return abs_max(
 // What both kernels know of their place.
 struct Place {
   int64_t b, head;
-  int h, hk, col0;
+  int h, hk, block, col0;  // block: the first column, col0: this lane's
 };
 
 template <int NT>
@@ -95,11 +95,95 @@ __device__ __forceinline__ Place place_of(const ChunkArgs& c) {
   // the workgroups of one head read the same fragments: on one XCD's L2
   const int id = xcd_logical_block((int)blockIdx.x, (int)gridDim.x);
   p.head = id / groups;
-  p.col0 = (int)(id - p.head * groups) * 16 * NT + (threadIdx.x & 15);
+  p.block = (int)(id - p.head * groups) * 16 * NT;
+  p.col0 = p.block + (threadIdx.x & 15);
   p.b = p.head / a.hv;
   p.h = (int)(p.head - p.b * a.hv);
   p.hk = p.h / (a.hv / a.hk);
   return p;
+}
+
+// This wave's 32 rows of a chunk in a tensor of tokens.
+template <int T, int NT>
+struct Rows {
+  char* lane;      // token 4 q of this wave's rows in the first chunk, column col0
+  int64_t stride;  // bytes between tokens
+  __device__ __forceinline__ Rows(const void* t, const int64_t (&st)[3], const Place& p, int hf,
+                                  int q)
+      : stride(st[1] * E) {
+    lane = (char*)t + (p.b * st[0] + p.h * st[2] + p.col0) * E + (32 * hf + 4 * q) * stride;
+  }
+  // a dense output
+  __device__ __forceinline__ Rows(void* t, int64_t l, int hv, int dv, const Place& p, int hf,
+                                  int q)
+      : stride((int64_t)hv * dv * E) {
+    lane = (char*)t + ((p.b * l * hv + p.h) * dv + p.col0) * E + (32 * hf + 4 * q) * stride;
+  }
+  // A chunk inside the sequence needs no look at each token.
+  __device__ __forceinline__ void load(typename Raw<T>::type (&f)[NT][2][4], int chunk,
+                                       int64_t len, bool whole, const bool (&ok)[NT], int hf,
+                                       int q) const {
+    const int64_t t0 = (int64_t)chunk * kChunk;
+    const char* at = lane + t0 * stride;
+    if (whole && t0 + kChunk <= len) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            f[nt][x][r] = ((const typename Raw<T>::type*)(at + (16 * x + r) * stride))[16 * nt];
+    } else {
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            f[nt][x][r] = 0;
+            if (ok[nt] && t0 + 32 * hf + 16 * x + 4 * q + r < len)
+              f[nt][x][r] = ((const typename Raw<T>::type*)(at + (16 * x + r) * stride))[16 * nt];
+          }
+    }
+  }
+  // Rows past the sequence's length are written as zeros.
+  __device__ __forceinline__ void store(const f32x4 (&f)[NT][2], int chunk, int64_t len, int64_t l,
+                                        bool whole, const bool (&ok)[NT], int hf, int q) const {
+    const int64_t t0 = (int64_t)chunk * kChunk;
+    char* at = lane + t0 * stride;
+    if (whole && t0 + kChunk <= len) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            store1<T>(at + (16 * x + r) * stride, 16 * nt, f[nt][x][r]);
+    } else {
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const int64_t t = t0 + 32 * hf + 16 * x + 4 * q + r;
+            if (ok[nt] && t < l)
+              store1<T>(at + (16 * x + r) * stride, 16 * nt, t < len ? f[nt][x][r] : 0.f);
+          }
+    }
+  }
+
+ private:
+  static constexpr int64_t E = ElemBytes<T>::value;
+};
+
+// Values of a 16-row result to rows row0 + 4 q + r of a matrix of dvp
+// columns, the matrix at a uniform address.
+__device__ __forceinline__ void store_tile(float* matrix, int row0, int dvp, uint32_t offset,
+                                           const f32x4& v) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    *(float*)((char*)(matrix + (int64_t)(row0 + r) * dvp) + offset) = v[r];
 }
 
 template <int T, int DP, int NT, bool BWD>
@@ -114,11 +198,13 @@ __global__ void __launch_bounds__(128) delta_scan(ChunkArgs c) {
   const int m = lane & 15, q = lane >> 4;
   const int64_t len = live_tokens(a, p.b);
   const int chunks = (int)((len + kChunk - 1) / kChunk);
+  const uint32_t loff = 16 * lane, soff = 4 * (4 * q * c.dvp + p.col0);
+  const bool whole = p.block + 16 * NT <= a.dv;  // no column past the head size
   bool ok[NT], in[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     ok[nt] = p.col0 + 16 * nt < a.dv;
-    in[nt] = p.col0 + 16 * nt < c.dvp;
+    in[nt] = p.block + 16 * nt < c.dvp;
   }
 
   f32x4 s[NT][MW];
@@ -140,50 +226,38 @@ __global__ void __launch_bounds__(128) delta_scan(ChunkArgs c) {
   const auto kid_of = [&](int chunk) { return (p.b * c.nc + chunk) * a.hk + p.hk; };
   const auto hid_of = [&](int chunk) { return (p.b * c.nc + chunk) * a.hv + p.h; };
   const auto load_rows = [&](half8(&f)[2][KS][NP], const Frag* base, int chunk) {
-    const Frag* src = base + kid_of(chunk) * NP * 4 * KS * 64 + lane;
+    const Frag* src = base + kid_of(chunk) * NP * 4 * KS * 64;
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-        for (int y = 0; y < NP; ++y) f[x][ks][y] = src[((y * 4 + 2 * hf + x) * KS + ks) * 64];
+        for (int y = 0; y < NP; ++y) f[x][ks][y] = at_lane(src + ((y * 4 + 2 * hf + x) * KS + ks) * 64, loff);
   };
   const auto load_kt = [&](int chunk) {
-    const Frag* src = c.kt + kid_of(chunk) * NP * MT * 2 * 64 + lane;
+    const Frag* src = c.kt + kid_of(chunk) * NP * MT * 2 * 64;
 #pragma unroll
     for (int i = 0; i < MW; ++i)
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
         for (int y = 0; y < NP; ++y)
-          kt[i][ks][y] = src[((y * MT + hf * MW + i) * 2 + ks) * 64];
+          kt[i][ks][y] = at_lane(src + ((y * MT + hf * MW + i) * 2 + ks) * 64, loff);
   };
   // rows 0..31 of a lower triangular operand have their first block only
   const auto load_tri = [&](auto& f, const Frag* base, int pieces, int chunk) {
-    const Frag* src = base + hid_of(chunk) * pieces * kTri * 64 + lane;
+    const Frag* src = base + hid_of(chunk) * pieces * kTri * 64;
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
         for (int y = 0; y < (int)(sizeof(f[0][0]) / sizeof(half8)); ++y)
-          if (ks == 0 || hf) f[x][ks][y] = src[(y * kTri + (hf ? 2 + 2 * x + ks : x)) * 64];
+          if (ks == 0 || hf)
+            f[x][ks][y] = at_lane(src + (y * kTri + (hf ? 2 + 2 * x + ks : x)) * 64, loff);
   };
-  const auto load_v = [&](int chunk) {
-    const int64_t t0 = (int64_t)chunk * kChunk;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int64_t t = t0 + 16 * (2 * hf + x) + 4 * q + r;
-          vr[nt][x][r] = 0;
-          if (ok[nt] && t < len)
-            vr[nt][x][r] = ((const typename R::type*)a.v)[p.b * a.v_stride[0] + t * a.v_stride[1] +
-                                                          p.h * a.v_stride[2] + p.col0 + 16 * nt];
-        }
-  };
+  const Rows<T, NT> rows_v(a.v, a.v_stride, p, hf, q), rows_o(a.o, a.l, a.hv, a.dv, p, hf, q);
+  const auto load_v = [&](int chunk) { rows_v.load(vr, chunk, len, whole, ok, hf, q); };
   if (chunks > 0) {
     gt.load(c.gate + hid_of(0), hf, q);
     load_rows(ka, c.ka, 0);
@@ -195,7 +269,7 @@ __global__ void __launch_bounds__(128) delta_scan(ChunkArgs c) {
   }
   for (int chunk = 0; chunk < chunks; ++chunk) {
     const int next = chunk + 1 < chunks ? chunk + 1 : chunk;
-    const int64_t t0 = (int64_t)chunk * kChunk, hid = hid_of(chunk);
+    const int64_t hid = hid_of(chunk);
     gn.load(c.gate + hid_of(next), hf, q);
     // the state's blocks of this wave
 #pragma unroll
@@ -237,7 +311,7 @@ __global__ void __launch_bounds__(128) delta_scan(ChunkArgs c) {
     }
     // Q S, while the other wave's block is on its way; an output of 16 bits
     // takes fewer pieces: bf16 one of each operand (2^-12 against its 2^-9)
-    f32x4 o[BWD ? 1 : NT][2];
+    f32x4 o[NT][2];
     if constexpr (!BWD) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -292,18 +366,14 @@ __global__ void __launch_bounds__(128) delta_scan(ChunkArgs c) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         if (!in[nt]) continue;
-        float* st = c.states + hid * DP * c.dvp + p.col0 + 16 * nt;
-        float* ep = c.e + hid * kChunk * c.dvp + p.col0 + 16 * nt;
 #pragma unroll
         for (int i = 0; i < MW; ++i)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            st[(int64_t)(16 * (hf * MW + i) + 4 * q + r) * c.dvp] = s[nt][i][r];
+          store_tile(c.states + hid * DP * c.dvp + 16 * nt, 16 * (hf * MW + i), c.dvp, soff,
+                     s[nt][i]);
 #pragma unroll
         for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            ep[(int64_t)(16 * (2 * hf + x) + 4 * q + r) * c.dvp] = e[nt][x][r];
+          store_tile(c.e + hid * kChunk * c.dvp + 16 * nt, 16 * (2 * hf + x), c.dvp, soff,
+                     e[nt][x]);
       }
     }
     exchange();
@@ -345,13 +415,9 @@ __global__ void __launch_bounds__(128) delta_scan(ChunkArgs c) {
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int64_t t = t0 + 16 * (2 * hf + x) + 4 * q + r;
-            if (ok[nt] && t < a.l)
-              store1<T>(a.o, ((p.b * a.l + t) * a.hv + p.h) * a.dv + p.col0 + 16 * nt,
-                        t < len ? o[nt][x][r] + fmaf(i0, acc[x][0][r], i1 * acc[x][1][r]) : 0.f);
-          }
+          for (int r = 0; r < 4; ++r) o[nt][x][r] += fmaf(i0, acc[x][0][r], i1 * acc[x][1][r]);
       }
+      rows_o.store(o, chunk, len, a.l, whole, ok, hf, q);
       load_tri(pa, c.pa, OP, next);
     }
     gt = gn;
@@ -390,11 +456,13 @@ __global__ void __launch_bounds__(128) delta_scan_bwd(ChunkArgs c) {
   const int m = lane & 15, q = lane >> 4;
   const int64_t len = live_tokens(a, p.b);
   const int chunks = (int)((len + kChunk - 1) / kChunk);
+  const uint32_t loff = 16 * lane, soff = 4 * (4 * q * c.dvp + p.col0);
+  const bool whole = p.block + 16 * NT <= a.dv;  // no column past the head size
   bool ok[NT], in[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     ok[nt] = p.col0 + 16 * nt < a.dv;
-    in[nt] = p.col0 + 16 * nt < c.dvp;
+    in[nt] = p.block + 16 * nt < c.dvp;
   }
   f32x4 s[NT][MW];
 #pragma unroll
@@ -414,51 +482,40 @@ __global__ void __launch_bounds__(128) delta_scan_bwd(ChunkArgs c) {
   const auto kid_of = [&](int chunk) { return (p.b * c.nc + chunk) * a.hk + p.hk; };
   const auto hid_of = [&](int chunk) { return (p.b * c.nc + chunk) * a.hv + p.h; };
   const auto load_ka = [&](int chunk) {
-    const Frag* src = c.ka + kid_of(chunk) * NP * 4 * KS * 64 + lane;
+    const Frag* src = c.ka + kid_of(chunk) * NP * 4 * KS * 64;
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-        for (int y = 0; y < NP; ++y) ka[x][ks][y] = src[((y * 4 + 2 * hf + x) * KS + ks) * 64];
+        for (int y = 0; y < NP; ++y)
+          ka[x][ks][y] = at_lane(src + ((y * 4 + 2 * hf + x) * KS + ks) * 64, loff);
   };
   const auto load_t = [&](half8(&f)[MW][2][NP], const Frag* base, int chunk) {
-    const Frag* src = base + kid_of(chunk) * NP * MT * 2 * 64 + lane;
+    const Frag* src = base + kid_of(chunk) * NP * MT * 2 * 64;
 #pragma unroll
     for (int i = 0; i < MW; ++i)
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
         for (int y = 0; y < NP; ++y)
-          f[i][ks][y] = src[((y * MT + hf * MW + i) * 2 + ks) * 64];
+          f[i][ks][y] = at_lane(src + ((y * MT + hf * MW + i) * 2 + ks) * 64, loff);
   };
   // rows 32..63 of an upper triangular operand have their second block only
   const auto load_tri = [&](half8(&f)[2][2][2], const Frag* base, int chunk) {
-    const Frag* src = base + hid_of(chunk) * 2 * kTri * 64 + lane;
+    const Frag* src = base + hid_of(chunk) * 2 * kTri * 64;
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
         for (int y = 0; y < 2; ++y)
-          if (ks == 1 || !hf) f[x][ks][y] = src[(y * kTri + (hf ? 4 + x : 2 * x + ks)) * 64];
+          if (ks == 1 || !hf)
+            f[x][ks][y] = at_lane(src + (y * kTri + (hf ? 4 + x : 2 * x + ks)) * 64, loff);
   };
-  const auto load_d = [&](int chunk) {
-    const int64_t t0 = (int64_t)chunk * kChunk;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int64_t t = t0 + 16 * (2 * hf + x) + 4 * q + r;
-          dr[nt][x][r] = 0;
-          if (ok[nt] && t < len)
-            dr[nt][x][r] =
-                ((const typename R::type*)a.dout)[p.b * a.do_stride[0] + t * a.do_stride[1] +
-                                                  p.h * a.do_stride[2] + p.col0 + 16 * nt];
-        }
-  };
+  const Rows<T, NT> rows_d(a.dout, a.do_stride, p, hf, q),
+      rows_dv(a.dv_out, a.l, a.hv, a.dv, p, hf, q);
+  const auto load_d = [&](int chunk) { rows_d.load(dr, chunk, len, whole, ok, hf, q); };
   if (chunks > 0) {
     const int last = chunks - 1;
     gt.load(c.gate + hid_of(last), hf, q);
@@ -471,7 +528,7 @@ __global__ void __launch_bounds__(128) delta_scan_bwd(ChunkArgs c) {
   }
   for (int chunk = chunks - 1; chunk >= 0; --chunk) {
     const int next = chunk > 0 ? chunk - 1 : 0;
-    const int64_t t0 = (int64_t)chunk * kChunk, hid = hid_of(chunk);
+    const int64_t hid = hid_of(chunk);
     gn.load(c.gate + hid_of(next), hf, q);
     f32x4 d[NT][2];
 #pragma unroll
@@ -526,14 +583,13 @@ __global__ void __launch_bounds__(128) delta_scan_bwd(ChunkArgs c) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       if (!in[nt]) continue;
-      float* st = c.dstates + hid * DP * c.dvp + p.col0 + 16 * nt;
 #pragma unroll
       for (int i = 0; i < MW; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          st[(int64_t)(16 * (hf * MW + i) + 4 * q + r) * c.dvp] = s[nt][i][r];
+        store_tile(c.dstates + hid * DP * c.dvp + 16 * nt, 16 * (hf * MW + i), c.dvp, soff,
+                   s[nt][i]);
     }
     exchange();
+    f32x4 g[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       f32x4 acc[2][2] = {};
@@ -550,24 +606,19 @@ __global__ void __launch_bounds__(128) delta_scan_bwd(ChunkArgs c) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) w[nt][x][r] -= fmaf(i0, acc[x][0][r], i1 * acc[x][1][r]);
         y[nt][x] = gt.beta[x] * w[nt][x];
-        const f32x4 dv = y[nt][x];
+        g[nt][x] = y[nt][x];
         y[nt][x] *= -gt.kinv * gt.into[x];
         d[nt][x] *= a.scale * gt.qinv * gt.into[x];
-        const int64_t row0 = 16 * (2 * hf + x) + 4 * q;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int64_t t = t0 + row0 + r;
-          if (in[nt]) c.dw[(hid * kChunk + row0 + r) * c.dvp + p.col0 + 16 * nt] = w[nt][x][r];
-          if (ok[nt] && t < a.l)
-            store1<T>(a.dv_out, ((p.b * a.l + t) * a.hv + p.h) * a.dv + p.col0 + 16 * nt,
-                      t < len ? dv[r] : 0.f);
-        }
+        if (in[nt])
+          store_tile(c.dw + hid * kChunk * c.dvp + 16 * nt, 16 * (2 * hf + x), c.dvp, soff,
+                     w[nt][x]);
       }
       // one scale for both operands, so that one sum takes both products
       const Scale ys = scale_of(column_max(fmaxf(abs_max2(y[nt]), abs_max2(d[nt]))));
       publish<2>(&bu[nt][hf], y[nt][0], y[nt][1], ys, lane);
       publish<2>(&bo[nt][hf], d[nt][0], d[nt][1], ys, lane);
     }
+    rows_dv.store(g, chunk, len, a.l, whole, ok, hf, q);
     load_tri(xt, c.xt, next);
     exchange();
 #pragma unroll

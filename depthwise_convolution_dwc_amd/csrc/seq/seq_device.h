@@ -128,12 +128,45 @@ __device__ __forceinline__ void store_any(int t, void* p, int64_t i, const float
   else store_vec<T_F16, N>(p, i, v);
 }
 
+// v of another lane of the same row of 16, by a move inside the row (CTRL: a
+// permutation of each four, a mirror of 8 or 16, a rotation).
+template <int CTRL>
+__device__ __forceinline__ float row_move(float v) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
+}
+
+// a = v of the even of two halves of a wave (of each two rows of 16), o = v
+// of the odd one, both in all lanes.  The swap exchanges the odd halves
+// (rows) of its first register with the even ones of its second.  (The
+// compiler's builtin returns its first result twice.)
+__device__ __forceinline__ void halves(float& a, float& o) {
+  o = a;
+  asm("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(a), "+v"(o));
+}
+__device__ __forceinline__ void rows16(float& a, float& o) {
+  o = a;
+  asm("s_nop 1\n\tv_permlane16_swap_b32 %0, %1" : "+v"(a), "+v"(o));
+}
+
 // Sum over groups of W adjacent lanes (W a power of two up to 64); every
-// lane of a group gets the same bits.
+// lane of a group gets the same bits.  Moves inside the registers: an
+// exchange through LDS costs each of the steps ten times as long.
 template <int W>
 __device__ __forceinline__ float lane_sum(float v) {
-#pragma unroll
-  for (int m = 1; m < W; m <<= 1) v += __shfl_xor(v, m, 64);
+  if constexpr (W >= 2) v += row_move<0xB1>(v);    // 1 0 3 2
+  if constexpr (W >= 4) v += row_move<0x4E>(v);    // 2 3 0 1
+  if constexpr (W >= 8) v += row_move<0x141>(v);   // mirror of 8
+  if constexpr (W >= 16) v += row_move<0x140>(v);  // mirror of 16
+  float o;
+  if constexpr (W >= 32) {
+    rows16(v, o);
+    v += o;
+  }
+  if constexpr (W >= 64) {
+    halves(v, o);
+    v += o;
+  }
   return v;
 }
 
