@@ -171,7 +171,7 @@ hipError_t launch_delta_scan(const ChunkArgs& c, bool bwd, hipStream_t st);
 // Back from the last chunk: dv, the state's gradient after each chunk, dw.
 hipError_t launch_delta_scan_bwd(const ChunkArgs& c, hipStream_t st);
 // dq, dk, dg, dbeta of each chunk.
-hipError_t launch_delta_grad(const ChunkArgs& c, hipStream_t st);
+hipError_t launch_delta_grad(ChunkArgs c, hipStream_t st);
 
 }  // namespace seq
 }  // namespace dwc

@@ -16,6 +16,7 @@
 // columns.  A wave owns 16 key dimensions of dQ and dK, so the states go from
 // memory to exactly one wave's registers; the operands that all waves share
 // lie in LDS.
+#include "../dwc_device.h"
 #include "seq_chunk.h"
 
 namespace dwc {
@@ -64,8 +65,16 @@ struct Int {
   static constexpr int value = V;
 };
 
-template <int T, int DP>
-__global__ void __launch_bounds__(DP * 4) delta_grad(ChunkArgs c) {
+// Waves a SIMD: two workgroups a compute unit, what their LDS leaves room
+// for, where a wave's registers allow it (8x2048 tokens, 16 heads, bf16: 396
+// us with 46 spilled registers, 425 us without and half the waves).
+constexpr int waves_of(int t, int dp, bool shared) {
+  return dp == 128 && !shared && t != T_F32 ? 4 : 2;
+}
+
+// SHARED: value heads share a key head, whose gradients are their sums.
+template <int T, int DP, bool SHARED>
+__global__ void __launch_bounds__(DP * 4, waves_of(T, DP, SHARED)) delta_grad(ChunkArgs c) {
   constexpr int NP = T == T_F32 ? 2 : 1;  // pieces of an input
   // pieces of what only dk (or only the rounded part of dq) sums: a bf16
   // output needs one, 2^-12 against its own 2^-9
@@ -75,12 +84,14 @@ __global__ void __launch_bounds__(DP * 4) delta_grad(ChunkArgs c) {
   extern __shared__ __align__(16) char lds_raw[];
   __shared__ float red[4][NW];
   __shared__ float sdot[NW][kChunk], sbeta[kChunk], svdv[kChunk];
+  __shared__ __align__(16) float sinto[kChunk], sout[kChunk];
   __shared__ double sg[kChunk];
   _Float16* lds = (_Float16*)lds_raw;
   _Float16 *tdo = lds, *tdv = lds + 2 * kTile, *tu = lds + 4 * kTile;
   _Float16 *tph = lds, *tpt = lds + 2 * kTile, *tb = lds + 4 * kTile;
   const DeltaArgs& a = c.a;
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, m0 = lane & 15, q0 = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, m0 = lane & 15, q0 = lane >> 4;
+  const int w = uniform(tid >> 6);
   const int row0 = tid / NW, part0 = tid % NW;  // for whole-tile loads
   const int64_t id = blockIdx.x;
   const int hk = (int)(id % a.hk);
@@ -89,13 +100,14 @@ __global__ void __launch_bounds__(DP * 4) delta_grad(ChunkArgs c) {
   const int64_t b = bc / c.nc;
   const int64_t len = live_tokens(a, b), t0 = (int64_t)chunk * kChunk;
   const int n = (int)(len - t0 < 0 ? 0 : (len - t0 < kChunk ? len - t0 : kChunk));
-  const int per = a.hv / a.hk;
-  f32x4 dq[4], dk[4];
+  const int per = SHARED ? a.hv / a.hk : 1;
+  f32x4 dq[4], dk[4], dqs[4];  // dqs: of the heads before this one
 #pragma unroll
-  for (int i = 0; i < 4; ++i) dq[i] = dk[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < 4; ++i) dq[i] = dk[i] = dqs[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   // this wave's key dimension: 16 w + lane % 16
-  const Frag* kt = c.kt + (id * NP * (DP / 16 * 2) + w * 2) * 64 + lane;
-  const Frag* qt = c.qt + (id * NP * (DP / 16 * 2) + w * 2) * 64 + lane;
+  const Frag* kt = c.kt + (id * NP * (DP / 16 * 2) + w * 2) * 64;
+  const Frag* qt = c.qt + (id * NP * (DP / 16 * 2) + w * 2) * 64;
+  const uint32_t loff = 16 * lane;
   constexpr int PIECE = DP / 16 * 2 * 64;
 
   for (int r = 0; r < per; ++r) {
@@ -120,16 +132,22 @@ __global__ void __launch_bounds__(DP * 4) delta_grad(ChunkArgs c) {
     constexpr int BOTH = NW == 4 ? 2 : 1;
     const int wr = w & 3;
     f32x4 dp[BOTH][4];
-    float qdot[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
       for (int x = 0; x < BOTH; ++x) dp[x][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int x = 0; x < 4; ++x) qdot[i][x] = 0.f;
+      if constexpr (SHARED) {
+        dqs[i] += dq[i];
+        dq[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
     }
     for (int v0 = 0; v0 < c.dvp; v0 += 64) {
       __syncthreads();  // the tiles' readers are done
+      if (v0 == 0 && tid < kChunk) {
+        sg[tid] = gate->g[tid];
+        sinto[tid] = gate->into[tid];
+        sout[tid] = gate->out[tid];
+      }
       asm volatile("" : "+v"(m), "+v"(q), "+v"(row), "+v"(part));
       float xd[CPT], xv[CPT], xu[CPT];
       float md = 0.f, mv = 0.f, mu = 0.f;
@@ -140,26 +158,37 @@ __global__ void __launch_bounds__(DP * 4) delta_grad(ChunkArgs c) {
         const float* wp = c.dw + (hid * kChunk + row) * c.dvp + col;
         const int64_t vb = b * a.v_stride[0] + t * a.v_stride[1] + h * a.v_stride[2] + col;
         const int64_t ob = b * a.do_stride[0] + t * a.do_stride[1] + h * a.do_stride[2] + col;
+        float v[CPT];
 #pragma unroll
-        for (int i = 0; i < CPT; i += 4) {
-          f32x4 ee = {0.f, 0.f, 0.f, 0.f}, ww = ee;
-          if (col < c.dvp) {
-            ee = *(const f32x4*)(ep + i);
-            ww = *(const f32x4*)(wp + i);
-          }
+        for (int i = 0; i < CPT; ++i) xd[i] = v[i] = xv[i] = xu[i] = 0.f;
+        if (c.wide) {  // dv is a multiple of 8: eight columns are in or out
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const bool in = row < n && col + i + j < a.dv;
-            xd[i + j] = in ? load1<T>(a.dout, ob + i + j) : 0.f;
-            const float v = in ? load1<T>(a.v, vb + i + j) : 0.f;
-            xv[i + j] = beta * ww[j];
-            xu[i + j] = beta * ee[j];
-            ew = fmaf(ee[j], ww[j], ew);
-            vdv = fmaf(v, xv[i + j], vdv);
-            md = fmaxf(md, fabsf(xd[i + j]));
-            mv = fmaxf(mv, fabsf(xv[i + j]));
-            mu = fmaxf(mu, fabsf(xu[i + j]));
-          }
+          for (int i = 0; i < CPT; i += 8)
+            if (row < n && col + i < a.dv) {
+              load_vec<T, 8>(a.dout, ob + i, xd + i);
+              load_vec<T, 8>(a.v, vb + i, v + i);
+            }
+        } else {
+#pragma unroll
+          for (int i = 0; i < CPT; ++i)
+            if (row < n && col + i < a.dv) {
+              xd[i] = load1<T>(a.dout, ob + i);
+              v[i] = load1<T>(a.v, vb + i);
+            }
+        }
+        if (col < c.dvp) {
+          load_vec<T_F32, CPT>(ep, 0, xu);
+          load_vec<T_F32, CPT>(wp, 0, xv);
+        }
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) {
+          ew = fmaf(xu[i], xv[i], ew);
+          xv[i] *= beta;
+          xu[i] *= beta;
+          vdv = fmaf(v[i], xv[i], vdv);
+          md = fmaxf(md, fabsf(xd[i]));
+          mv = fmaxf(mv, fabsf(xv[i]));
+          mu = fmaxf(mu, fabsf(xu[i]));
         }
       }
       md = wave_max(md);
@@ -225,66 +254,74 @@ __global__ void __launch_bounds__(DP * 4) delta_grad(ChunkArgs c) {
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int x = 0; x < 4; ++x) sds = fmaf(s[i][x], g[i][x], sds);
-        const Scale ss = scale_of(column_max(abs_max(s)));
-        const Scale sgr = scale_of(column_max(abs_max(g)));
-        half8 fs[2][2], fg[2][2];
+        // one state after the other: fragments of both would not fit
+        {
+          const Scale ss = scale_of(column_max(abs_max(s)));
+          half8 fs[2][2];
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          to_frag<2>(s[2 * ks], s[2 * ks + 1], ss.mul, fs[ks]);
-          to_frag<2>(g[2 * ks], g[2 * ks + 1], sgr.mul, fg[ks]);
-        }
-        half8 fq[2][NP], fk[2][NP];
+          for (int ks = 0; ks < 2; ++ks) to_frag<2>(s[2 * ks], s[2 * ks + 1], ss.mul, fs[ks]);
+          const float cq = a.scale * sd.inv * ss.inv, ck = -sv.inv * ss.inv;
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
+          for (int i = 0; i < 4; ++i) {
+            // loads of later rows are not pulled ahead of this one's products
+            __builtin_amdgcn_sched_barrier(0);
+            f32x4 xq = {0.f, 0.f, 0.f, 0.f}, xk = xq;
 #pragma unroll
-          for (int y = 0; y < NP; ++y) {
-            fq[ks][y] = qt[y * PIECE + ks * 64];
-            fk[ks][y] = kt[y * PIECE + ks * 64];
+            for (int ks = 0; ks < 2; ++ks) {
+              half8 fo[NP], fv[OP];
+#pragma unroll
+              for (int y = 0; y < NP; ++y) fo[y] = frag8(tdo + y * kTile, 16 * i + m, ks, q);
+#pragma unroll
+              for (int y = 0; y < OP; ++y) fv[y] = frag8(tdv + y * kTile, 16 * i + m, ks, q);
+              xq = mfma_pieces<NP, 2>(fo, fs[ks], xq);
+              xk = mfma_pieces<OP, OP>(fv, fs[ks], xk);
+            }
+            const f32x4 into = *(const f32x4*)(sinto + 16 * i + 4 * q);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              dq[i][x] = fmaf(cq * into[x], xq[x], dq[i][x]);
+              dk[i][x] = fmaf(ck * into[x], xk[x], dk[i][x]);
+            }
           }
-        const float cq = a.scale * sd.inv * ss.inv, ck = -sv.inv * ss.inv,
-                    cu = su.inv * sgr.inv;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // loads of later rows are not pulled ahead of this one's products:
-          // all at once they would not fit the registers
-          __builtin_amdgcn_sched_barrier(0);
-          f32x4 xq = {0.f, 0.f, 0.f, 0.f}, xk = xq, xs = xq;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        {
+          const Scale sgr = scale_of(column_max(abs_max(g)));
+          half8 fg[2][2], fk[2][NP];
 #pragma unroll
           for (int ks = 0; ks < 2; ++ks) {
-            half8 fo[NP], fv[2], fu[2];
+            to_frag<2>(g[2 * ks], g[2 * ks + 1], sgr.mul, fg[ks]);
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              if (y < NP) fo[y] = frag8(tdo + y * kTile, 16 * i + m, ks, q);
-              if (y < OP) fv[y] = frag8(tdv + y * kTile, 16 * i + m, ks, q);
-              fu[y] = frag8(tu + y * kTile, 16 * i + m, ks, q);
-            }
-            xq = mfma_pieces<NP, 2>(fo, fs[ks], xq);
-            xk = mfma_pieces<OP, OP>(fv, fs[ks], xk);
-            xs = mfma_pieces<2, 2>(fu, fg[ks], xs);
+            for (int y = 0; y < NP; ++y) fk[ks][y] = at_lane(kt + y * PIECE + ks * 64, loff);
           }
-          const f32x4 into = *(const f32x4*)(gate->into + 16 * i + 4 * q);
-          const f32x4 out = *(const f32x4*)(gate->out + 16 * i + 4 * q);
+          const float cu = su.inv * sgr.inv;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            // q and k at this result's place, from their fragments
-            const int slot = (i & 1) * 4 + x;
-            float qv = (float)fq[i >> 1][0][slot], kv = (float)fk[i >> 1][0][slot];
-            if constexpr (NP == 2) {
-              qv += (float)fq[i >> 1][1][slot];
-              kv += (float)fk[i >> 1][1][slot];
+          for (int i = 0; i < 4; ++i) {
+            __builtin_amdgcn_sched_barrier(0);
+            f32x4 xs = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+              const half8 fu[2] = {frag8(tu, 16 * i + m, ks, q),
+                                   frag8(tu + kTile, 16 * i + m, ks, q)};
+              xs = mfma_pieces<2, 2>(fu, fg[ks], xs);
             }
-            const float u = cq * into[x] * xq[x], v = cu * out[x] * xs[x];
-            qdot[i][x] = fmaf(qv * qinv, u, qdot[i][x]);
-            kdk = fmaf(kv * kinv, v, kdk);
-            dq[i][x] += u;
-            dk[i][x] += fmaf(ck * into[x], xk[x], v);
+            const f32x4 out = *(const f32x4*)(sout + 16 * i + 4 * q);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              // k at this result's place, from its fragments
+              const int slot = (i & 1) * 4 + x;
+              float kv = (float)fk[i >> 1][0][slot];
+              if constexpr (NP == 2) kv += (float)fk[i >> 1][1][slot];
+              const float v = cu * out[x] * xs[x];
+              kdk = fmaf(kv * kinv, v, kdk);
+              dk[i][x] += v;
+            }
           }
         }
       }
     }
     // Ph, Ph^T and B + B^T to LDS
     asm volatile("" : "+v"(m), "+v"(q), "+v"(row), "+v"(part));
-    if (tid < kChunk) sg[tid] = gate->g[tid];
     __syncthreads();
     float mx[2] = {0.f, 0.f};
 #pragma unroll
@@ -324,22 +361,41 @@ __global__ void __launch_bounds__(DP * 4) delta_grad(ChunkArgs c) {
       const bool ph = BOTH == 2 ? y == 0 : w < 4;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
+        // four rows of a column: together in the transposes
+        half4 hi, lo;
+        const int r4 = 16 * wr + 4 * q, cc = 16 * j + m;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int rr = 16 * wr + 4 * q + i, cc = 16 * j + m;
-          _Float16 hi, lo;
-          split(dp[y][j][i] * (ph ? sp.mul : sb.mul), &hi, &lo);
-          if (ph) {
-            tph[rr * kPitch + cc] = hi;
-            tph[kTile + rr * kPitch + cc] = lo;
-            tpt[cc * kPitch + rr] = hi;
-            if constexpr (OP == 2) tpt[kTile + cc * kPitch + rr] = lo;
-          } else if (cc <= rr) {
-            tb[rr * kPitch + cc] = hi;
-            tb[cc * kPitch + rr] = hi;
+          _Float16 h, l;
+          split(dp[y][j][i] * (ph ? sp.mul : sb.mul), &h, &l);
+          hi[i] = h;
+          lo[i] = l;
+        }
+        if (ph) {
+          *(half4*)(tpt + cc * kPitch + r4) = hi;
+          if constexpr (OP == 2) *(half4*)(tpt + kTile + cc * kPitch + r4) = lo;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            tph[(r4 + i) * kPitch + cc] = hi[i];
+            tph[kTile + (r4 + i) * kPitch + cc] = lo[i];
+          }
+        } else if (j < wr) {
+          *(half4*)(tb + cc * kPitch + r4) = hi;
+          if constexpr (OP == 2) *(half4*)(tb + kTile + cc * kPitch + r4) = lo;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            tb[(r4 + i) * kPitch + cc] = hi[i];
+            if constexpr (OP == 2) tb[kTile + (r4 + i) * kPitch + cc] = lo[i];
+          }
+        } else if (j == wr) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (cc > r4 + i) continue;
+            tb[(r4 + i) * kPitch + cc] = hi[i];
+            tb[cc * kPitch + r4 + i] = hi[i];
             if constexpr (OP == 2) {
-              tb[kTile + rr * kPitch + cc] = lo;
-              tb[kTile + cc * kPitch + rr] = lo;
+              tb[kTile + (r4 + i) * kPitch + cc] = lo[i];
+              tb[kTile + cc * kPitch + r4 + i] = lo[i];
             }
           }
         }
@@ -353,8 +409,8 @@ __global__ void __launch_bounds__(DP * 4) delta_grad(ChunkArgs c) {
       for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
         for (int y = 0; y < NP; ++y) {
-          fq[ks][y] = qt[y * PIECE + ks * 64];
-          fk[ks][y] = kt[y * PIECE + ks * 64];
+          fq[ks][y] = at_lane(qt + y * PIECE + ks * 64, loff);
+          fk[ks][y] = at_lane(kt + y * PIECE + ks * 64, loff);
         }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -378,24 +434,18 @@ __global__ void __launch_bounds__(DP * 4) delta_grad(ChunkArgs c) {
         }
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
+          // q . dq of the token, from q's fragments
           const int slot = (i & 1) * 4 + x;
           float qv = (float)fq[i >> 1][0][slot];
           if constexpr (NP == 2) qv += (float)fq[i >> 1][1][slot];
-          const float u = sp.inv * kinv * xq[x];
-          qdot[i][x] = fmaf(qv * qinv, u, qdot[i][x]);
-          dq[i][x] += u;
+          dq[i][x] = fmaf(sp.inv * kinv, xq[x], dq[i][x]);
+          const float d = lane_sum<16>(qv * qinv * dq[i][x]);
+          if (m == 0) sdot[w][16 * i + 4 * q + x] = d;
           dk[i][x] += fmaf(sp.inv * qinv, xp[x], sb.inv * kinv * xb[x]);
         }
       }
     }
     // dbeta and dg
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const float d = lane_sum<16>(qdot[i][x]);
-        if (m == 0) sdot[w][16 * i + 4 * q + x] = d;
-      }
     ew = lane_sum<NW>(ew);
     vdv = lane_sum<NW>(vdv);
     if (part == 0) {
@@ -436,7 +486,7 @@ __global__ void __launch_bounds__(DP * 4) delta_grad(ChunkArgs c) {
         const int t = 16 * i + 4 * q0 + x, col = 16 * w + m0;
         if (t0 + t >= a.l || col >= a.dk) continue;
         const int64_t at = ((b * a.l + t0 + t) * a.hk + hk) * a.dk + col;
-        store1<T>(a.dq, at, t < n ? dq[i][x] : 0.f);
+        store1<T>(a.dq, at, t < n ? dqs[i][x] + dq[i][x] : 0.f);
         store1<T>(a.dk_out, at, t < n ? dk[i][x] : 0.f);
       }
 }
@@ -444,13 +494,22 @@ __global__ void __launch_bounds__(DP * 4) delta_grad(ChunkArgs c) {
 template <int T>
 void go(const ChunkArgs& c, hipStream_t st) {
   const dim3 grid((uint32_t)(c.a.b * c.nc * c.a.hk));
-  if (c.a.dk <= 64) hipLaunchKernelGGL((delta_grad<T, 64>), grid, dim3(256), kLds, st, c);
-  else hipLaunchKernelGGL((delta_grad<T, 128>), grid, dim3(512), kLds, st, c);
+  if (c.a.hv == c.a.hk) {
+    if (c.a.dk <= 64) hipLaunchKernelGGL((delta_grad<T, 64, false>), grid, dim3(256), kLds, st, c);
+    else hipLaunchKernelGGL((delta_grad<T, 128, false>), grid, dim3(512), kLds, st, c);
+  } else {
+    if (c.a.dk <= 64) hipLaunchKernelGGL((delta_grad<T, 64, true>), grid, dim3(256), kLds, st, c);
+    else hipLaunchKernelGGL((delta_grad<T, 128, true>), grid, dim3(512), kLds, st, c);
+  }
 }
 
 }  // namespace grad
 
-hipError_t launch_delta_grad(const ChunkArgs& c, hipStream_t st) {
+hipError_t launch_delta_grad(ChunkArgs c, hipStream_t st) {
+  const int64_t unit = c.a.type == T_F32 ? 4 : 8;
+  c.wide = c.a.dv % 8 == 0 && ((uintptr_t)c.a.v | (uintptr_t)c.a.dout) % 16 == 0;
+  for (int i = 0; i < 3; ++i)
+    c.wide = c.wide && c.a.v_stride[i] % unit == 0 && c.a.do_stride[i] % unit == 0;
   if (c.a.type == T_F32) grad::go<T_F32>(c, st);
   else if (c.a.type == T_BF16) grad::go<T_BF16>(c, st);
   else grad::go<T_F16>(c, st);
