@@ -62,28 +62,31 @@ __device__ __forceinline__ f32x2 row_sum2(float u, float v, float* lds) {
   }
 }
 
+// A row of x, zeros past its end and past the last row.
 template <int XT, int VEC, int LPR, int NV>
-__global__ void __launch_bounds__(LPR <= 64 ? kBlock : LPR) norm_fwd(NormArgs a) {
-  constexpr int ROWS = LPR <= 64 ? kBlock / LPR : 1;
-  __shared__ float lds[2 * (LPR <= 64 ? 1 : LPR / 64)];
-  const int lane = threadIdx.x % LPR;
-  const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / LPR;
-  const bool live = row < a.rows;  // lanes of one row agree
-  const int64_t base = row * a.x_stride;
-  float x[NV][VEC];
-  float s = 0.f;
+__device__ __forceinline__ void load_row(const NormArgs& a, int64_t row, int lane,
+                                         float (&x)[NV][VEC]) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int64_t col = (int64_t)(i * LPR + lane) * VEC;
-    if (live && col < a.c) {
-      load_vec<XT, VEC>(a.x, base + col, x[i]);
+    if (row < a.rows && col < a.c) {  // lanes of one row agree on the first
+      load_vec<XT, VEC>(a.x, row * a.x_stride + col, x[i]);
     } else {
 #pragma unroll
       for (int j = 0; j < VEC; ++j) x[i][j] = 0.f;
     }
+  }
+}
+
+template <int VEC, int LPR, int NV>
+__device__ __forceinline__ void norm_row(const NormArgs& a, int64_t row, int lane,
+                                         float (&x)[NV][VEC], float* lds) {
+  const bool live = row < a.rows;
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < VEC; ++j) s += x[i][j];
-  }
   const float c = (float)a.c;
   // divided, not multiplied by 1 / c: a constant row gives its own value back
   const float mean = row_sum<LPR>(s, lds) / c;
@@ -121,6 +124,25 @@ __global__ void __launch_bounds__(LPR <= 64 ? kBlock : LPR) norm_fwd(NormArgs a)
   }
 }
 
+// Rows a lane group takes: two where a row is one load a lane, so that twice
+// the bytes are under way (200704 rows of 128, fp32 to bf16: 27 us, 29 us
+// one at a time).
+template <int NV>
+constexpr int kRows = NV == 1 ? 2 : 1;
+
+template <int XT, int VEC, int LPR, int NV>
+__global__ void __launch_bounds__(LPR <= 64 ? kBlock : LPR) norm_fwd(NormArgs a) {
+  constexpr int ROWS = LPR <= 64 ? kBlock / LPR : 1, U = kRows<NV>;
+  __shared__ float lds[2 * (LPR <= 64 ? 1 : LPR / 64)];
+  const int lane = threadIdx.x % LPR;
+  const int64_t row = (int64_t)blockIdx.x * ROWS * U + threadIdx.x / LPR;
+  float x[U][NV][VEC];
+#pragma unroll
+  for (int u = 0; u < U; ++u) load_row<XT, VEC, LPR, NV>(a, row + u * ROWS, lane, x[u]);
+#pragma unroll
+  for (int u = 0; u < U; ++u) norm_row<VEC, LPR, NV>(a, row + u * ROWS, lane, x[u], lds);
+}
+
 // Each group of LPR lanes walks rows group, group + groups * ROWS, ... and
 // keeps its columns' sums of dy h and dy in registers; a workgroup's row
 // groups are joined in LDS in a fixed order and the workgroups' partials by
@@ -144,26 +166,43 @@ __global__ void __launch_bounds__(LPR <= 64 ? kBlock : LPR) norm_bwd(NormArgs a)
   }
   const float inv_c = 1.0f / (float)a.c;
   const int64_t steps = (a.rows + (int64_t)a.groups * ROWS - 1) / ((int64_t)a.groups * ROWS);
-  for (int64_t it = 0; it < steps; ++it) {
-    const int64_t row = (it * a.groups + blockIdx.x) * ROWS + sub;
+  // the next row is read before this one's sums are made
+  float xn[NV][VEC], en[NV][VEC], mean_n, rstd_n;
+  const auto fetch = [&](int64_t row) {
     const bool live = row < a.rows;
-    const float mean = live ? a.mean[row] : 0.f, rstd = live ? a.rstd[row] : 0.f;
-    float h[NV][VEC], e[NV][VEC];
-    float se = 0.f, sh = 0.f;
+    mean_n = live ? a.mean[row] : 0.f;
+    rstd_n = live ? a.rstd[row] : 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int64_t col = (int64_t)(i * LPR + lane) * VEC;
       if (live && col < a.c) {
-        load_vec<XT, VEC>(a.x, row * a.x_stride + col, h[i]);
-        load_any<VEC>(a.y_type, a.dy, row * a.dy_stride + col, e[i]);
+        load_vec<XT, VEC>(a.x, row * a.x_stride + col, xn[i]);
+        load_any<VEC>(a.y_type, a.dy, row * a.dy_stride + col, en[i]);
       } else {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-          h[i][j] = mean;
-          e[i][j] = 0.f;
+          xn[i][j] = mean_n;
+          en[i][j] = 0.f;
         }
       }
     }
+  };
+  fetch((int64_t)blockIdx.x * ROWS + sub);
+  for (int64_t it = 0; it < steps; ++it) {
+    const int64_t row = (it * a.groups + blockIdx.x) * ROWS + sub;
+    const bool live = row < a.rows;
+    const float mean = mean_n, rstd = rstd_n;
+    float h[NV][VEC], e[NV][VEC];
+    float se = 0.f, sh = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        h[i][j] = xn[i][j];
+        e[i][j] = en[i][j];
+      }
+    // (a wide row's registers are taken)
+    if constexpr (NV * VEC <= 8) fetch(row + (int64_t)a.groups * ROWS);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
@@ -188,6 +227,7 @@ __global__ void __launch_bounds__(LPR <= 64 ? kBlock : LPR) norm_bwd(NormArgs a)
         store_vec<XT, VEC>(a.y, row * a.c + col, e[i]);
       }
     }
+    if constexpr (NV * VEC > 8) fetch(row + (int64_t)a.groups * ROWS);
   }
   float* part = a.part + (int64_t)blockIdx.x * 2 * a.c;
 #pragma unroll
@@ -292,24 +332,24 @@ __global__ void __launch_bounds__(kBlock) norm_cols_long(NormArgs a) {
   part[a.c + c] = db;
 }
 
-// dw, db from the partials: 32 columns x 32 slices of the groups a
+// dw, db from the partials: 16 columns x 64 slices of the groups a
 // workgroup, each slice's sum in order, the slices' sums in order.
 __global__ void __launch_bounds__(1024) norm_reduce(const float* part, float* dw, float* db,
                                                     int64_t c, int groups) {
-  __shared__ float lds[32][33];
-  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-  const int64_t col = (int64_t)blockIdx.x * 32 + lane;
+  __shared__ float lds[64][17];
+  const int lane = threadIdx.x & 15, slice = threadIdx.x >> 4;
+  const int64_t col = (int64_t)blockIdx.x * 16 + lane;
   float s = 0.f;
   if (col < 2 * c) {
 #pragma unroll 8
-    for (int g = slice; g < groups; g += 32) s += part[(int64_t)g * 2 * c + col];
+    for (int g = slice; g < groups; g += 64) s += part[(int64_t)g * 2 * c + col];
   }
   lds[slice][lane] = s;
   __syncthreads();
   if (slice == 0 && col < 2 * c) {
     s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) s += lds[i][lane];
+    for (int i = 0; i < 64; ++i) s += lds[i][lane];
     float* out = col < c ? dw : db;
     if (out) out[col < c ? col : col - c] = s;
   }
@@ -359,7 +399,7 @@ namespace norm {
 template <int XT, int VEC, int LPR, int NV>
 void go(bool bwd, const NormArgs& a, hipStream_t st) {
   constexpr int block = LPR <= 64 ? kBlock : LPR;
-  constexpr int rows = block / LPR;
+  constexpr int rows = block / LPR * kRows<NV>;
   if (bwd)
     hipLaunchKernelGGL((norm_bwd<XT, VEC, LPR, NV>), dim3(a.groups), dim3(block), 0, st, a);
   else
@@ -440,7 +480,7 @@ hipError_t launch_norm_bwd(const NormArgs& a, float* dw, float* db, hipStream_t 
     if (e != hipSuccess) return e;
   }
   if (dw || db)
-    hipLaunchKernelGGL(norm_reduce, dim3((uint32_t)((2 * a.c + 31) / 32)), dim3(1024), 0, st,
+    hipLaunchKernelGGL(norm_reduce, dim3((uint32_t)((2 * a.c + 15) / 16)), dim3(1024), 0, st,
                        a.part, dw, db, a.c, a.rows > 0 ? a.groups : 0);
   return hipGetLastError();
 }
