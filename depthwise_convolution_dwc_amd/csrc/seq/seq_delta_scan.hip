@@ -81,21 +81,33 @@ __device__ __forceinline__ void publish(Block* blk, const f32x4& t0, const f32x4
 
 __device__ __forceinline__ float abs_max2(const f32x4 (&v)[2]) { return abs_max(v); }
 
+// The blocks of two waves that share columns.
+template <int KS, int NT, bool BWD>
+struct Blocks {
+  Block bs[NT][KS], by[NT][2], bu[NT][2], bo[BWD ? 1 : NT][2];
+};
+template <int KS, int NT>
+struct BlocksBack {
+  Block bs[NT][KS], by[NT][2], bu[NT][2], bo[NT][2], bd[NT][2];
+};
+
 // What both kernels know of their place.
 struct Place {
   int64_t b, head;
   int h, hk, block, col0;  // block: the first column, col0: this lane's
 };
 
-template <int NT>
+template <int NT, int NC>
 __device__ __forceinline__ Place place_of(const ChunkArgs& c) {
   Place p;
   const DeltaArgs& a = c.a;
-  const int groups = (c.dvp / 16 + NT - 1) / NT;
+  const int groups = (c.dvp / 16 + NT * NC - 1) / (NT * NC);
   // the workgroups of one head read the same fragments: on one XCD's L2
   const int id = xcd_logical_block((int)blockIdx.x, (int)gridDim.x);
   p.head = id / groups;
-  p.block = (int)(id - p.head * groups) * 16 * NT;
+  // (past dvp for the last pair of waves of an odd number of blocks, which
+  // then only keeps the exchanges company)
+  p.block = ((int)(id - p.head * groups) * NC + uniform((int)threadIdx.x >> 7)) * 16 * NT;
   p.col0 = p.block + (threadIdx.x & 15);
   p.b = p.head / a.hv;
   p.h = (int)(p.head - p.b * a.hv);
@@ -186,15 +198,17 @@ __device__ __forceinline__ void store_tile(float* matrix, int row0, int dvp, uin
     *(float*)((char*)(matrix + (int64_t)(row0 + r) * dvp) + offset) = v[r];
 }
 
-template <int T, int DP, int NT, bool BWD>
-__global__ void __launch_bounds__(128) delta_scan(ChunkArgs c) {
+// NT: 16-column blocks of a wave.  NC: pairs of waves of a workgroup.
+template <int T, int DP, int NT, int NC, bool BWD>
+__global__ void __launch_bounds__(128 * NC) delta_scan(ChunkArgs c) {
   constexpr int NP = T == T_F32 ? 2 : 1, OP = T == T_BF16 ? 1 : 2;
   constexpr int KS = DP / 32, MT = DP / 16, MW = MT / 2;
   typedef Raw<T> R;
-  __shared__ Block bs[NT][KS], by[NT][2], bu[NT][2], bo[BWD ? 1 : NT][2];
+  extern __shared__ __align__(16) char lds[];
+  auto& [bs, by, bu, bo] = ((Blocks<KS, NT, BWD>*)lds)[uniform((int)threadIdx.x >> 7)];
   const DeltaArgs& a = c.a;
-  const Place p = place_of<NT>(c);
-  const int lane = threadIdx.x & 63, hf = uniform((int)threadIdx.x >> 6);
+  const Place p = place_of<NT, NC>(c);
+  const int lane = threadIdx.x & 63, hf = uniform((int)threadIdx.x >> 6) & 1;
   const int m = lane & 15, q = lane >> 4;
   const int64_t len = live_tokens(a, p.b);
   const int chunks = (int)((len + kChunk - 1) / kChunk);
@@ -444,15 +458,16 @@ __global__ void __launch_bounds__(128) delta_scan(ChunkArgs c) {
 //   dU = P^T dO + exp(G_64 - G) o (K dS),   W = dU - X^T (beta o dU),
 //   dV = beta o W,
 //   dS <- exp(G_64) dS + Q^T (scale exp(G) o dO) - K^T (exp(G) o dV).
-template <int T, int DP, int NT>
-__global__ void __launch_bounds__(128) delta_scan_bwd(ChunkArgs c) {
+template <int T, int DP, int NT, int NC>
+__global__ void __launch_bounds__(128 * NC) delta_scan_bwd(ChunkArgs c) {
   constexpr int NP = T == T_F32 ? 2 : 1;
   constexpr int KS = DP / 32, MT = DP / 16, MW = MT / 2;
   typedef Raw<T> R;
-  __shared__ Block bs[NT][KS], by[NT][2], bu[NT][2], bo[NT][2], bd[NT][2];
+  extern __shared__ __align__(16) char lds[];
+  auto& [bs, by, bu, bo, bd] = ((BlocksBack<KS, NT>*)lds)[uniform((int)threadIdx.x >> 7)];
   const DeltaArgs& a = c.a;
-  const Place p = place_of<NT>(c);
-  const int lane = threadIdx.x & 63, hf = uniform((int)threadIdx.x >> 6);
+  const Place p = place_of<NT, NC>(c);
+  const int lane = threadIdx.x & 63, hf = uniform((int)threadIdx.x >> 6) & 1;
   const int m = lane & 15, q = lane >> 4;
   const int64_t len = live_tokens(a, p.b);
   const int chunks = (int)((len + kChunk - 1) / kChunk);
@@ -666,37 +681,47 @@ __global__ void __launch_bounds__(128) delta_scan_bwd(ChunkArgs c) {
   }
 }
 
-template <int T, int DP, int NT>
-void go_nt(const ChunkArgs& c, int what, hipStream_t st) {
-  const int groups = (c.dvp / 16 + NT - 1) / NT;
-  const dim3 grid((uint32_t)(c.a.b * c.a.hv * groups)), block(128);
-  if (what == 0) hipLaunchKernelGGL((delta_scan<T, DP, NT, false>), grid, block, 0, st, c);
-  else if (what == 1) hipLaunchKernelGGL((delta_scan<T, DP, NT, true>), grid, block, 0, st, c);
-  else hipLaunchKernelGGL((delta_scan_bwd<T, DP, NT>), grid, block, 0, st, c);
+template <int T, int DP, int NT, int NC>
+hipError_t go_nt(const ChunkArgs& c, int what, hipStream_t st) {
+  constexpr int KS = DP / 32;
+  const int groups = (c.dvp / 16 + NT * NC - 1) / (NT * NC);
+  const dim3 grid((uint32_t)(c.a.b * c.a.hv * groups)), block(128 * NC);
+  auto* f = what == 0   ? &delta_scan<T, DP, NT, NC, false>
+            : what == 1 ? &delta_scan<T, DP, NT, NC, true>
+                        : &delta_scan_bwd<T, DP, NT, NC>;
+  const int bytes = NC * (int)(what == 0   ? sizeof(Blocks<KS, NT, false>)
+                               : what == 1 ? sizeof(Blocks<KS, NT, true>)
+                                           : sizeof(BlocksBack<KS, NT>));
+  if (bytes > 64 * 1024) {  // more than a launch may ask for unasked
+    const hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void*>(f),
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (err != hipSuccess) return err;
+  }
+  hipLaunchKernelGGL(f, grid, block, bytes, st, c);
+  return hipGetLastError();
 }
 
 template <int T, int DP>
-void go(const ChunkArgs& c, int what, hipStream_t st) {
-  // 32 columns a workgroup read each fragment half as often; 16 columns give
-  // twice the workgroups, which few heads need to reach the compute units
-  // (and fp32 fragments of 128 dimensions leave no registers for 32)
+hipError_t go(const ChunkArgs& c, int what, hipStream_t st) {
+  // 32 columns a wave and two pairs a workgroup read each fragment from L2 a
+  // quarter as often; one pair of 16 columns gives four times the workgroups,
+  // which few heads need to reach the compute units (and fp32 fragments of
+  // 128 dimensions leave no registers for 32)
   if constexpr (T != T_F32 || DP == 64) {
-    if (c.a.b * c.a.hv * (c.dvp / 16) > 512) return go_nt<T, DP, 2>(c, what, st);
+    if (c.a.b * c.a.hv * (c.dvp / 16) > 512) return go_nt<T, DP, 2, 2>(c, what, st);
   }
-  go_nt<T, DP, 1>(c, what, st);
+  return go_nt<T, DP, 1, 1>(c, what, st);
 }
 
 template <int T>
-void go_dp(const ChunkArgs& c, int what, hipStream_t st) {
-  if (c.a.dk <= 64) go<T, 64>(c, what, st);
-  else go<T, 128>(c, what, st);
+hipError_t go_dp(const ChunkArgs& c, int what, hipStream_t st) {
+  return c.a.dk <= 64 ? go<T, 64>(c, what, st) : go<T, 128>(c, what, st);
 }
 
 inline hipError_t go_type(const ChunkArgs& c, int what, hipStream_t st) {
-  if (c.a.type == T_F32) go_dp<T_F32>(c, what, st);
-  else if (c.a.type == T_BF16) go_dp<T_BF16>(c, what, st);
-  else go_dp<T_F16>(c, what, st);
-  return hipGetLastError();
+  if (c.a.type == T_F32) return go_dp<T_F32>(c, what, st);
+  if (c.a.type == T_BF16) return go_dp<T_BF16>(c, what, st);
+  return go_dp<T_F16>(c, what, st);
 }
 
 }  // namespace scan
