@@ -116,6 +116,10 @@ int check_delta(const dwc_delta_problem* p, int max_dk) {
   if (p->hv > 65536 || p->l > ((int64_t)1 << 30) || p->b > 65535 ||
       p->b * p->hv > ((int64_t)1 << 17) || p->b * p->hv * ((p->l + 63) / 64) > ((int64_t)1 << 24) - 1)
     return fail(DWC_ERR_UNSUPPORTED, "delta rule sizes past the launch range");
+  // up to 512 threads for 64 tokens of a head, up to 256 for 16 of its columns
+  if (max_dk == 128 && (p->b * p->hv * ((p->l + 63) / 64) >= ((int64_t)1 << 23) ||
+                        p->b * p->hv * (((int64_t)p->dv + 15) / 16) >= ((int64_t)1 << 24)))
+    return fail(DWC_ERR_UNSUPPORTED, "delta rule sizes past the launch range");
   return DWC_OK;
 }
 
@@ -438,12 +442,11 @@ int dwc_delta_bwd(const dwc_delta_problem* p, const void* dout, const float* ds1
   hipError_t err = hipSuccess;
   delta_layout(p, true, (char*)workspace, &c);
   if (p->l == 0) {  // the state passes through, and its gradient
-    if (ds0) err = launch_delta_scan_bwd(c, hs);
+    if (ds0) err = launch_delta_scan(c, true, hs);
     return hip_result(err, "dwc_delta_bwd launch");
   }
   err = launch_delta_prep(c, true, hs);
   if (err == hipSuccess) err = launch_delta_scan(c, true, hs);
-  if (err == hipSuccess) err = launch_delta_scan_bwd(c, hs);
   if (err == hipSuccess) err = launch_delta_grad(c, hs);
   return hip_result(err, "dwc_delta_bwd launch");
 }

@@ -166,10 +166,9 @@ __device__ __forceinline__ float abs_max(const f32x4 (&v)[N]) {
 }
 
 hipError_t launch_delta_prep(const ChunkArgs& c, bool bwd, hipStream_t st);
-// Chunk by chunk: o and s1, or (bwd) the state before each chunk and E.
+// Chunk by chunk: o and s1, or (bwd) the state before each chunk and E, and
+// back from the last chunk dv, the state's gradient after each chunk and dw.
 hipError_t launch_delta_scan(const ChunkArgs& c, bool bwd, hipStream_t st);
-// Back from the last chunk: dv, the state's gradient after each chunk, dw.
-hipError_t launch_delta_scan_bwd(const ChunkArgs& c, hipStream_t st);
 // dq, dk, dg, dbeta of each chunk.
 hipError_t launch_delta_grad(ChunkArgs c, hipStream_t st);
 

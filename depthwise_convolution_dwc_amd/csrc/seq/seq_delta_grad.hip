@@ -16,6 +16,10 @@
 // columns.  A wave owns 16 key dimensions of dQ and dK, so the states go from
 // memory to exactly one wave's registers; the operands that all waves share
 // lie in LDS.
+//
+// Bound: waits.  MI355X, 8x2048 tokens of 16 heads, 128x128 states, bf16: 396
+// us; moving its 0.8 GB would take 165 us, vector instructions keep a SIMD
+// busy 42% of the time, matrix ones 8%.
 #include "../dwc_device.h"
 #include "seq_chunk.h"
 

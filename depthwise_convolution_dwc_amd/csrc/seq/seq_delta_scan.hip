@@ -12,14 +12,19 @@
 // refilled for the next chunk as soon as this chunk is done with it, so that
 // no exchange waits for memory.
 //
-// Bound: the chain of products and exchanges of a chunk, about 3000 cycles,
-// times the chunks of the longest sequence.
+// Bound: the chain of products and exchanges of a chunk (a wave issues half
+// of its cycles, three quarters of that vector instructions, 13% matrix
+// ones), times the chunks of the longest sequence.  MI355X, 128x128 states,
+// bf16: 2.5 us a chunk at one workgroup a compute unit (4096 tokens of 32
+// heads: 162 us), 6 us where every SIMD has a wave with 32 columns (8x2048
+// tokens of 16 heads: 193 us; with every load and store at the first chunk,
+// 170 us).
 #include "../dwc_device.h"
 #include "seq_chunk.h"
 
 namespace dwc {
 namespace seq {
-namespace scan {
+namespace scans {
 
 // The 4 fp32 values of rows 16 i + 4 q .. + 3.
 __device__ __forceinline__ f32x4 row4(const float* p, int i, int q) {
@@ -98,12 +103,12 @@ struct Place {
 };
 
 template <int NT, int NC>
-__device__ __forceinline__ Place place_of(const ChunkArgs& c) {
+__device__ __forceinline__ Place place_of(const ChunkArgs& c, int block, int blocks) {
   Place p;
   const DeltaArgs& a = c.a;
   const int groups = (c.dvp / 16 + NT * NC - 1) / (NT * NC);
   // the workgroups of one head read the same fragments: on one XCD's L2
-  const int id = xcd_logical_block((int)blockIdx.x, (int)gridDim.x);
+  const int id = xcd_logical_block(block, blocks);
   p.head = id / groups;
   // (past dvp for the last pair of waves of an odd number of blocks, which
   // then only keeps the exchanges company)
@@ -199,15 +204,15 @@ __device__ __forceinline__ void store_tile(float* matrix, int row0, int dvp, uin
 }
 
 // NT: 16-column blocks of a wave.  NC: pairs of waves of a workgroup.
+// block of blocks: the workgroup's number among those of its kind.
 template <int T, int DP, int NT, int NC, bool BWD>
-__global__ void __launch_bounds__(128 * NC) delta_scan(ChunkArgs c) {
+__device__ __forceinline__ void scan(const ChunkArgs& c, int block, int blocks, char* lds) {
   constexpr int NP = T == T_F32 ? 2 : 1, OP = T == T_BF16 ? 1 : 2;
   constexpr int KS = DP / 32, MT = DP / 16, MW = MT / 2;
   typedef Raw<T> R;
-  extern __shared__ __align__(16) char lds[];
   auto& [bs, by, bu, bo] = ((Blocks<KS, NT, BWD>*)lds)[uniform((int)threadIdx.x >> 7)];
   const DeltaArgs& a = c.a;
-  const Place p = place_of<NT, NC>(c);
+  const Place p = place_of<NT, NC>(c, block, blocks);
   const int lane = threadIdx.x & 63, hf = uniform((int)threadIdx.x >> 6) & 1;
   const int m = lane & 15, q = lane >> 4;
   const int64_t len = live_tokens(a, p.b);
@@ -459,14 +464,13 @@ __global__ void __launch_bounds__(128 * NC) delta_scan(ChunkArgs c) {
 //   dV = beta o W,
 //   dS <- exp(G_64) dS + Q^T (scale exp(G) o dO) - K^T (exp(G) o dV).
 template <int T, int DP, int NT, int NC>
-__global__ void __launch_bounds__(128 * NC) delta_scan_bwd(ChunkArgs c) {
+__device__ __forceinline__ void scan_back(const ChunkArgs& c, int block, int blocks, char* lds) {
   constexpr int NP = T == T_F32 ? 2 : 1;
   constexpr int KS = DP / 32, MT = DP / 16, MW = MT / 2;
   typedef Raw<T> R;
-  extern __shared__ __align__(16) char lds[];
   auto& [bs, by, bu, bo, bd] = ((BlocksBack<KS, NT>*)lds)[uniform((int)threadIdx.x >> 7)];
   const DeltaArgs& a = c.a;
-  const Place p = place_of<NT, NC>(c);
+  const Place p = place_of<NT, NC>(c, block, blocks);
   const int lane = threadIdx.x & 63, hf = uniform((int)threadIdx.x >> 6) & 1;
   const int m = lane & 15, q = lane >> 4;
   const int64_t len = live_tokens(a, p.b);
@@ -682,16 +686,33 @@ __global__ void __launch_bounds__(128 * NC) delta_scan_bwd(ChunkArgs c) {
 }
 
 template <int T, int DP, int NT, int NC>
-hipError_t go_nt(const ChunkArgs& c, int what, hipStream_t st) {
+__global__ void __launch_bounds__(128 * NC) delta_scan(ChunkArgs c) {
+  extern __shared__ __align__(16) char lds[];
+  scan<T, DP, NT, NC, false>(c, (int)blockIdx.x, (int)gridDim.x, lds);
+}
+
+// The states again and their gradients: neither needs the other, so half of
+// the workgroups do the one and half the other, which few heads leave room
+// for (2x700 tokens of 8 heads, 64x64, fp32: 26 + 36 us one after the other,
+// 38 us together; 8x2048 tokens of 16 heads, bf16, fill the device with either:
+// 215 + 290 us, 510 us together).
+template <int T, int DP, int NT, int NC>
+__global__ void __launch_bounds__(128 * NC) delta_scan_bwd(ChunkArgs c) {
+  extern __shared__ __align__(16) char lds[];
+  const int blocks = (int)(gridDim.x / 2), block = (int)blockIdx.x;
+  if (block < blocks) scan_back<T, DP, NT, NC>(c, block, blocks, lds);
+  else scan<T, DP, NT, NC, true>(c, block - blocks, blocks, lds);
+}
+
+template <int T, int DP, int NT, int NC>
+hipError_t go_nt(const ChunkArgs& c, bool bwd, hipStream_t st) {
   constexpr int KS = DP / 32;
   const int groups = (c.dvp / 16 + NT * NC - 1) / (NT * NC);
-  const dim3 grid((uint32_t)(c.a.b * c.a.hv * groups)), block(128 * NC);
-  auto* f = what == 0   ? &delta_scan<T, DP, NT, NC, false>
-            : what == 1 ? &delta_scan<T, DP, NT, NC, true>
-                        : &delta_scan_bwd<T, DP, NT, NC>;
-  const int bytes = NC * (int)(what == 0   ? sizeof(Blocks<KS, NT, false>)
-                               : what == 1 ? sizeof(Blocks<KS, NT, true>)
-                                           : sizeof(BlocksBack<KS, NT>));
+  const dim3 grid((uint32_t)(c.a.b * c.a.hv * groups * (bwd ? 2 : 1))), block(128 * NC);
+  auto* f = bwd ? &delta_scan_bwd<T, DP, NT, NC> : &delta_scan<T, DP, NT, NC>;
+  // (what a backward scan keeps is more than what recomputed states need)
+  const int bytes =
+      NC * (int)(bwd ? sizeof(BlocksBack<KS, NT>) : sizeof(Blocks<KS, NT, false>));
   if (bytes > 64 * 1024) {  // more than a launch may ask for unasked
     const hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void*>(f),
                                                hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -702,36 +723,33 @@ hipError_t go_nt(const ChunkArgs& c, int what, hipStream_t st) {
 }
 
 template <int T, int DP>
-hipError_t go(const ChunkArgs& c, int what, hipStream_t st) {
+hipError_t go(const ChunkArgs& c, bool bwd, hipStream_t st) {
   // 32 columns a wave and two pairs a workgroup read each fragment from L2 a
-  // quarter as often; one pair of 16 columns gives four times the workgroups,
-  // which few heads need to reach the compute units (and fp32 fragments of
-  // 128 dimensions leave no registers for 32)
+  // quarter as often (8x2048 tokens of 16 heads: states again in 215 us, 235
+  // with one pair, 265 with 16 columns); one pair of 16 columns gives four
+  // times the workgroups, which few heads need to reach the compute units
+  // (and fp32 fragments of 128 dimensions leave no registers for 32)
   if constexpr (T != T_F32 || DP == 64) {
-    if (c.a.b * c.a.hv * (c.dvp / 16) > 512) return go_nt<T, DP, 2, 2>(c, what, st);
+    if (c.a.b * c.a.hv * (c.dvp / 16) > 512) return go_nt<T, DP, 2, 2>(c, bwd, st);
   }
-  return go_nt<T, DP, 1, 1>(c, what, st);
+  return go_nt<T, DP, 1, 1>(c, bwd, st);
 }
 
 template <int T>
-hipError_t go_dp(const ChunkArgs& c, int what, hipStream_t st) {
-  return c.a.dk <= 64 ? go<T, 64>(c, what, st) : go<T, 128>(c, what, st);
+hipError_t go_dp(const ChunkArgs& c, bool bwd, hipStream_t st) {
+  return c.a.dk <= 64 ? go<T, 64>(c, bwd, st) : go<T, 128>(c, bwd, st);
 }
 
-inline hipError_t go_type(const ChunkArgs& c, int what, hipStream_t st) {
-  if (c.a.type == T_F32) return go_dp<T_F32>(c, what, st);
-  if (c.a.type == T_BF16) return go_dp<T_BF16>(c, what, st);
-  return go_dp<T_F16>(c, what, st);
+inline hipError_t go_type(const ChunkArgs& c, bool bwd, hipStream_t st) {
+  if (c.a.type == T_F32) return go_dp<T_F32>(c, bwd, st);
+  if (c.a.type == T_BF16) return go_dp<T_BF16>(c, bwd, st);
+  return go_dp<T_F16>(c, bwd, st);
 }
 
-}  // namespace scan
+}  // namespace scans
 
 hipError_t launch_delta_scan(const ChunkArgs& c, bool bwd, hipStream_t st) {
-  return scan::go_type(c, bwd ? 1 : 0, st);
-}
-
-hipError_t launch_delta_scan_bwd(const ChunkArgs& c, hipStream_t st) {
-  return scan::go_type(c, 2, st);
+  return scans::go_type(c, bwd, st);
 }
 
 }  // namespace seq

@@ -7,7 +7,9 @@
 // in registers, CL lanes across (16 bytes each) and 64 / CL groups of RPL
 // rows down, so tokens need no barrier and waves nothing of each other, and a
 // lane's part of q and k is contiguous.  Bound for one
-// token of many sequences: memory, the state read and written once.
+// token of many sequences: memory, the state read and written once (128
+// sequences of 32 heads, 128x128: 94 us, 5.7 TB/s); for one sequence the
+// latency of its loads (8 heads: 5 us).
 #include "seq_delta.h"
 #include "seq_device.h"
 

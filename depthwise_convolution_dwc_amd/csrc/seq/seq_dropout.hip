@@ -9,7 +9,8 @@
 //
 // Bound: memory.  A thread makes the words of 8 elements of 16 bits (4 of
 // 32), which is one 16-byte load and store a stream; the 7 rounds cost 14
-// wide integer products per 4 elements, which the loads hide.
+// wide integer products per 4 elements, which the loads hide.  MI355X, 51.4M
+// bf16: with a residual 57 us (5.4 TB/s), without 34 us (6.0 TB/s).
 #include "seq_device.h"
 #include "seq_launch.h"
 

@@ -11,7 +11,9 @@
 // differences from it, which loses nothing to cancellation the way
 // mean(x^2) - m^2 does.  LPR lanes share a row; 8 to 64 of them lie inside a
 // wave, so short rows leave no lane idle, and rows past 64 * VEC * NV
-// elements take a whole workgroup.
+// elements take a whole workgroup.  MI355X: 200704 rows of 128, fp32 to bf16,
+// in 27 us (5.7 TB/s); 100352 rows of 512, bf16, there in 35 us (5.9 TB/s) and
+// back in 56 us (5.5 TB/s) and 5 us for the partials.
 #include "seq_device.h"
 #include "seq_launch.h"
 

@@ -198,3 +198,12 @@ def test_delta_chunked_pointers_refused():
             assert call(s1=at(names.index("s0"))) == ALIAS
         assert call(p=delta(q=(-4, 1, 1))) == BAD
         assert call(p=delta(b=0)) == 0
+
+
+@pytest.mark.parametrize("change", [dict(b=4096, hk=16, hv=16, l=64 * 128),
+                                    dict(b=65535, hk=2, hv=2, dv=4096)])
+def test_delta_chunked_launch_range(change):
+    need = ctypes.c_size_t()
+    p = delta(**change)
+    f = dwc.lib().dwc_delta_workspace_size
+    assert [f(ctypes.byref(p), op, ctypes.byref(need)) for op in (0, 1)] == [UNSUPPORTED] * 2
