@@ -9,15 +9,18 @@
 // blocks that one wave owns whole, so a block's scale needs no other wave,
 // and the blocks go through LDS (three exchanges a chunk).  The fragments on
 // the left are each wave's own: they go from memory to registers, each
-// refilled for the next chunk as soon as this chunk is done with it, so that
-// no exchange waits for memory.
+// refilled for the next chunk once this chunk is done with it, so that no
+// exchange waits for memory.  (Issued before an exchange they hold up the
+// wave's partner, after it the products that follow: forward the former is
+// faster, 194 against 207 us at 8x2048 tokens of 16 heads; beside the stores
+// of the backward scans the latter, 455 against 505 us.)
 //
 // Bound: the chain of products and exchanges of a chunk (a wave issues half
 // of its cycles, three quarters of that vector instructions, 13% matrix
 // ones), times the chunks of the longest sequence.  MI355X, 128x128 states,
 // bf16: 2.5 us a chunk at one workgroup a compute unit (4096 tokens of 32
-// heads: 162 us), 6 us where every SIMD has a wave with 32 columns (8x2048
-// tokens of 16 heads: 193 us; with every load and store at the first chunk,
+// heads: 164 us), 6 us where every SIMD has a wave with 32 columns (8x2048
+// tokens of 16 heads: 194 us; with every load and store at the first chunk,
 // 170 us).
 #include "../dwc_device.h"
 #include "seq_chunk.h"
@@ -379,8 +382,9 @@ __device__ __forceinline__ void scan(const ChunkArgs& c, int block, int blocks, 
       for (int x = 0; x < 2; ++x) u[nt][x] *= gt.out[x];
       publish<2>(&bu[nt][hf], u[nt][0], u[nt][1], scale_of(column_max(abs_max2(u[nt]))), lane);
     }
-    load_tri(xa, c.xa, 2, next);
-    if constexpr (BWD) {
+    if constexpr (!BWD) {
+      load_tri(xa, c.xa, 2, next);
+    } else {
       // what the gradient needs of this chunk
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -397,6 +401,7 @@ __device__ __forceinline__ void scan(const ChunkArgs& c, int block, int blocks, 
     }
     exchange();
     // S <- exp(G_64) S + K^T (exp(G_64 - G) o U)
+    if constexpr (BWD) load_tri(xa, c.xa, 2, next);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       half8 f[2][2];
@@ -596,8 +601,6 @@ __device__ __forceinline__ void scan_back(const ChunkArgs& c, int block, int blo
       }
       publish<2>(&by[nt][hf], y[nt][0], y[nt][1], scale_of(column_max(abs_max2(y[nt]))), lane);
     }
-    load_ka(next);
-    load_tri(pt, c.pt, next);
     // the state's gradient after this chunk, while the exchange is under way
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -609,6 +612,8 @@ __device__ __forceinline__ void scan_back(const ChunkArgs& c, int block, int blo
     }
     exchange();
     f32x4 g[NT][2];
+    load_ka(next);
+    load_tri(pt, c.pt, next);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       f32x4 acc[2][2] = {};
@@ -638,8 +643,8 @@ __device__ __forceinline__ void scan_back(const ChunkArgs& c, int block, int blo
       publish<2>(&bo[nt][hf], d[nt][0], d[nt][1], ys, lane);
     }
     rows_dv.store(g, chunk, len, a.l, whole, ok, hf, q);
-    load_tri(xt, c.xt, next);
     exchange();
+    load_tri(xt, c.xt, next);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       half8 f[2][2], g[2][2];
@@ -693,9 +698,8 @@ __global__ void __launch_bounds__(128 * NC) delta_scan(ChunkArgs c) {
 
 // The states again and their gradients: neither needs the other, so half of
 // the workgroups do the one and half the other, which few heads leave room
-// for (2x700 tokens of 8 heads, 64x64, fp32: 26 + 36 us one after the other,
-// 38 us together; 8x2048 tokens of 16 heads, bf16, fill the device with either:
-// 215 + 290 us, 510 us together).
+// for (2x700 tokens of 8 heads, 64x64, fp32: 36 us together, 26 + 36 one after
+// the other; 8x2048 tokens of 16 heads, bf16, fill the device with either).
 template <int T, int DP, int NT, int NC>
 __global__ void __launch_bounds__(128 * NC) delta_scan_bwd(ChunkArgs c) {
   extern __shared__ __align__(16) char lds[];
