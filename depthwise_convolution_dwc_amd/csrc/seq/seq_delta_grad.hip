@@ -17,9 +17,10 @@
 // memory to exactly one wave's registers; the operands that all waves share
 // lie in LDS.
 //
-// Bound: waits.  MI355X, 8x2048 tokens of 16 heads, 128x128 states, bf16: 396
-// us; moving its 0.8 GB would take 165 us, vector instructions keep a SIMD
-// busy 42% of the time, matrix ones 8%.
+// Bound: waits, at two waves a SIMD.  MI355X, 8x2048 tokens of 16 heads,
+// 128x128 states, bf16: 446 us; moving its 0.8 GB would take 165 us.  Twice
+// the waves took 396 us, with registers spilled to memory, which no kernel
+// here does.
 #include "../dwc_device.h"
 #include "seq_chunk.h"
 
@@ -69,16 +70,12 @@ struct Int {
   static constexpr int value = V;
 };
 
-// Waves a SIMD: two workgroups a compute unit, what their LDS leaves room
-// for, where a wave's registers allow it (8x2048 tokens, 16 heads, bf16: 396
-// us with 46 spilled registers, 425 us without and half the waves).
-constexpr int waves_of(int t, int dp, bool shared) {
-  return dp == 128 && !shared && t != T_F32 ? 4 : 2;
-}
+// Waves a SIMD that leave a wave registers for all it holds.
+constexpr int waves_of(int dp, bool shared) { return dp == 64 && shared ? 1 : 2; }
 
 // SHARED: value heads share a key head, whose gradients are their sums.
 template <int T, int DP, bool SHARED>
-__global__ void __launch_bounds__(DP * 4, waves_of(T, DP, SHARED)) delta_grad(ChunkArgs c) {
+__global__ void __launch_bounds__(DP * 4, waves_of(DP, SHARED)) delta_grad(ChunkArgs c) {
   constexpr int NP = T == T_F32 ? 2 : 1;  // pieces of an input
   // pieces of what only dk (or only the rounded part of dq) sums: a bf16
   // output needs one, 2^-12 against its own 2^-9
