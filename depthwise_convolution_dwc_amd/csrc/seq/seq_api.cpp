@@ -193,7 +193,7 @@ DeltaArgs delta_args(const dwc_delta_problem* p, const void* q, const void* k, c
 
 // The chunked kernels' workspace, laid out from base (null: sizes only).
 size_t delta_layout(const dwc_delta_problem* p, bool bwd, char* base, ChunkArgs* c) {
-  const int64_t np = p->dtype == DWC_F32 ? 2 : 1, op = p->dtype == DWC_BF16 ? 1 : 2;
+  const int64_t np = p->dtype == DWC_F32 ? 2 : 1;
   const int64_t dp = p->dk <= 64 ? 64 : 128;
   c->nc = (int)((p->l + kChunk - 1) / kChunk);
   c->dvp = (p->dv + 15) / 16 * 16;
@@ -210,7 +210,7 @@ size_t delta_layout(const dwc_delta_problem* p, bool bwd, char* base, ChunkArgs*
   take(&c->gate, nv * (int64_t)sizeof(Gate));
   if (!bwd) {
     take(&c->qa, frags * 16);
-    take(&c->pa, tri * op * 16);
+    take(&c->pa, tri * 2 * 16);
   } else {
     take(&c->qt, frags * 16);
     take(&c->xt, tri * 2 * 16);

@@ -77,9 +77,6 @@ constexpr int waves_of(int dp, bool shared) { return dp == 64 && shared ? 1 : 2;
 template <int T, int DP, bool SHARED>
 __global__ void __launch_bounds__(DP * 4, waves_of(DP, SHARED)) delta_grad(ChunkArgs c) {
   constexpr int NP = T == T_F32 ? 2 : 1;  // pieces of an input
-  // pieces of what only dk (or only the rounded part of dq) sums: a bf16
-  // output needs one, 2^-12 against its own 2^-9
-  constexpr int OP = T == T_BF16 ? 1 : 2;
   constexpr int NW = DP / 16;   // waves
   constexpr int CPT = 64 / NW;  // columns of a 64-wide tile a thread loads
   extern __shared__ __align__(16) char lds_raw[];
@@ -269,13 +266,13 @@ __global__ void __launch_bounds__(DP * 4, waves_of(DP, SHARED)) delta_grad(Chunk
             f32x4 xq = {0.f, 0.f, 0.f, 0.f}, xk = xq;
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-              half8 fo[NP], fv[OP];
+              half8 fo[NP];
 #pragma unroll
               for (int y = 0; y < NP; ++y) fo[y] = frag8(tdo + y * kTile, 16 * i + m, ks, q);
-#pragma unroll
-              for (int y = 0; y < OP; ++y) fv[y] = frag8(tdv + y * kTile, 16 * i + m, ks, q);
+              const half8 fv[2] = {frag8(tdv, 16 * i + m, ks, q),
+                                   frag8(tdv + kTile, 16 * i + m, ks, q)};
               xq = mfma_pieces<NP, 2>(fo, fs[ks], xq);
-              xk = mfma_pieces<OP, OP>(fv, fs[ks], xk);
+              xk = mfma_pieces<2, 2>(fv, fs[ks], xk);
             }
             const f32x4 into = *(const f32x4*)(sinto + 16 * i + 4 * q);
 #pragma unroll
@@ -374,7 +371,7 @@ __global__ void __launch_bounds__(DP * 4, waves_of(DP, SHARED)) delta_grad(Chunk
         }
         if (ph) {
           *(half4*)(tpt + cc * kPitch + r4) = hi;
-          if constexpr (OP == 2) *(half4*)(tpt + kTile + cc * kPitch + r4) = lo;
+          *(half4*)(tpt + kTile + cc * kPitch + r4) = lo;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             tph[(r4 + i) * kPitch + cc] = hi[i];
@@ -382,11 +379,11 @@ __global__ void __launch_bounds__(DP * 4, waves_of(DP, SHARED)) delta_grad(Chunk
           }
         } else if (j < wr) {
           *(half4*)(tb + cc * kPitch + r4) = hi;
-          if constexpr (OP == 2) *(half4*)(tb + kTile + cc * kPitch + r4) = lo;
+          *(half4*)(tb + kTile + cc * kPitch + r4) = lo;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             tb[(r4 + i) * kPitch + cc] = hi[i];
-            if constexpr (OP == 2) tb[kTile + (r4 + i) * kPitch + cc] = lo[i];
+            tb[kTile + (r4 + i) * kPitch + cc] = lo[i];
           }
         } else if (j == wr) {
 #pragma unroll
@@ -394,10 +391,8 @@ __global__ void __launch_bounds__(DP * 4, waves_of(DP, SHARED)) delta_grad(Chunk
             if (cc > r4 + i) continue;
             tb[(r4 + i) * kPitch + cc] = hi[i];
             tb[cc * kPitch + r4 + i] = hi[i];
-            if constexpr (OP == 2) {
-              tb[kTile + (r4 + i) * kPitch + cc] = lo[i];
-              tb[kTile + cc * kPitch + r4 + i] = lo[i];
-            }
+            tb[kTile + (r4 + i) * kPitch + cc] = lo[i];
+            tb[kTile + cc * kPitch + r4 + i] = lo[i];
           }
         }
       }
@@ -424,14 +419,14 @@ __global__ void __launch_bounds__(DP * 4, waves_of(DP, SHARED)) delta_grad(Chunk
                                 frag44(tph + kTile, 16 * i + m, ks, q)};
             xq = mfma_pieces<2, NP>(f, fk[ks], xq);
           }
-          half8 f[OP], g[OP];
+          half8 f[2], g[2];
 #pragma unroll
-          for (int y = 0; y < OP; ++y) {
+          for (int y = 0; y < 2; ++y) {
             f[y] = frag44(tpt + y * kTile, 16 * i + m, ks, q);
             g[y] = frag44(tb + y * kTile, 16 * i + m, ks, q);
           }
-          if (ks == 1 || i < 2) xp = mfma_pieces<OP, NP>(f, fq[ks], xp);
-          xb = mfma_pieces<OP, NP>(g, fk[ks], xb);
+          if (ks == 1 || i < 2) xp = mfma_pieces<2, NP>(f, fq[ks], xp);
+          xb = mfma_pieces<2, NP>(g, fk[ks], xb);
         }
 #pragma unroll
         for (int x = 0; x < 4; ++x) {

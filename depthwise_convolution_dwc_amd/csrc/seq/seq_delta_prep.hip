@@ -55,9 +55,9 @@ __device__ __forceinline__ half8 row_frag(const _Float16* row, int ks, int q) {
   return half8{u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
 }
 
-// Pieces of the lower triangular tile in LDS (or of its transpose) to their
+// Both pieces of the lower triangular tile in LDS (or of its transpose) to their
 // blocks.  Wave w takes every fourth block.
-template <int P, bool TRANSPOSED>
+template <bool TRANSPOSED>
 __device__ __forceinline__ void write_tri(const float* tile, float s, Frag* dst) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, m = lane & 15, q = lane >> 4;
   for (int blk = w; blk < kTri; blk += 4) {
@@ -84,15 +84,15 @@ __device__ __forceinline__ void write_tri(const float* tile, float s, Frag* dst)
       lo[j] = l;
     }
     dst[blk * 64 + lane] = hi;
-    if constexpr (P == 2) dst[(kTri + blk) * 64 + lane] = lo;
+    dst[(kTri + blk) * 64 + lane] = lo;
   }
 }
 
-// T: type of q and k.  DP: head size padded.  NP: pieces of an input.  OP:
-// pieces of P in the forward pass.  BWD: also the transposes.
+// T: type of q and k.  DP: head size padded.  NP: pieces of an input.  BWD:
+// also the transposes.
 template <int T, int DP, bool WIDE, bool BWD>
 __global__ void __launch_bounds__(256, BWD ? 3 : 4) delta_prep(ChunkArgs c) {
-  constexpr int NP = T == T_F32 ? 2 : 1, OP = T == T_BF16 ? 1 : 2;
+  constexpr int NP = T == T_F32 ? 2 : 1;
   constexpr int KS = DP / 32, PITCH = DP + 8, PER = DP / 4;
   extern __shared__ __align__(16) char lds[];
   __shared__ float red[4][4];
@@ -347,12 +347,12 @@ __global__ void __launch_bounds__(256, BWD ? 3 : 4) delta_prep(ChunkArgs c) {
       gate->kinv = kinv;
       gate->qinv = qinv;
     }
-    write_tri<2, false>(tx, xs.mul, c.xa + hid * 2 * kTri * 64);
+    write_tri<false>(tx, xs.mul, c.xa + hid * 2 * kTri * 64);
     if constexpr (BWD) {
-      write_tri<2, true>(tx, xs.mul, c.xt + hid * 2 * kTri * 64);
-      write_tri<2, true>(tn, ps.mul, c.pt + hid * 2 * kTri * 64);
+      write_tri<true>(tx, xs.mul, c.xt + hid * 2 * kTri * 64);
+      write_tri<true>(tn, ps.mul, c.pt + hid * 2 * kTri * 64);
     } else {
-      write_tri<OP, false>(tn, ps.mul, c.pa + hid * OP * kTri * 64);
+      write_tri<false>(tn, ps.mul, c.pa + hid * 2 * kTri * 64);
     }
   }
 }

@@ -210,7 +210,7 @@ __device__ __forceinline__ void store_tile(float* matrix, int row0, int dvp, uin
 // block of blocks: the workgroup's number among those of its kind.
 template <int T, int DP, int NT, int NC, bool BWD>
 __device__ __forceinline__ void scan(const ChunkArgs& c, int block, int blocks, char* lds) {
-  constexpr int NP = T == T_F32 ? 2 : 1, OP = T == T_BF16 ? 1 : 2;
+  constexpr int NP = T == T_F32 ? 2 : 1;
   constexpr int KS = DP / 32, MT = DP / 16, MW = MT / 2;
   typedef Raw<T> R;
   auto& [bs, by, bu, bo] = ((Blocks<KS, NT, BWD>*)lds)[uniform((int)threadIdx.x >> 7)];
@@ -242,7 +242,7 @@ __device__ __forceinline__ void scan(const ChunkArgs& c, int block, int blocks, 
       }
 
   // this wave's fragments and values of one chunk
-  half8 ka[2][KS][NP], kt[MW][2][NP], xa[2][2][2], qa[2][KS][NP], pa[2][2][OP];
+  half8 ka[2][KS][NP], kt[MW][2][NP], xa[2][2][2], qa[2][KS][NP], pa[2][2][2];
   typename R::type vr[NT][2][4];
   Gates gt, gn;
   const auto kid_of = [&](int chunk) { return (p.b * c.nc + chunk) * a.hk + p.hk; };
@@ -267,14 +267,14 @@ __device__ __forceinline__ void scan(const ChunkArgs& c, int block, int blocks, 
           kt[i][ks][y] = at_lane(src + ((y * MT + hf * MW + i) * 2 + ks) * 64, loff);
   };
   // rows 0..31 of a lower triangular operand have their first block only
-  const auto load_tri = [&](auto& f, const Frag* base, int pieces, int chunk) {
-    const Frag* src = base + hid_of(chunk) * pieces * kTri * 64;
+  const auto load_tri = [&](half8(&f)[2][2][2], const Frag* base, int chunk) {
+    const Frag* src = base + hid_of(chunk) * 2 * kTri * 64;
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-        for (int y = 0; y < (int)(sizeof(f[0][0]) / sizeof(half8)); ++y)
+        for (int y = 0; y < 2; ++y)
           if (ks == 0 || hf)
             f[x][ks][y] = at_lane(src + (y * kTri + (hf ? 2 + 2 * x + ks : x)) * 64, loff);
   };
@@ -285,9 +285,9 @@ __device__ __forceinline__ void scan(const ChunkArgs& c, int block, int blocks, 
     load_rows(ka, c.ka, 0);
     load_v(0);
     if constexpr (!BWD) load_rows(qa, c.qa, 0);
-    load_tri(xa, c.xa, 2, 0);
+    load_tri(xa, c.xa, 0);
     load_kt(0);
-    if constexpr (!BWD) load_tri(pa, c.pa, OP, 0);
+    if constexpr (!BWD) load_tri(pa, c.pa, 0);
   }
   for (int chunk = 0; chunk < chunks; ++chunk) {
     const int next = chunk + 1 < chunks ? chunk + 1 : chunk;
@@ -331,8 +331,7 @@ __device__ __forceinline__ void scan(const ChunkArgs& c, int block, int blocks, 
       for (int x = 0; x < 2; ++x) u[nt][x] = gt.beta[x] * e[nt][x];
       publish<2>(&by[nt][hf], u[nt][0], u[nt][1], scale_of(column_max(abs_max2(u[nt]))), lane);
     }
-    // Q S, while the other wave's block is on its way; an output of 16 bits
-    // takes fewer pieces: bf16 one of each operand (2^-12 against its 2^-9)
+    // Q S, while the other wave's block is on its way
     f32x4 o[NT][2];
     if constexpr (!BWD) {
 #pragma unroll
@@ -340,12 +339,10 @@ __device__ __forceinline__ void scan(const ChunkArgs& c, int block, int blocks, 
         f32x4 acc[2][2] = {};
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          half8 f[OP];
-#pragma unroll
-          for (int y = 0; y < OP; ++y) f[y] = bs[nt][ks].f[y][lane];
+          const half8 f[2] = {bs[nt][ks].f[0][lane], bs[nt][ks].f[1][lane]};
 #pragma unroll
           for (int x = 0; x < 2; ++x)
-            acc[x][ks / (KS / 2)] = mfma_pieces<NP, OP>(qa[x][ks], f, acc[x][ks / (KS / 2)]);
+            acc[x][ks / (KS / 2)] = mfma_pieces<NP, 2>(qa[x][ks], f, acc[x][ks / (KS / 2)]);
         }
         const float sc = a.scale * gt.qinv;
         const float i0 = sc * bs[nt][0].inv[m], i1 = sc * bs[nt][KS - 1].inv[m];
@@ -377,13 +374,13 @@ __device__ __forceinline__ void scan(const ChunkArgs& c, int block, int blocks, 
         u[nt][x] = gt.beta[x] * e[nt][x];
       }
       if constexpr (!BWD)
-        publish<OP>(&bo[nt][hf], u[nt][0], u[nt][1], scale_of(column_max(abs_max2(u[nt]))), lane);
+        publish<2>(&bo[nt][hf], u[nt][0], u[nt][1], scale_of(column_max(abs_max2(u[nt]))), lane);
 #pragma unroll
       for (int x = 0; x < 2; ++x) u[nt][x] *= gt.out[x];
       publish<2>(&bu[nt][hf], u[nt][0], u[nt][1], scale_of(column_max(abs_max2(u[nt]))), lane);
     }
     if constexpr (!BWD) {
-      load_tri(xa, c.xa, 2, next);
+      load_tri(xa, c.xa, next);
     } else {
       // what the gradient needs of this chunk
 #pragma unroll
@@ -401,7 +398,7 @@ __device__ __forceinline__ void scan(const ChunkArgs& c, int block, int blocks, 
     }
     exchange();
     // S <- exp(G_64) S + K^T (exp(G_64 - G) o U)
-    if constexpr (BWD) load_tri(xa, c.xa, 2, next);
+    if constexpr (BWD) load_tri(xa, c.xa, next);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       half8 f[2][2];
@@ -429,11 +426,9 @@ __device__ __forceinline__ void scan(const ChunkArgs& c, int block, int blocks, 
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
           if (ks > hf) break;
-          half8 f[OP];
+          const half8 f[2] = {bo[nt][ks].f[0][lane], bo[nt][ks].f[1][lane]};
 #pragma unroll
-          for (int y = 0; y < OP; ++y) f[y] = bo[nt][ks].f[y][lane];
-#pragma unroll
-          for (int x = 0; x < 2; ++x) acc[x][ks] = mfma_pieces<OP, OP>(pa[x][ks], f, acc[x][ks]);
+          for (int x = 0; x < 2; ++x) acc[x][ks] = mfma_pieces<2, 2>(pa[x][ks], f, acc[x][ks]);
         }
         const float i0 = gt.pinv * bo[nt][0].inv[m], i1 = gt.pinv * bo[nt][1].inv[m];
 #pragma unroll
@@ -442,7 +437,7 @@ __device__ __forceinline__ void scan(const ChunkArgs& c, int block, int blocks, 
           for (int r = 0; r < 4; ++r) o[nt][x][r] += fmaf(i0, acc[x][0][r], i1 * acc[x][1][r]);
       }
       rows_o.store(o, chunk, len, a.l, whole, ok, hf, q);
-      load_tri(pa, c.pa, OP, next);
+      load_tri(pa, c.pa, next);
     }
     gt = gn;
   }
