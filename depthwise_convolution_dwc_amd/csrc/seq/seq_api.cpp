@@ -213,6 +213,8 @@ size_t delta_layout(const dwc_delta_problem* p, bool bwd, char* base, ChunkArgs*
     take(&c->pa, tri * 2 * 16);
   } else {
     take(&c->qt, frags * 16);
+    take(&c->kk, nk * kLow * 64 * 16);
+    take(&c->qk, nk * kLow * 64 * 16);
     take(&c->xt, tri * 2 * 16);
     take(&c->pt, tri * 2 * 16);
     take(&c->states, nv * dp * c->dvp * 4);

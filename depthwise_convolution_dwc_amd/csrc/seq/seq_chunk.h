@@ -64,16 +64,23 @@ __device__ __forceinline__ constexpr int tri_block_t(int m, int ks) {
 }
 constexpr int kTri = 6;
 
+// 16x16 blocks of the weakly lower triangle of a 64x64 matrix, as results of
+// the matrix cores: lane l of block (i, j) has rows 16 i + 4 (l / 16) .. + 3
+// of column 16 j + l % 16.
+__device__ __forceinline__ constexpr int low_block(int i, int j) { return i * (i + 1) / 2 + j; }
+constexpr int kLow = 10;
+
 struct ChunkArgs {
   DeltaArgs a;
   int nc;        // chunks of the longest sequence
   int dvp;       // dv rounded up to 16
   Frag *ka, *qa, *kt, *qt;   // per (b, chunk, hk): [piece][block][64]
   Frag *xa, *pa, *xt, *pt;   // per (b, chunk, hv): [piece][kTri][64]
+  f32x4 *kk, *qk;            // K K^T and Q K^T per (b, chunk, hk): [kLow][64]
   Gate* gate;                // per (b, chunk, hv)
   float *states, *dstates;   // per (b, chunk, hv): dp x dvp, before the chunk / after it
   float *e, *dw;             // per (b, chunk, hv): 64 x dvp
-  bool wide;  // v and dout can be read 16 bytes at a time, dv is a multiple of 8
+  bool wide;  // dout can be read 16 bytes at a time, dv is a multiple of 8
 };
 
 __device__ __forceinline__ int64_t live_tokens(const DeltaArgs& a, int64_t b) {

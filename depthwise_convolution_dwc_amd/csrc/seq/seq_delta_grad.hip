@@ -6,10 +6,17 @@
 //   dQ = scale exp(G) o (dO S^T) + Ph K
 //   dK = -exp(G) o (dV S^T) + exp(G_64 - G) o (U dS^T) + Ph^T Q + (B + B^T) K
 //   dbeta_t = E_t . W_t
-// and, since S_t exp(-G_t) depends on g through v exp(-G) and o exp(G) alone,
-//   dG_t = q_t . dq_t - v_t . dv_t  for each token,
-//   dg_t = sum of dG_s over s >= t in the chunk + <dS, S after the chunk>,
-//   <dS, S after> = exp(G_64) <dS, S> + sum_t k_t . (exp(G_64 - G) o U dS^T)_t.
+// g_s is in the exponent of every decay whose range holds it, so dg_s sums
+// what each of these decays contributes:
+//   exp(G_t), t >= s:             q_t . (scale exp(G) o (dO S^T))_t
+//                                 - k_t . (exp(G) o (dV S^T))_t
+//   exp(G_64 - G_j), j < s:       k_j . (exp(G_64 - G) o (U dS^T))_j
+//   D_tj, j < s <= t:             Ph_tj (q_t . k_j) + B_tj (k_t . k_j)
+//   exp(G_64):                    exp(G_64) <dS, S>
+// Every term carries its own decay and none is the difference of larger
+// ones: dg keeps its bits where it is small.  (q . dq - v . dv summed over
+// the tokens from s on is the same number, but the pairs of a token with
+// itself, which do not decay, are in both.)
 //
 // One workgroup of DP / 16 waves a (sequence, chunk, key head), the value
 // heads that share the key head one after another, dv in blocks of 64
@@ -80,8 +87,10 @@ __global__ void __launch_bounds__(DP * 4, waves_of(DP, SHARED)) delta_grad(Chunk
   constexpr int NW = DP / 16;   // waves
   constexpr int CPT = 64 / NW;  // columns of a 64-wide tile a thread loads
   extern __shared__ __align__(16) char lds_raw[];
-  __shared__ float red[4][NW];
-  __shared__ float sdot[NW][kChunk], sbeta[kChunk], svdv[kChunk];
+  __shared__ float red[3][NW];
+  // each wave's part of what the decays exp(G_t), exp(G_64 - G_j) and D take
+  // to dg
+  __shared__ float sinto_g[NW][kChunk], sout_g[NW][kChunk], spair_g[NW][kChunk], sbeta[kChunk];
   __shared__ __align__(16) float sinto[kChunk], sout[kChunk];
   __shared__ double sg[kChunk];
   _Float16* lds = (_Float16*)lds_raw;
@@ -124,7 +133,9 @@ __global__ void __launch_bounds__(DP * 4, waves_of(DP, SHARED)) delta_grad(Chunk
     }
     const Gate* gate = c.gate + hid;
     const float beta = gate->beta[row], kinv = gate->kinv, qinv = gate->qinv;
-    float ew = 0.f, vdv = 0.f, sds = 0.f, kdk = 0.f;
+    float ew = 0.f, sds = 0.f;
+    // this wave's key dimensions of k . dk by the decays exp(G) and exp(G_64 - G)
+    f32x4 kin[4], kout[4];
     // rows 16 wr.., columns 16 j.. of dO U^T and dV U^T: with 8 waves four
     // of them take the one and four the other, with 4 waves each takes both
     constexpr int BOTH = NW == 4 ? 2 : 1;
@@ -132,6 +143,7 @@ __global__ void __launch_bounds__(DP * 4, waves_of(DP, SHARED)) delta_grad(Chunk
     f32x4 dp[BOTH][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      kin[i] = kout[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int x = 0; x < BOTH; ++x) dp[x][i] = f32x4{0.f, 0.f, 0.f, 0.f};
       if constexpr (SHARED) {
@@ -154,25 +166,17 @@ __global__ void __launch_bounds__(DP * 4, waves_of(DP, SHARED)) delta_grad(Chunk
         const int64_t t = t0 + row;
         const float* ep = c.e + (hid * kChunk + row) * c.dvp + col;
         const float* wp = c.dw + (hid * kChunk + row) * c.dvp + col;
-        const int64_t vb = b * a.v_stride[0] + t * a.v_stride[1] + h * a.v_stride[2] + col;
         const int64_t ob = b * a.do_stride[0] + t * a.do_stride[1] + h * a.do_stride[2] + col;
-        float v[CPT];
 #pragma unroll
-        for (int i = 0; i < CPT; ++i) xd[i] = v[i] = xv[i] = xu[i] = 0.f;
+        for (int i = 0; i < CPT; ++i) xd[i] = xv[i] = xu[i] = 0.f;
         if (c.wide) {  // dv is a multiple of 8: eight columns are in or out
 #pragma unroll
           for (int i = 0; i < CPT; i += 8)
-            if (row < n && col + i < a.dv) {
-              load_vec<T, 8>(a.dout, ob + i, xd + i);
-              load_vec<T, 8>(a.v, vb + i, v + i);
-            }
+            if (row < n && col + i < a.dv) load_vec<T, 8>(a.dout, ob + i, xd + i);
         } else {
 #pragma unroll
           for (int i = 0; i < CPT; ++i)
-            if (row < n && col + i < a.dv) {
-              xd[i] = load1<T>(a.dout, ob + i);
-              v[i] = load1<T>(a.v, vb + i);
-            }
+            if (row < n && col + i < a.dv) xd[i] = load1<T>(a.dout, ob + i);
         }
         if (col < c.dvp) {
           load_vec<T_F32, CPT>(ep, 0, xu);
@@ -183,7 +187,6 @@ __global__ void __launch_bounds__(DP * 4, waves_of(DP, SHARED)) delta_grad(Chunk
           ew = fmaf(xu[i], xv[i], ew);
           xv[i] *= beta;
           xu[i] *= beta;
-          vdv = fmaf(v[i], xv[i], vdv);
           md = fmaxf(md, fabsf(xd[i]));
           mv = fmaxf(mv, fabsf(xv[i]));
           mu = fmaxf(mu, fabsf(xu[i]));
@@ -252,6 +255,19 @@ __global__ void __launch_bounds__(DP * 4, waves_of(DP, SHARED)) delta_grad(Chunk
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int x = 0; x < 4; ++x) sds = fmaf(s[i][x], g[i][x], sds);
+        half8 fk[2][NP];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+          for (int y = 0; y < NP; ++y) fk[ks][y] = at_lane(kt + y * PIECE + ks * 64, loff);
+        // k at the place of value x of row block i of a result, from its
+        // fragments
+        const auto k_at = [&](int i, int x) {
+          const int slot = (i & 1) * 4 + x;
+          float v = (float)fk[i >> 1][0][slot];
+          if constexpr (NP == 2) v += (float)fk[i >> 1][1][slot];
+          return v;
+        };
         // one state after the other: fragments of both would not fit
         {
           const Scale ss = scale_of(column_max(abs_max(s)));
@@ -278,20 +294,18 @@ __global__ void __launch_bounds__(DP * 4, waves_of(DP, SHARED)) delta_grad(Chunk
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               dq[i][x] = fmaf(cq * into[x], xq[x], dq[i][x]);
-              dk[i][x] = fmaf(ck * into[x], xk[x], dk[i][x]);
+              const float v = ck * into[x] * xk[x];
+              kin[i][x] = fmaf(k_at(i, x), v, kin[i][x]);
+              dk[i][x] += v;
             }
           }
         }
         __builtin_amdgcn_sched_barrier(0);
         {
           const Scale sgr = scale_of(column_max(abs_max(g)));
-          half8 fg[2][2], fk[2][NP];
+          half8 fg[2][2];
 #pragma unroll
-          for (int ks = 0; ks < 2; ++ks) {
-            to_frag<2>(g[2 * ks], g[2 * ks + 1], sgr.mul, fg[ks]);
-#pragma unroll
-            for (int y = 0; y < NP; ++y) fk[ks][y] = at_lane(kt + y * PIECE + ks * 64, loff);
-          }
+          for (int ks = 0; ks < 2; ++ks) to_frag<2>(g[2 * ks], g[2 * ks + 1], sgr.mul, fg[ks]);
           const float cu = su.inv * sgr.inv;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -306,12 +320,8 @@ __global__ void __launch_bounds__(DP * 4, waves_of(DP, SHARED)) delta_grad(Chunk
             const f32x4 out = *(const f32x4*)(sout + 16 * i + 4 * q);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              // k at this result's place, from its fragments
-              const int slot = (i & 1) * 4 + x;
-              float kv = (float)fk[i >> 1][0][slot];
-              if constexpr (NP == 2) kv += (float)fk[i >> 1][1][slot];
               const float v = cu * out[x] * xs[x];
-              kdk = fmaf(kv * kinv, v, kdk);
+              kout[i][x] = fmaf(k_at(i, x), v, kout[i][x]);
               dk[i][x] += v;
             }
           }
@@ -322,19 +332,49 @@ __global__ void __launch_bounds__(DP * 4, waves_of(DP, SHARED)) delta_grad(Chunk
     asm volatile("" : "+v"(m), "+v"(q), "+v"(row), "+v"(part));
     __syncthreads();
     float mx[2] = {0.f, 0.f};
+    f32x4 pair[4];  // what the decay of each pair of tokens contributes
+#pragma unroll
+    for (int j = 0; j < 4; ++j) pair[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int x = 0; x < BOTH; ++x) {
       const bool ph = BOTH == 2 ? x == 0 : w < 4;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 4; ++j) {
+        if (j > wr) continue;  // zero as it is
+        const f32x4 with =
+            (ph ? c.qk : c.kk)[(id * kLow + low_block(wr, j)) * 64 + 16 * q + m];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int rr = 16 * wr + 4 * q + i, cc = 16 * j + m;
           const float d = cc <= rr ? __builtin_amdgcn_exp2f((float)(sg[rr] - sg[cc])) : 0.f;
           const float v = ph ? a.scale * d * dp[x][j][i] : -d * dp[x][j][i];
+          if (cc < rr) pair[j][i] = fmaf(v, with[i], pair[j][i]);
           dp[x][j][i] = cc < rr || (ph && cc == rr) ? v : 0.f;
           mx[x] = fmaxf(mx[x], fabsf(dp[x][j][i]));
         }
+      }
+    }
+    // The pairs (t, j) with j < s <= t, summed for each s: over j < s inside
+    // each row t, then over this wave's rows t >= s.
+    {
+      f32x4 before = {0.f, 0.f, 0.f, 0.f};  // of the blocks left of this one
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float sum = 0.f;
+        if (j <= wr) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (16 * j + m <= 16 * wr + 4 * q + i) sum += before[i] + sum_before16(pair[j][i]);
+            before[i] += lane_sum<16>(pair[j][i]);
+          }
+          float o;
+          rows16(sum, o);
+          sum += o;
+          halves(sum, o);
+          sum += o;
+        }
+        if (q == 0) spair_g[w][16 * j + m] = sum;
+      }
     }
     if (BOTH == 1 && w >= 4) {
       mx[1] = mx[0];
@@ -430,45 +470,44 @@ __global__ void __launch_bounds__(DP * 4, waves_of(DP, SHARED)) delta_grad(Chunk
         }
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          // q . dq of the token, from q's fragments
+          // q at this place, from its fragments; dq is by exp(G) so far
           const int slot = (i & 1) * 4 + x;
           float qv = (float)fq[i >> 1][0][slot];
           if constexpr (NP == 2) qv += (float)fq[i >> 1][1][slot];
+          const float in = lane_sum<16>(fmaf(qv * qinv, dq[i][x], kinv * kin[i][x]));
+          const float out = lane_sum<16>(kinv * kout[i][x]);
+          if (m == 0) {
+            sinto_g[w][16 * i + 4 * q + x] = in;
+            sout_g[w][16 * i + 4 * q + x] = out;
+          }
           dq[i][x] = fmaf(sp.inv * kinv, xq[x], dq[i][x]);
-          const float d = lane_sum<16>(qv * qinv * dq[i][x]);
-          if (m == 0) sdot[w][16 * i + 4 * q + x] = d;
           dk[i][x] += fmaf(sp.inv * qinv, xp[x], sb.inv * kinv * xb[x]);
         }
       }
     }
     // dbeta and dg
     ew = lane_sum<NW>(ew);
-    vdv = lane_sum<NW>(vdv);
-    if (part == 0) {
-      sbeta[row] = ew;
-      svdv[row] = vdv;
-    }
+    if (part == 0) sbeta[row] = ew;
     sds = lane_sum<64>(sds);
-    kdk = lane_sum<64>(kdk);
-    if (lane == 0) {
-      red[2][w] = sds;
-      red[3][w] = kdk;
-    }
+    if (lane == 0) red[2][w] = sds;
     __syncthreads();
     if (w == 0) {
-      float d = -svdv[lane], far = 0.f, ends = 0.f;
+      float d = 0.f, early = 0.f, pairs = 0.f, far = 0.f;
 #pragma unroll
       for (int i = 0; i < NW; ++i) {
-        d += sdot[i][lane];
+        d += sinto_g[i][lane];
+        if (lane > 0) early += sout_g[i][lane - 1];
+        pairs += spair_g[i][lane];
         far += red[2][i];
-        ends += red[3][i];
       }
+      // over the tokens from this one on, and over those before it
 #pragma unroll
       for (int i = 1; i < 64; i <<= 1) {
-        const float o = __shfl_down(d, i, 64);
+        const float o = __shfl_down(d, i, 64), p = __shfl_up(early, i, 64);
         if (lane + i < 64) d += o;
+        if (lane >= i) early += p;
       }
-      d += gate->total * far + ends;
+      d += early + pairs + gate->total * far;
       if (t0 + lane < a.l) {
         a.dg[(b * a.l + t0 + lane) * a.hv + h] = lane < n ? d : 0.f;
         a.dbeta[(b * a.l + t0 + lane) * a.hv + h] = lane < n ? sbeta[lane] : 0.f;
@@ -503,9 +542,8 @@ void go(const ChunkArgs& c, hipStream_t st) {
 
 hipError_t launch_delta_grad(ChunkArgs c, hipStream_t st) {
   const int64_t unit = c.a.type == T_F32 ? 4 : 8;
-  c.wide = c.a.dv % 8 == 0 && ((uintptr_t)c.a.v | (uintptr_t)c.a.dout) % 16 == 0;
-  for (int i = 0; i < 3; ++i)
-    c.wide = c.wide && c.a.v_stride[i] % unit == 0 && c.a.do_stride[i] % unit == 0;
+  c.wide = c.a.dv % 8 == 0 && (uintptr_t)c.a.dout % 16 == 0;
+  for (int i = 0; i < 3; ++i) c.wide = c.wide && c.a.do_stride[i] % unit == 0;
   if (c.a.type == T_F32) grad::go<T_F32>(c, st);
   else if (c.a.type == T_BF16) grad::go<T_BF16>(c, st);
   else grad::go<T_F16>(c, st);

@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(256, BWD ? 3 : 4) delta_prep(ChunkArgs c) {
 
   // K and Q to LDS as scaled pieces; places past the sequence or the head
   // size are zero whatever memory holds there
-  float kinv, qinv;
+  float kinv = 0.f, qinv = 0.f;
   {
     // a thread takes every fourth 8 values of a row
     const int row = tid >> 2, part = tid & 3;
@@ -224,6 +224,15 @@ __global__ void __launch_bounds__(256, BWD ? 3 : 4) delta_prep(ChunkArgs c) {
         fb[p] = row_frag(rows + (p * kChunk + 16 * j + m) * PITCH, ks, q);
       kk[j] = mfma_pieces<NP, NP>(fk, fb, kk[j]);
       qk[j] = mfma_pieces<NP, NP>(fq, fb, qk[j]);
+    }
+  }
+  if constexpr (BWD) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j > w) continue;
+      const int64_t at = (id * kLow + low_block(w, j)) * 64 + lane;
+      c.kk[at] = kk[j] * kinv * kinv;
+      c.qk[at] = qk[j] * kinv * qinv;
     }
   }
   // fragments of the transposes (rows are key dimensions)

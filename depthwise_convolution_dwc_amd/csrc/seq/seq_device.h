@@ -170,5 +170,15 @@ __device__ __forceinline__ float lane_sum(float v) {
   return v;
 }
 
+// Sum over the lanes before this one in its row of 16: shifted by one lane,
+// then summed up to this lane.
+__device__ __forceinline__ float sum_before16(float v) {
+  v = row_move<0x111>(v);
+  v += row_move<0x111>(v);
+  v += row_move<0x112>(v);
+  v += row_move<0x114>(v);
+  return v + row_move<0x118>(v);
+}
+
 }  // namespace seq
 }  // namespace dwc

@@ -1,7 +1,7 @@
 """What single values of the chunked gated delta rule and of its gradients are
-worth: outputs of 16 bits before they are rounded.  Norms of whole outputs
-are tested in test_delta_gpu.py, whose F bounds an output's error before its
-rounding as a share of its 2-norm.
+worth: outputs of 16 bits before they are rounded, the gradient of every
+decay.  Norms of whole outputs are tested in test_delta_gpu.py, whose F
+bounds an output's error before its rounding as a share of its 2-norm.
 """
 
 import pytest
@@ -13,7 +13,7 @@ if not torch.cuda.is_available():
     pytest.skip("no GPU", allow_module_level=True)
 
 from gpu_helpers import dwc, log, sync  # noqa: E402
-from test_delta_gpu import F, wanted  # noqa: E402
+from test_delta_gpu import F, TOL, wanted  # noqa: E402
 from test_sequence_gpu import BF16, F16, F32, delta_inputs, randn, rel  # noqa: E402
 
 
@@ -36,3 +36,58 @@ def test_16_bit_outputs_are_rounded_once(dtype, shape):
         r = rel(g, w.to(dtype).double())
         log(f"{name} {r:.3g}")
         assert r < (F * torch.finfo(dtype).eps) ** 0.5, (name, r)
+
+
+def decay_products(a, dout, ds1):
+    """dg in 64 bits and, for each token, the 2-norms' product of what it is
+    the inner product of: the decayed state and its gradient."""
+    q, k, v, g, beta, s0 = (t.double() for t in a)
+    n, r = v.shape[1], v.shape[2] // q.shape[2]
+    q, k = q.repeat_interleave(r, 2), k.repeat_interleave(r, 2)
+    outer = lambda x, y: x[..., :, None] * y[..., None, :]  # noqa: E731
+    down = lambda m, x: (m * x[..., :, None]).sum(-2)  # noqa: E731
+    scale, s, kept = a[0].shape[3] ** -0.5, s0, []
+    for t in range(n):
+        dec = s * g[:, t].exp()[..., None, None]
+        s = dec + outer(k[:, t], beta[:, t, :, None] * (v[:, t] - down(dec, k[:, t])))
+        kept.append(dec)
+    ds, dg, size = ds1.double(), torch.zeros_like(g), torch.zeros_like(g)
+    for t in reversed(range(n)):
+        ds = ds + scale * outer(q[:, t], dout[:, t].double())
+        ds = ds - outer(k[:, t], beta[:, t, :, None] * down(ds, k[:, t]))
+        dg[:, t] = (kept[t] * ds).sum((-1, -2))
+        size[:, t] = kept[t].flatten(-2).norm(dim=-1) * ds.flatten(-2).norm(dim=-1)
+        ds = ds * g[:, t].exp()[..., None, None]
+    return dg, size
+
+
+DECAYS = [(-3.0, None), (-10.0, None), (-16.0, None), (-30.0, None), (-5.0, 70), (-16.0, 70),
+          (-30.0, 63), (-30.0, 64), (-60.0, 5), (-float("inf"), 70), (-float("inf"), 64)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("shape", [(1, 130, 2, 2, 64, 64), (1, 150, 1, 2, 128, 128),
+                                   (2, 128, 1, 3, 40, 24)])
+@pytest.mark.parametrize("g,at", DECAYS)
+def test_gradient_of_each_decay(dtype, shape, g, at):
+    """Every token's dg by itself: an inner product of the decayed state and
+    its gradient, so off by at most F of their norms' product, however small
+    the decay makes it.  One strong decay among mild ones, or all alike."""
+    log(f"case dg {dtype} {shape} {g} {at}")
+    a = list(delta_inputs(sum(shape), *shape, dtype))
+    a[3] = a[3].clone()
+    a[3][:, slice(None) if at is None else at] = g
+    b, n, hk, hv, dk, dv = shape
+    dout, ds1 = randn(5, b, n, hv, dv, dtype=dtype), randn(6, b, hv, dk, dv, scale=0.1)
+    grads = dwc.delta_rule_bwd(dout, ds1, *a)
+    sync()
+    want, size = decay_products(a, dout, ds1)
+    off = (grads[3].double() - want).abs()
+    worst = (off / size.clamp_min(1e-300)).max().item()
+    log(f"dg {worst:.3g}, dg of the strong one {(off / want.abs().clamp_min(1e-300))[:, at or 0].max().item():.3g}")
+    assert torch.isfinite(grads[3]).all() and (off <= F * size).all(), worst
+    _, _, wg = wanted(a, dout, ds1)
+    for name, x, w in zip(("dq", "dk", "dv", "dg", "dbeta", "ds0"), grads, wg):
+        r = rel(x, w)
+        log(f"{name} {r:.3g}")
+        assert r < TOL[x.dtype], (name, r)
