@@ -43,7 +43,8 @@ struct Gate {
   float total;         // exp(G_64)
   // the packed values of X, P, K and Q times these are the true ones
   float xinv, pinv, kinv, qinv;
-  float pad[3];
+  // (backward) the larger of the last two, and what each of them is of it
+  float top, kpart, qpart;
   double g[kChunk];    // G_t log2(e)
 };
 
@@ -94,14 +95,16 @@ __device__ __forceinline__ f32x4 mfma(half8 a, half8 b, f32x4 c) {
 }
 
 // The power of two that brings a largest magnitude m to 2^14..2^15, and its
-// inverse; tiny m (and zero) are treated as 2^-40, so that both and their
-// products with other scales stay normal numbers.
+// inverse.  m below 2^-101 (and zero) is treated as 2^-101: both stay normal
+// numbers, also times a decay, and an inverse times another one is exact
+// down to 2^-149.  Factors of an operand go to the product's result and not
+// into the operand, whose scale would then meet the limit earlier.
 struct Scale {
   float mul, inv;
 };
 __device__ __forceinline__ Scale scale_of(float m) {
   int e = (int)((__builtin_bit_cast(uint32_t, m) >> 23) & 255) - 126;  // m < 2^e
-  e = e < -40 ? -40 : (e > 125 ? 125 : e);
+  e = e < -100 ? -100 : (e > 125 ? 125 : e);
   return Scale{__builtin_bit_cast(float, (uint32_t)(127 + 15 - e) << 23),
                __builtin_bit_cast(float, (uint32_t)(127 + e - 15) << 23)};
 }

@@ -256,10 +256,15 @@ __global__ void __launch_bounds__(DP * 4, waves_of(DP, SHARED)) delta_grad(Chunk
 #pragma unroll
           for (int x = 0; x < 4; ++x) sds = fmaf(s[i][x], g[i][x], sds);
         half8 fk[2][NP];
+        const auto load_k = [&]() {
+          uint32_t at = loff;
+          asm volatile("" : "+v"(at));  // loaded again, not held, where it says so
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
+          for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-          for (int y = 0; y < NP; ++y) fk[ks][y] = at_lane(kt + y * PIECE + ks * 64, loff);
+            for (int y = 0; y < NP; ++y) fk[ks][y] = at_lane(kt + y * PIECE + ks * 64, at);
+        };
+        load_k();
         // k at the place of value x of row block i of a result, from its
         // fragments
         const auto k_at = [&](int i, int x) {
@@ -274,7 +279,7 @@ __global__ void __launch_bounds__(DP * 4, waves_of(DP, SHARED)) delta_grad(Chunk
           half8 fs[2][2];
 #pragma unroll
           for (int ks = 0; ks < 2; ++ks) to_frag<2>(s[2 * ks], s[2 * ks + 1], ss.mul, fs[ks]);
-          const float cq = a.scale * sd.inv * ss.inv, ck = -sv.inv * ss.inv;
+          const float cq = a.scale * sd.inv, ck = -sv.inv;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             // loads of later rows are not pulled ahead of this one's products
@@ -293,8 +298,8 @@ __global__ void __launch_bounds__(DP * 4, waves_of(DP, SHARED)) delta_grad(Chunk
             const f32x4 into = *(const f32x4*)(sinto + 16 * i + 4 * q);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              dq[i][x] = fmaf(cq * into[x], xq[x], dq[i][x]);
-              const float v = ck * into[x] * xk[x];
+              dq[i][x] = fmaf(cq * into[x], ss.inv * xq[x], dq[i][x]);
+              const float v = ck * into[x] * (ss.inv * xk[x]);
               kin[i][x] = fmaf(k_at(i, x), v, kin[i][x]);
               dk[i][x] += v;
             }
@@ -304,9 +309,9 @@ __global__ void __launch_bounds__(DP * 4, waves_of(DP, SHARED)) delta_grad(Chunk
         {
           const Scale sgr = scale_of(column_max(abs_max(g)));
           half8 fg[2][2];
+          if constexpr (SHARED && NP == 2) load_k();  // (no registers to hold it)
 #pragma unroll
           for (int ks = 0; ks < 2; ++ks) to_frag<2>(g[2 * ks], g[2 * ks + 1], sgr.mul, fg[ks]);
-          const float cu = su.inv * sgr.inv;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             __builtin_amdgcn_sched_barrier(0);
@@ -320,7 +325,7 @@ __global__ void __launch_bounds__(DP * 4, waves_of(DP, SHARED)) delta_grad(Chunk
             const f32x4 out = *(const f32x4*)(sout + 16 * i + 4 * q);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const float v = cu * out[x] * xs[x];
+              const float v = su.inv * out[x] * (sgr.inv * xs[x]);
               kout[i][x] = fmaf(k_at(i, x), v, kout[i][x]);
               dk[i][x] += v;
             }

@@ -355,6 +355,12 @@ __global__ void __launch_bounds__(256, BWD ? 3 : 4) delta_prep(ChunkArgs c) {
       gate->pinv = ps.inv;
       gate->kinv = kinv;
       gate->qinv = qinv;
+      if constexpr (BWD) {
+        const float most = fmaxf(kinv, qinv);
+        gate->top = most;
+        gate->kpart = kinv / most;  // powers of two: exact
+        gate->qpart = qinv / most;
+      }
     }
     write_tri<false>(tx, xs.mul, c.xa + hid * 2 * kTri * 64);
     if constexpr (BWD) {

@@ -54,7 +54,7 @@ struct Raw<T_F32> {
 // This wave's rows of a chunk's gates.
 struct Gates {
   f32x4 into[2], out[2], beta[2];
-  float total, xinv, pinv, kinv, qinv;
+  float total, xinv, pinv, kinv, qinv, top, kpart, qpart;
   __device__ __forceinline__ void load(const Gate* g, int hf, int q) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -67,6 +67,9 @@ struct Gates {
     pinv = g->pinv;
     kinv = g->kinv;
     qinv = g->qinv;
+    top = g->top;
+    kpart = g->kpart;
+    qpart = g->qpart;
   }
 };
 
@@ -626,13 +629,14 @@ __device__ __forceinline__ void scan_back(const ChunkArgs& c, int block, int blo
         for (int r = 0; r < 4; ++r) w[nt][x][r] -= fmaf(i0, acc[x][0][r], i1 * acc[x][1][r]);
         y[nt][x] = gt.beta[x] * w[nt][x];
         g[nt][x] = y[nt][x];
-        y[nt][x] *= -gt.kinv * gt.into[x];
-        d[nt][x] *= a.scale * gt.qinv * gt.into[x];
+        y[nt][x] *= -gt.kpart * gt.into[x];
+        d[nt][x] *= a.scale * gt.qpart * gt.into[x];
         if (in[nt])
           store_tile(c.dw + hid * kChunk * c.dvp + 16 * nt, 16 * (2 * hf + x), c.dvp, soff,
                      w[nt][x]);
       }
-      // one scale for both operands, so that one sum takes both products
+      // one scale for both operands, so that one sum takes both products; of
+      // K's and Q's own scales they take what the two differ by
       const Scale ys = scale_of(column_max(fmaxf(abs_max2(y[nt]), abs_max2(d[nt]))));
       publish<2>(&bu[nt][hf], y[nt][0], y[nt][1], ys, lane);
       publish<2>(&bo[nt][hf], d[nt][0], d[nt][1], ys, lane);
@@ -650,7 +654,7 @@ __device__ __forceinline__ void scan_back(const ChunkArgs& c, int block, int blo
           f[ks][z] = bu[nt][ks].f[z][lane];
           g[ks][z] = bo[nt][ks].f[z][lane];
         }
-      const float i0 = bu[nt][0].inv[m], i1 = bu[nt][1].inv[m];
+      const float i0 = gt.top * bu[nt][0].inv[m], i1 = gt.top * bu[nt][1].inv[m];
 #pragma unroll
       for (int i = 0; i < MW; ++i) {
         f32x4 acc[2] = {};

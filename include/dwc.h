@@ -342,7 +342,9 @@ int dwc_dropout(const dwc_dropout_problem* p, const void* x,
  * 0).  q, k, v, s0 of live tokens must be finite in the chunked calls: a
  * matrix product multiplies masked places by zero too, so an infinity or
  * NaN in a live token may turn outputs of earlier tokens of its chunk of 64
- * into NaN. */
+ * into NaN.  Magnitudes do not matter to them while an operand's largest (of
+ * q, k, v, dout in a chunk, of a column of a state) is above 1e-30 and the
+ * results are above 1e-33; smaller ones lose bits. */
 typedef struct {
     int64_t b, l;           /* sequences and tokens, >= 0                   */
     int64_t q_stride[3], k_stride[3], v_stride[3], g_stride[3],

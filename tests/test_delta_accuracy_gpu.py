@@ -1,6 +1,6 @@
 """What single values of the chunked gated delta rule and of its gradients are
 worth: outputs of 16 bits before they are rounded, the gradient of every
-decay.  Norms of whole outputs are tested in test_delta_gpu.py, whose F
+decay, small magnitudes.  Norms of whole outputs are tested in test_delta_gpu.py, whose F
 bounds an output's error before its rounding as a share of its 2-norm.
 """
 
@@ -13,7 +13,7 @@ if not torch.cuda.is_available():
     pytest.skip("no GPU", allow_module_level=True)
 
 from gpu_helpers import dwc, log, sync  # noqa: E402
-from test_delta_gpu import F, TOL, wanted  # noqa: E402
+from test_delta_gpu import F, TOL, check, wanted  # noqa: E402
 from test_sequence_gpu import BF16, F16, F32, delta_inputs, randn, rel  # noqa: E402
 
 
@@ -91,3 +91,41 @@ def test_gradient_of_each_decay(dtype, shape, g, at):
         r = rel(x, w)
         log(f"{name} {r:.3g}")
         assert r < TOL[x.dtype], (name, r)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [(1, 130, 2, 2, 64, 64), (1, 150, 1, 2, 128, 128),
+                                   (2, 100, 2, 2, 40, 24)])
+@pytest.mark.parametrize("power", [-80, -60, -30, 20])
+def test_small_values_keep_their_bits(dtype, shape, power):
+    """The gradients are linear in dout and ds1, o and s1 in v and s0: scaled
+    by a power of two they come out scaled, bit by bit."""
+    log(f"case small {dtype} {shape} {power}")
+    a = list(delta_inputs(sum(shape), *shape, dtype))
+    b, n, hk, hv, dk, dv = shape
+    dout, ds1 = randn(7, b, n, hv, dv, dtype=dtype), randn(8, b, hv, dk, dv, scale=0.1)
+    f = 2.0 ** power
+    for name, x, y in zip(("dq", "dk", "dv", "dg", "dbeta", "ds0"),
+                          dwc.delta_rule_bwd(dout * f, ds1 * f, *a),
+                          dwc.delta_rule_bwd(dout, ds1, *a)):
+        assert torch.equal(x, y * f), (name, rel(x, y.double() * f))
+    small = a[:2] + [a[2] * f] + a[3:5] + [a[5] * f]
+    for name, x, y in zip(("o", "s1"), dwc.delta_rule(*small), dwc.delta_rule(*a)):
+        assert torch.equal(x, y * f), (name, rel(x, y.double() * f))
+    # and for small values of everything else
+    for name, x, y in zip(("dq", "dk", "dv", "dg", "dbeta", "ds0"),
+                          dwc.delta_rule_bwd(dout, ds1, *small),
+                          dwc.delta_rule_bwd(dout, ds1, *a)):
+        assert torch.equal(x, y if name == "dv" or name == "ds0" else y * f), name
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("which", [0, 1])
+def test_one_of_queries_and_keys_small_or_zero(dtype, which):
+    """A product of the backward pass takes K and Q together: neither may
+    cost the other its bits."""
+    for f in (0.0, 2.0 ** -60, 2.0 ** 30):
+        log(f"case small {dtype} {which} {f}")
+        a = list(delta_inputs(9, 1, 150, 1, 2, 64, 40, dtype))
+        a[which] = a[which] * f if which == 0 else a[which] * min(f, 1.0)
+        check(a)
