@@ -38,6 +38,7 @@ EXPORTED = (
     "dwc_check", "dwc_plan_describe", "dwc_fwd", "dwc_fwd_fused", "dwc_bwd_data",
     "dwc_bwd_filter_workspace_size", "dwc_bwd_filter", "dwc_bwd_filter_noalloc",
     "dwc_layer_norm", "dwc_layer_norm_bwd_workspace_size", "dwc_layer_norm_bwd", "dwc_dropout",
+    "dwc_dropout_at",
     "dwc_delta_step", "dwc_delta_workspace_size", "dwc_delta_fwd", "dwc_delta_bwd",
 )
 

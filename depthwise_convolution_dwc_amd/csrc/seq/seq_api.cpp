@@ -225,6 +225,40 @@ size_t delta_layout(const dwc_delta_problem* p, bool bwd, char* base, ChunkArgs*
   return at;
 }
 
+int run_dropout(const dwc_dropout_problem* p, const void* x, const void* residual, void* y,
+                const uint64_t* position, void* stream) {
+  if (!p) return fail(DWC_ERR_BAD_PARAM, "problem pointer is NULL");
+  if (p->n < 0) return fail(DWC_ERR_BAD_PARAM, "need n >= 0");
+  if (!is_type(p->dtype))
+    return fail(DWC_ERR_BAD_PARAM, "dropout types are DWC_F32, DWC_BF16 and DWC_F16");
+  if (!(p->p >= 0.0 && p->p <= 1.0)) return fail(DWC_ERR_BAD_PARAM, "need 0 <= p <= 1");
+  if (p->n > (int64_t)1 << 33)  // a launch has fewer than 2^32 threads
+    return fail(DWC_ERR_UNSUPPORTED, "dropout sizes past the launch range");
+  if (p->n == 0) return DWC_OK;
+  if (!x || !y) return fail(DWC_ERR_BAD_PARAM, "x or y pointer is NULL");
+  const int64_t e = bytes_of(p->dtype);
+  const Span in[] = {{x, p->n * e, e}, {residual, residual ? p->n * e : 0, e},
+                     {position, position ? 8 : 0, 8}};
+  const Span out[] = {{y, p->n * e, e}};
+  const int st = check_spans(in, out);
+  if (st != DWC_OK) return st;
+  DropArgs a{};
+  a.x = x;
+  a.res = residual;
+  a.y = y;
+  a.n = p->n;
+  a.offset = p->offset;
+  a.position = position;
+  a.key0 = (uint32_t)p->seed;
+  a.key1 = (uint32_t)(p->seed >> 32);
+  const double t = std::nearbyint(p->p * 4294967296.0);  // ties to even
+  a.drop_all = t >= 4294967296.0;
+  a.threshold = a.drop_all ? 0xffffffffu : (uint32_t)t;
+  a.scale = p->p < 1.0 ? (float)(1.0 / (1.0 - p->p)) : 0.f;
+  a.type = p->dtype;
+  return hip_result(launch_dropout(a, (hipStream_t)stream), "dropout launch");
+}
+
 }  // namespace
 
 extern "C" {
@@ -305,34 +339,13 @@ int dwc_layer_norm_bwd(const dwc_norm_problem* p, const void* dy, const void* x,
 
 int dwc_dropout(const dwc_dropout_problem* p, const void* x, const void* residual, void* y,
                 void* stream) {
-  if (!p) return fail(DWC_ERR_BAD_PARAM, "problem pointer is NULL");
-  if (p->n < 0) return fail(DWC_ERR_BAD_PARAM, "need n >= 0");
-  if (!is_type(p->dtype))
-    return fail(DWC_ERR_BAD_PARAM, "dropout types are DWC_F32, DWC_BF16 and DWC_F16");
-  if (!(p->p >= 0.0 && p->p <= 1.0)) return fail(DWC_ERR_BAD_PARAM, "need 0 <= p <= 1");
-  if (p->n > (int64_t)1 << 33)  // a launch has fewer than 2^32 threads
-    return fail(DWC_ERR_UNSUPPORTED, "dropout sizes past the launch range");
-  if (p->n == 0) return DWC_OK;
-  if (!x || !y) return fail(DWC_ERR_BAD_PARAM, "x or y pointer is NULL");
-  const int64_t e = bytes_of(p->dtype);
-  const Span in[] = {{x, p->n * e, e}, {residual, residual ? p->n * e : 0, e}};
-  const Span out[] = {{y, p->n * e, e}};
-  const int st = check_spans(in, out);
-  if (st != DWC_OK) return st;
-  DropArgs a{};
-  a.x = x;
-  a.res = residual;
-  a.y = y;
-  a.n = p->n;
-  a.offset = p->offset;
-  a.key0 = (uint32_t)p->seed;
-  a.key1 = (uint32_t)(p->seed >> 32);
-  const double t = std::nearbyint(p->p * 4294967296.0);  // ties to even
-  a.drop_all = t >= 4294967296.0;
-  a.threshold = a.drop_all ? 0xffffffffu : (uint32_t)t;
-  a.scale = p->p < 1.0 ? (float)(1.0 / (1.0 - p->p)) : 0.f;
-  a.type = p->dtype;
-  return hip_result(launch_dropout(a, (hipStream_t)stream), "dwc_dropout launch");
+  return run_dropout(p, x, residual, y, nullptr, stream);
+}
+
+int dwc_dropout_at(const dwc_dropout_problem* p, const void* x, const void* residual, void* y,
+                   const uint64_t* position, void* stream) {
+  if (!position) return fail(DWC_ERR_BAD_PARAM, "position pointer is NULL");
+  return run_dropout(p, x, residual, y, position, stream);
 }
 
 int dwc_delta_step(const dwc_delta_problem* p, const void* q, const void* k, const void* v,

@@ -43,6 +43,7 @@ template <int T, int VEC, bool WIDE, bool RES>
 __global__ void __launch_bounds__(256) dropout(DropArgs a) {
   const int64_t i0 = ((int64_t)blockIdx.x * 256 + threadIdx.x) * VEC;
   if (i0 >= a.n) return;
+  const uint64_t first = a.offset + (a.position ? *a.position : 0);
   float x[VEC], r[VEC];
   const bool whole = WIDE && i0 + VEC <= a.n;
   if (whole) {
@@ -58,7 +59,7 @@ __global__ void __launch_bounds__(256) dropout(DropArgs a) {
 #pragma unroll
   for (int q = 0; q < VEC / 4; ++q) {
     uint32_t w[4];
-    philox7(a.offset + (uint64_t)(i0 / 4 + q), a.key0, a.key1, w);
+    philox7(first + (uint64_t)(i0 / 4 + q), a.key0, a.key1, w);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       // a select, so that a dropped infinity or NaN leaves zero

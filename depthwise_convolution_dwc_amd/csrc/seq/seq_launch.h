@@ -42,6 +42,7 @@ struct DropArgs {
   void* y;
   int64_t n;
   uint64_t offset;
+  const uint64_t* position;  // added to offset where the kernel runs; may be null
   uint32_t key0, key1;
   uint32_t threshold;
   int drop_all;

@@ -25,6 +25,7 @@ causal depthwise convolution.
 
 from __future__ import annotations
 
+import itertools
 import math
 from typing import NamedTuple, Optional, Tuple, Union
 
@@ -220,11 +221,14 @@ class LayerNorm(torch.nn.Module):
 
 class DropoutFunction(torch.autograd.Function):
     """``sequence.dropout``: the mask is made again from (seed, offset) in the
-    backward pass, nothing is saved."""
+    backward pass, nothing is saved but an offset in device memory."""
 
     @staticmethod
     def forward(ctx, x, p, seed, offset, residual):
         ctx.key = (p, seed, offset)
+        if isinstance(offset, torch.Tensor):
+            ctx.key = (p, seed)
+            ctx.save_for_backward(offset)
         ctx.residual = residual is not None
         return sequence.dropout(x, p, seed, offset, residual=residual)
 
@@ -232,14 +236,15 @@ class DropoutFunction(torch.autograd.Function):
     def backward(ctx, gy):
         gx = None
         if ctx.needs_input_grad[0]:
-            gx = sequence.dropout(gy.contiguous(), *ctx.key)
+            gx = sequence.dropout(gy.contiguous(), *ctx.key, *ctx.saved_tensors)
         return gx, None, None, None, gy if ctx.residual else None
 
 
-def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0,
+def dropout(x: torch.Tensor, p: float, seed: int, offset: Union[int, torch.Tensor] = 0,
             residual: Optional[torch.Tensor] = None) -> torch.Tensor:
     """residual + (kept ? x / (1 - p) : 0) with autograd; the mask is a
-    function of (seed, offset, element index)."""
+    function of (seed, offset, element index).  An offset in device memory
+    must keep its value until the backward pass."""
     return DropoutFunction.apply(x.contiguous(), p, seed, offset,
                                  residual.contiguous() if residual is not None else None)
 
@@ -282,6 +287,9 @@ class MixerState(NamedTuple):
     states: torch.Tensor
 
 
+_seeds = itertools.count()
+
+
 class GatedDeltaMixer(torch.nn.Module):
     """A residual sequence layer on b x l x channels:
 
@@ -293,13 +301,21 @@ class GatedDeltaMixer(torch.nn.Module):
 
     ``forward`` takes whole sequences (``lengths`` where they are unequal: y
     past a length is x) and returns (y, MixerState); ``step`` takes one token
-    of each sequence and updates the state in place.  Dropout is active in
-    training; its masks are a function of ``seed`` and of how many elements
-    earlier calls covered."""
+    of each sequence and updates the state in place.
+
+    Dropout is active in training; its masks are a function of ``seed`` (by
+    default a number that no other layer of the process has) and of how many
+    elements earlier calls covered.  That count is ``position``, a buffer on
+    the device: it is saved with the parameters, and a captured step counts on
+    with each replay.  A call that is recomputed in the backward pass
+    (activation checkpointing) has to name its masks: ``forward(..., offset)``
+    takes them there, from an int or an int64 value in device memory, and
+    leaves the count alone; later calls are independent at offsets at least
+    (numel + 3) // 4 apart."""
 
     def __init__(self, channels: int, heads: int, key_heads: Optional[int] = None,
                  key_dim: int = 128, value_dim: int = 128, kernel_size: int = 4,
-                 p: float = 0.0, seed: int = 0, eps: float = 1e-5, device=None,
+                 p: float = 0.0, seed: Optional[int] = None, eps: float = 1e-5, device=None,
                  dtype=torch.float32):
         super().__init__()
         key_heads = heads if key_heads is None else key_heads
@@ -313,8 +329,9 @@ class GatedDeltaMixer(torch.nn.Module):
             raise ValueError("p must be 0..1")
         self.heads, self.key_heads = int(heads), int(key_heads)
         self.key_dim, self.value_dim = int(key_dim), int(value_dim)
-        self.kernel_size, self.p, self.seed = int(kernel_size), float(p), int(seed)
-        self.offset = 0
+        self.kernel_size, self.p = int(kernel_size), float(p)
+        self.seed = next(_seeds) if seed is None else int(seed)
+        self.register_buffer("position", torch.zeros((), dtype=torch.int64, device=device))
         nk, nv = self.key_heads * self.key_dim, self.heads * self.value_dim
         self.mixed = 2 * nk + nv
         kw = dict(device=device, dtype=dtype)
@@ -329,6 +346,20 @@ class GatedDeltaMixer(torch.nn.Module):
         f32 = dict(device=device, dtype=torch.float32)
         self.a = torch.nn.Parameter(torch.zeros(self.heads, **f32))
         self.g_bias = torch.nn.Parameter(torch.zeros(self.heads, **f32))
+
+    @property
+    def offset(self) -> int:
+        """The value of ``position``: where the next call's masks begin."""
+        return int(self.position)
+
+    @offset.setter
+    def offset(self, value: int) -> None:
+        self.position.fill_(int(value))
+
+    def _load_from_state_dict(self, state_dict, prefix, *args):
+        # a state saved without the count leaves it as it is
+        state_dict.setdefault(prefix + "position", self.position)
+        super()._load_from_state_dict(state_dict, prefix, *args)
 
     def _rates(self, h):
         r = self.w_rate(h).float()
@@ -345,17 +376,23 @@ class GatedDeltaMixer(torch.nn.Module):
         v = c[..., 2 * nk:].unflatten(-1, (self.heads, self.value_dim)).to(dt)
         return qk[..., :self.key_heads, :], qk[..., self.key_heads:, :], v
 
-    def _out(self, x, h, o):
+    def _out(self, x, h, o, offset=None):
         y = self.w_out(self.out_norm(o).flatten(-2) * F.silu(self.w_gate(h)))
         y = y.to(x.dtype)
         if not self.training or self.p == 0.0:
             return x + y
-        offset = self.offset
-        self.offset += (y.numel() + 3) // 4
+        if offset is None:
+            if torch._C._current_graph_task_id() != -1:
+                raise RuntimeError("a call recomputed in the backward pass would take other "
+                                   "dropout masks than the first one did: give both an offset")
+            offset = self.position.clone()
+            self.position += (y.numel() + 3) // 4
         return dropout(y, self.p, self.seed, offset, residual=x)
 
     def forward(self, x: torch.Tensor, state: Optional[MixerState] = None,
-                lengths: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, MixerState]:
+                lengths: Optional[torch.Tensor] = None,
+                offset: Union[int, torch.Tensor, None] = None
+                ) -> Tuple[torch.Tensor, MixerState]:
         b, n, _ = x.shape
         h = self.norm(x, self.w_in.weight.dtype)
         m, taps = self.w_in(h), self.kernel_size - 1
@@ -366,7 +403,7 @@ class GatedDeltaMixer(torch.nn.Module):
         g, beta = self._rates(h)
         o, s1 = delta_rule(*self._heads(c), g, beta, state.states if state is not None else None,
                            lengths)
-        y = self._out(x, h, o)
+        y = self._out(x, h, o, offset)
         if lengths is None:
             return y, MixerState(m[:, n:].contiguous(), s1)
         ends = lengths.clamp(0, n).long()

@@ -14,7 +14,7 @@ import contextlib
 import ctypes
 import math
 import struct
-from typing import Optional, Tuple
+from typing import Optional, Tuple, Union
 
 import torch
 
@@ -68,6 +68,7 @@ def bind(l: ctypes.CDLL) -> None:
     l.dwc_layer_norm_bwd_workspace_size.argtypes = [vp, ctypes.POINTER(sz)]
     l.dwc_layer_norm_bwd.argtypes = [vp] * 10 + [sz, vp]
     l.dwc_dropout.argtypes = [vp] * 5
+    l.dwc_dropout_at.argtypes = [vp] * 6
     l.dwc_delta_step.argtypes = [vp] * 11
     l.dwc_delta_workspace_size.argtypes = [vp, ctypes.c_int, ctypes.POINTER(sz)]
     l.dwc_delta_fwd.argtypes = [vp] * 11 + [sz, vp]
@@ -216,19 +217,27 @@ def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: 
     return dx, dw, db
 
 
-def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0,
+def dropout(x: torch.Tensor, p: float, seed: int, offset: Union[int, torch.Tensor] = 0,
             residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
             stream=None) -> torch.Tensor:
     """residual + (kept ? x / (1 - p) : 0), the mask a function of (seed,
     offset, element index).  The gradient of x is this call on dy with the
     same p, seed and offset; elements of later calls that must not share a
-    mask take an offset at least (numel + 3) // 4 further."""
+    mask take an offset at least (numel + 3) // 4 further.  An offset may be
+    one int64 value in device memory, which is read when the kernel runs: a
+    captured call then takes a new one with each replay."""
     index = _device_tensor(x, "x", _TYPES)
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
     if residual is not None:
         _device_tensor(residual, "residual", (x.dtype,), index)
         _dense(residual, "residual", x.shape)
+    at = None
+    if isinstance(offset, torch.Tensor):
+        at, offset = offset, 0
+        _device_tensor(at, "offset", (torch.int64,), index)
+        if at.numel() != 1:
+            raise ValueError("offset must be one value")
     if not 0 <= int(seed) < 1 << 64 or not 0 <= int(offset) < 1 << 64:
         raise ValueError("seed and offset must be in 0 .. 2^64 - 1")
     if out is not None:
@@ -240,7 +249,11 @@ def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0,
         if y is None:
             y = torch.empty_like(x, memory_format=_DENSE)
         s = _raw(stream, index, y if out is None else None)
-        _raise(lib().dwc_dropout(d, x.data_ptr(), _ptr(residual), y.data_ptr(), s))
+        if at is None:
+            _raise(lib().dwc_dropout(d, x.data_ptr(), _ptr(residual), y.data_ptr(), s))
+        else:
+            _raise(lib().dwc_dropout_at(d, x.data_ptr(), _ptr(residual), y.data_ptr(),
+                                        at.data_ptr(), s))
     return y
 
 

@@ -323,6 +323,13 @@ typedef struct {
 int dwc_dropout(const dwc_dropout_problem* p, const void* x,
                 const void* residual, void* y, void* stream);
 
+/* The same with *position, in device memory, added to the problem's offset
+ * (modulo 2^64).  It is read when the kernel runs: a call captured into a
+ * graph takes the value of each replay. */
+int dwc_dropout_at(const dwc_dropout_problem* p, const void* x,
+                   const void* residual, void* y, const uint64_t* position,
+                   void* stream);
+
 /* The gated delta rule.  Per sequence and value head, with a state S of
  * dk x dv that starts at s0 (or zero), a_t = exp(g_t):
  *   u_t = beta_t (v_t - (a_t S_{t-1})^T k_t),  S_t = a_t S_{t-1} + k_t u_t^T,

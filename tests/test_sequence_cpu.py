@@ -207,3 +207,12 @@ def test_delta_chunked_launch_range(change):
     p = delta(**change)
     f = dwc.lib().dwc_delta_workspace_size
     assert [f(ctypes.byref(p), op, ctypes.byref(need)) for op in (0, 1)] == [UNSUPPORTED] * 2
+
+
+def test_dropout_position_refused():
+    p, f = seq.DropoutProblem(16, 0.5, 1, 0, 0, 0), dwc.lib().dwc_dropout_at
+    a = (ctypes.byref(p), at(0), None, at(1))
+    assert f(*a, None, None) == BAD
+    assert f(*a, at(2, 4), None) == MISALIGNED
+    assert f(*a, at(1, 56), None) == ALIAS
+    assert f(None, at(0), None, at(1), at(2), None) == BAD
