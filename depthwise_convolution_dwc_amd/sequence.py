@@ -4,8 +4,10 @@ torch tensors.  Argument marshalling only, like the package's other calls;
 the formulas stand in include/dwc.h.
 
 Every call runs on the current stream of the tensors' device, or on
-``stream``; outputs and workspaces that a call allocates are then recorded
-on that stream, so that the allocator does not hand them out too early.
+``stream``.  What a call allocates comes from the memory of the stream that
+it runs on, and outputs are recorded on the current one too, so that the
+allocator does not hand a block out while either stream has work on it; the
+caller orders the two streams' work on the tensors themselves.
 """
 
 from __future__ import annotations
@@ -78,21 +80,31 @@ def bind(l: ctypes.CDLL) -> None:
 _HERE = contextlib.nullcontext()
 
 
-def _on(index):
-    """The device made current, if it is not."""
-    return _HERE if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
-
-
-def _raw(stream, index, *made):
-    """The stream to launch on; tensors allocated here are marked as used on
-    a stream given."""
+def _on(index, stream):
+    """The device made current, if it is not; with a stream given, that
+    stream."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(index)
-    s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
-    for t in made:
-        if t is not None:
-            t.record_stream(s)
-    return s.cuda_stream
+        return _HERE if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=index)
+    if stream.device_index != index:
+        raise ValueError(f"stream must be one of cuda:{index}, got cuda:{stream.device_index}")
+    return torch.cuda.stream(stream)
+
+
+def _raw(index):
+    """The current stream's handle."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _returned(stream, index, *made):
+    """Tensors allocated on a stream given are marked as used on the current
+    one, where the caller drops them."""
+    if stream is not None:
+        here = torch.cuda.current_stream(index)
+        for t in made:
+            if t is not None:
+                t.record_stream(here)
 
 
 def _device_tensor(t, name, dtypes, index=None):
@@ -173,15 +185,15 @@ def layer_norm(x: torch.Tensor, w: Optional[torch.Tensor] = None,
         raise TypeError(f"out_dtype must be one of {_TYPES}, got {out_dtype}")
     p = _NORM(x.numel() // c, c, _row_stride(x, "x"), c, _DTYPE_CODE[x.dtype],
               _DTYPE_CODE[out_dtype], wt, eps)
-    with _on(index):
+    with _on(index, stream):
         y = out
         if y is None:
             y = torch.empty_like(x, dtype=out_dtype, memory_format=_DENSE)
         mean = x.new_empty(lead, dtype=torch.float32)
         rstd = torch.empty_like(mean)
-        s = _raw(stream, index, y if out is None else None, mean, rstd)
         _raise(lib().dwc_layer_norm(p, x.data_ptr(), _ptr(w), _ptr(b), y.data_ptr(),
-                                    mean.data_ptr(), rstd.data_ptr(), s))
+                                    mean.data_ptr(), rstd.data_ptr(), _raw(index)))
+    _returned(stream, index, y if out is None else None, mean, rstd)
     return y, mean, rstd
 
 
@@ -203,17 +215,18 @@ def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: 
     wt = _weights(w, None, c, index)
     p = _NORM(x.numel() // c, c, _row_stride(x, "x"), _row_stride(dy, "dy"),
               _DTYPE_CODE[x.dtype], _DTYPE_CODE[dy.dtype], wt, 0.0)
-    with _on(index):
+    with _on(index, stream):
         need = ctypes.c_size_t()
         _raise(lib().dwc_layer_norm_bwd_workspace_size(p, ctypes.byref(need)))
         ws = x.new_empty(need.value, dtype=torch.uint8)
         dx = torch.empty_like(x, memory_format=_DENSE)
         dw = x.new_empty(c, dtype=torch.float32)
         db = torch.empty_like(dw)
-        s = _raw(stream, index, ws, dx, dw, db)
         _raise(lib().dwc_layer_norm_bwd(p, dy.data_ptr(), x.data_ptr(), mean.data_ptr(),
                                         rstd.data_ptr(), _ptr(w), dx.data_ptr(), dw.data_ptr(),
-                                        db.data_ptr(), ws.data_ptr(), need.value, s))
+                                        db.data_ptr(), ws.data_ptr(), need.value,
+                                        _raw(index)))
+    _returned(stream, index, dx, dw, db)
     return dx, dw, db
 
 
@@ -244,16 +257,17 @@ def dropout(x: torch.Tensor, p: float, seed: int, offset: Union[int, torch.Tenso
         _device_tensor(out, "out", (x.dtype,), index)
         _dense(out, "out", x.shape)
     d = _DROPOUT(x.numel(), p, int(seed), int(offset), _DTYPE_CODE[x.dtype], 0)
-    with _on(index):
+    with _on(index, stream):
         y = out
         if y is None:
             y = torch.empty_like(x, memory_format=_DENSE)
-        s = _raw(stream, index, y if out is None else None)
+        s = _raw(index)
         if at is None:
             _raise(lib().dwc_dropout(d, x.data_ptr(), _ptr(residual), y.data_ptr(), s))
         else:
             _raise(lib().dwc_dropout_at(d, x.data_ptr(), _ptr(residual), y.data_ptr(),
                                         at.data_ptr(), s))
+    _returned(stream, index, y if out is None else None)
     return y
 
 
@@ -320,15 +334,15 @@ def delta_rule_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.
     if out_state is not None:
         _device_tensor(out_state, "out_state", _F32, index)
         _dense(out_state, "out_state", states)
-    with _on(index):
+    with _on(index, stream):
         o = torch.empty_like(v, memory_format=_DENSE)
         s1 = out_state
         if s1 is None:
             s1 = g.new_empty(states)
-        s = _raw(stream, index, o, s1 if out_state is None else None)
         _raise(lib().dwc_delta_step(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
                                     beta.data_ptr(), _ptr(s0), _ptr(lengths), o.data_ptr(),
-                                    s1.data_ptr(), s))
+                                    s1.data_ptr(), _raw(index)))
+    _returned(stream, index, o, s1 if out_state is None else None)
     return o, s1
 
 
@@ -344,14 +358,14 @@ def delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
     None.  o: b x l x hv x dv of v's dtype; s1: the states after the last
     token.  scale defaults to 1 / sqrt(dk)."""
     p, index, states = _delta(q, k, v, g, beta, s0, lengths, scale)
-    with _on(index):
+    with _on(index, stream):
         ws, need = _workspace(p, DELTA_FWD, q)
         o = torch.empty_like(v, memory_format=_DENSE)
         s1 = g.new_empty(states)
-        s = _raw(stream, index, ws, o, s1)
         _raise(lib().dwc_delta_fwd(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
                                    beta.data_ptr(), _ptr(s0), _ptr(lengths), o.data_ptr(),
-                                   s1.data_ptr(), ws.data_ptr(), need, s))
+                                   s1.data_ptr(), ws.data_ptr(), need, _raw(index)))
+    _returned(stream, index, o, s1)
     return o, s1
 
 
@@ -365,7 +379,7 @@ def delta_rule_bwd(dout: torch.Tensor, ds1: Optional[torch.Tensor], q: torch.Ten
     if ds1 is not None:
         _device_tensor(ds1, "ds1", _F32, index)
         _dense(ds1, "ds1", states)
-    with _on(index):
+    with _on(index, stream):
         ws, need = _workspace(p, DELTA_BWD, q)
         dq = torch.empty_like(q, memory_format=_DENSE)
         dk = torch.empty_like(q, memory_format=_DENSE)
@@ -373,12 +387,12 @@ def delta_rule_bwd(dout: torch.Tensor, ds1: Optional[torch.Tensor], q: torch.Ten
         dg = torch.empty_like(g, memory_format=_DENSE)
         dbeta = torch.empty_like(g, memory_format=_DENSE)
         ds0 = torch.empty_like(s0) if s0 is not None else None
-        s = _raw(stream, index, ws, dq, dk, dv, dg, dbeta, ds0)
         _raise(lib().dwc_delta_bwd(p, dout.data_ptr(), _ptr(ds1), q.data_ptr(), k.data_ptr(),
                                    v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(s0),
                                    _ptr(lengths), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
                                    dg.data_ptr(), dbeta.data_ptr(), _ptr(ds0), ws.data_ptr(),
-                                   need, s))
+                                   need, _raw(index)))
+    _returned(stream, index, dq, dk, dv, dg, dbeta, ds0)
     return dq, dk, dv, dg, dbeta, ds0
 
 
