@@ -107,6 +107,12 @@ def _returned(stream, index, *made):
                 t.record_stream(here)
 
 
+def _written(t):
+    """A tensor that was given to be written: graphs that saved it know."""
+    if t is not None and not t.is_inference():
+        torch.autograd.graph.increment_version(t)
+
+
 def _device_tensor(t, name, dtypes, index=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -194,6 +200,7 @@ def layer_norm(x: torch.Tensor, w: Optional[torch.Tensor] = None,
         _raise(lib().dwc_layer_norm(p, x.data_ptr(), _ptr(w), _ptr(b), y.data_ptr(),
                                     mean.data_ptr(), rstd.data_ptr(), _raw(index)))
     _returned(stream, index, y if out is None else None, mean, rstd)
+    _written(out)
     return y, mean, rstd
 
 
@@ -268,6 +275,7 @@ def dropout(x: torch.Tensor, p: float, seed: int, offset: Union[int, torch.Tenso
             _raise(lib().dwc_dropout_at(d, x.data_ptr(), _ptr(residual), y.data_ptr(),
                                         at.data_ptr(), s))
     _returned(stream, index, y if out is None else None)
+    _written(out)
     return y
 
 
@@ -343,6 +351,7 @@ def delta_rule_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.
                                     beta.data_ptr(), _ptr(s0), _ptr(lengths), o.data_ptr(),
                                     s1.data_ptr(), _raw(index)))
     _returned(stream, index, o, s1 if out_state is None else None)
+    _written(out_state)
     return o, s1
 
 
