@@ -25,6 +25,7 @@ causal depthwise convolution.
 
 from __future__ import annotations
 
+import functools
 import itertools
 import math
 from typing import NamedTuple, Optional, Tuple, Union
@@ -170,9 +171,26 @@ class DepthwiseConv2d(torch.nn.Module):
                 f"padding={self.padding}, layout={self.layout!r}")
 
 
+class _Gradients(torch.autograd.Function):
+    """A call that makes gradients and has none of its own: a second
+    derivative that needs them raises, on whatever path it comes."""
+
+    @staticmethod
+    def forward(ctx, call, *tensors):
+        return call(*tensors)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("layer_norm and delta_rule are differentiable once")
+
+
+def _gradients(call, *tensors):
+    return _Gradients.apply(call, *tensors) if torch.is_grad_enabled() else call(*tensors)
+
+
 class LayerNormFunction(torch.autograd.Function):
     """``sequence.layer_norm`` and its gradients; mean and rstd are kept, the
-    normalised rows are computed again."""
+    normalised rows are computed again.  Differentiable once."""
 
     @staticmethod
     def forward(ctx, x, w, b, eps, out_dtype):
@@ -184,7 +202,7 @@ class LayerNormFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, gy):
         x, w, mean, rstd = ctx.saved_tensors
-        dx, dw, db = sequence.layer_norm_bwd(gy.contiguous(), x, mean, rstd, w)
+        dx, dw, db = _gradients(sequence.layer_norm_bwd, gy.contiguous(), x, mean, rstd, w)
         return (dx, dw.to(w.dtype) if w is not None else None,
                 db.to(ctx.b_dtype) if ctx.b_dtype is not None else None, None, None)
 
@@ -236,7 +254,8 @@ class DropoutFunction(torch.autograd.Function):
     def backward(ctx, gy):
         gx = None
         if ctx.needs_input_grad[0]:
-            gx = sequence.dropout(gy.contiguous(), *ctx.key, *ctx.saved_tensors)
+            # (differentiable again: the same linear map)
+            gx = dropout(gy, *ctx.key, *ctx.saved_tensors)
         return gx, None, None, None, gy if ctx.residual else None
 
 
@@ -250,7 +269,8 @@ def dropout(x: torch.Tensor, p: float, seed: int, offset: Union[int, torch.Tenso
 
 
 class DeltaRuleFunction(torch.autograd.Function):
-    """``sequence.delta_rule`` and its gradients; only the inputs are saved."""
+    """``sequence.delta_rule`` and its gradients; only the inputs are saved.
+    Differentiable once."""
 
     @staticmethod
     def forward(ctx, q, k, v, g, beta, s0, lengths, scale):
@@ -265,8 +285,8 @@ class DeltaRuleFunction(torch.autograd.Function):
         do = torch.zeros_like(v, memory_format=torch.contiguous_format) if do is None \
             else do.contiguous()
         ds1 = ds1.contiguous() if ds1 is not None else None
-        return sequence.delta_rule_bwd(do, ds1, q, k, v, g, beta, s0, lengths,
-                                       ctx.scale) + (None, None)
+        return _gradients(functools.partial(sequence.delta_rule_bwd, scale=ctx.scale), do, ds1,
+                          q, k, v, g, beta, s0, lengths) + (None, None)
 
 
 def delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,

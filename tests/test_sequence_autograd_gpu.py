@@ -1,5 +1,5 @@
 """The sequence operators under autograd's rules: no buffer is changed behind
-a graph that saved it."""
+a graph that saved it, no second derivative vanishes silently."""
 
 import pytest
 
@@ -58,3 +58,28 @@ def test_outputs_given_without_autograd():
         s = a[5].clone()
         o, s1 = dwc.delta_rule_step(*a[:5], s, out_state=s)
         assert s1 is s and torch.equal(s, dwc.delta_rule_step(*a)[1])
+
+
+def second(out, leaf):
+    """The gradient of a penalty on a gradient."""
+    g = torch.autograd.grad(out.square().sum(), leaf, create_graph=True)[0]
+    return torch.autograd.grad(g.square().sum() + leaf.sum(), leaf)[0]
+
+
+def test_second_derivatives():
+    x, w = randn(1, 6, 40).requires_grad_(), randn(2, 40)
+    with pytest.raises(RuntimeError, match="differentiable once"):
+        second(dnn.layer_norm(x, w), x)
+    a = [t.clone().requires_grad_() for t in delta_inputs(4, 1, 5, 1, 1, 8, 8, F32)]
+    with pytest.raises(RuntimeError, match="differentiable once"):
+        second(dnn.delta_rule(*a)[0], a[2])
+    # y = 2 x where kept: the gradient is 8 x there, its penalty's 128 x + 1
+    x, r = randn(3, 50).requires_grad_(), randn(5, 50)
+    kept = dwc.dropout(torch.ones_like(x), 0.5, 7).bool()
+    want = torch.where(kept, 128 * x.detach() + 1, 1.0)
+    assert torch.equal(second(dnn.dropout(x, 0.5, 7), x), want)
+    at = torch.zeros((), dtype=torch.int64, device="cuda")
+    assert torch.equal(second(dnn.dropout(x, 0.5, 7, at), x), want)
+    y = dnn.dropout(x, 0.5, 7, residual=r)
+    g = torch.autograd.grad(y, x, torch.ones_like(y), create_graph=True)[0]
+    assert torch.equal(g, 2.0 * kept)
