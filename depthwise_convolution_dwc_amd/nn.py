@@ -425,7 +425,8 @@ class GatedDeltaMixer(torch.nn.Module):
                            lengths)
         y = self._out(x, h, o, offset)
         if lengths is None:
-            return y, MixerState(m[:, n:].contiguous(), s1)
+            # (a copy also where one sequence's part is contiguous as it is)
+            return y, MixerState(m[:, n:].clone(memory_format=torch.contiguous_format), s1)
         ends = lengths.clamp(0, n).long()
         live = (torch.arange(n, device=x.device) < ends[:, None])[..., None]
         at = ends[:, None] + torch.arange(taps, device=x.device)
