@@ -414,7 +414,13 @@ class GatedDeltaMixer(torch.nn.Module):
                 offset: Union[int, torch.Tensor, None] = None
                 ) -> Tuple[torch.Tensor, MixerState]:
         b, n, _ = x.shape
-        h = self.norm(x, self.w_in.weight.dtype)
+        seen = x
+        if lengths is not None:
+            ends = lengths.clamp(0, n).long()
+            live = (torch.arange(n, device=x.device) < ends[:, None])[..., None]
+            # what stands past a length is not used, not even times a zero gradient
+            seen = torch.where(live, x, 0.0)
+        h = self.norm(seen, self.w_in.weight.dtype)
         m, taps = self.w_in(h), self.kernel_size - 1
         past = state.taps if state is not None else m.new_zeros(b, taps, self.mixed)
         m = torch.cat([past, m], 1)
@@ -427,8 +433,6 @@ class GatedDeltaMixer(torch.nn.Module):
         if lengths is None:
             # (a copy also where one sequence's part is contiguous as it is)
             return y, MixerState(m[:, n:].clone(memory_format=torch.contiguous_format), s1)
-        ends = lengths.clamp(0, n).long()
-        live = (torch.arange(n, device=x.device) < ends[:, None])[..., None]
         at = ends[:, None] + torch.arange(taps, device=x.device)
         kept = m.gather(1, at[..., None].expand(-1, -1, self.mixed))
         return torch.where(live, y, x), MixerState(kept, s1)
