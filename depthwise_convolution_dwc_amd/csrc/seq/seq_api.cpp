@@ -79,6 +79,9 @@ int check_norm(const dwc_norm_problem* p, bool bwd) {
   // a launch has fewer than 2^32 threads; the widest rows take 1024 each
   if (p->rows > (p->c > 512 ? (int64_t)1 << 22 : (int64_t)1 << 26) - 1)
     return fail(DWC_ERR_UNSUPPORTED, "layer norm rows past the launch range");
+  // and the sums of dw and db take 64 a column
+  if (bwd && p->c >= (int64_t)1 << 25)
+    return fail(DWC_ERR_UNSUPPORTED, "layer norm columns past the launch range");
   return DWC_OK;
 }
 

@@ -293,7 +293,7 @@ int dwc_layer_norm(const dwc_norm_problem* p, const void* x, const void* w,
                    const void* b, void* y, float* mean, float* rstd,
                    void* stream);
 
-/* Bytes of workspace dwc_layer_norm_bwd needs (column partials). */
+/* Bytes of workspace dwc_layer_norm_bwd needs (column partials); c < 2^25. */
 int dwc_layer_norm_bwd_workspace_size(const dwc_norm_problem* p, size_t* bytes);
 
 /* dx: rows x c, dense; dw, db: c fp32 values (either may be NULL), summed

@@ -216,3 +216,15 @@ def test_dropout_position_refused():
     assert f(*a, at(2, 4), None) == MISALIGNED
     assert f(*a, at(1, 56), None) == ALIAS
     assert f(None, at(0), None, at(1), at(2), None) == BAD
+
+
+def test_norm_bwd_columns_past_the_launch_range():
+    """The columns' sums take 64 threads each of a launch's 2^32."""
+    need, f = ctypes.c_size_t(), dwc.lib().dwc_layer_norm_bwd
+    size = dwc.lib().dwc_layer_norm_bwd_workspace_size
+    for c, status in (((1 << 25) - 1, 0), (1 << 25, UNSUPPORTED), (1 << 30, UNSUPPORTED)):
+        p = ctypes.byref(norm(rows=2, c=c, xs=c, ds=c))
+        assert size(p, ctypes.byref(need)) == status
+        if status:
+            far = [i << 40 for i in range(1, 10)]
+            assert f(p, *far[:8], far[8], 1 << 40, None) == status and dwc.last_error()
