@@ -17,10 +17,11 @@
 // pairs (hi hi + hi lo + lo hi, summed in fp32 by the instruction) is off by
 // about 2^-23 of its size, as an fp32 product is.  The scale 2^s brings the
 // largest magnitude of the operand (a column of a state, a whole tile of the
-// others) to 2^14..2^15: values down to 2^-29 of the largest keep all bits
-// and smaller ones an absolute error of 2^-40 of the largest.  bf16 and fp16
-// inputs are exact in one fp16 number at such a scale.  States, sums and
-// statistics stay fp32.
+// others) to 2^14..2^15.  hi then keeps 11 bits down to 2^-28 of the largest,
+// and lo, a multiple of 2^-24, the other 11 down to about 2^-17 of it: below
+// that a pair is off by at most 2^-39 of the largest.  fp16 inputs, and bf16
+// ones down to 2^-31 of the largest, are exact in one fp16 number.  States,
+// sums and statistics stay fp32.
 #pragma once
 
 #include "seq_delta.h"

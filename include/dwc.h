@@ -351,7 +351,10 @@ int dwc_dropout_at(const dwc_dropout_problem* p, const void* x,
  * NaN in a live token may turn outputs of earlier tokens of its chunk of 64
  * into NaN.  Magnitudes do not matter to them while an operand's largest (of
  * q, k, v, dout in a chunk, of a column of a state) is above 1e-30 and the
- * results are above 1e-33; smaller ones lose bits. */
+ * results are above 1e-33; smaller ones lose bits.  Inside a chunk a value
+ * takes part with 22 bits, or with an error of 2^-39 of its operand's largest
+ * where that is more: tokens that differ by more than 2^17 in size do not
+ * keep all bits of the small ones. */
 typedef struct {
     int64_t b, l;           /* sequences and tokens, >= 0                   */
     int64_t q_stride[3], k_stride[3], v_stride[3], g_stride[3],

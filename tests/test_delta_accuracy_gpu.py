@@ -1,7 +1,8 @@
 """What single values of the chunked gated delta rule and of its gradients are
 worth: outputs of 16 bits before they are rounded, the gradient of every
-decay, small magnitudes.  Norms of whole outputs are tested in test_delta_gpu.py, whose F
-bounds an output's error before its rounding as a share of its 2-norm.
+decay, small magnitudes, small tokens beside large ones.  Norms of whole
+outputs are tested in test_delta_gpu.py, whose F bounds an output's error
+before its rounding as a share of its 2-norm.
 """
 
 import pytest
@@ -14,7 +15,7 @@ if not torch.cuda.is_available():
 
 from gpu_helpers import dwc, log, sync  # noqa: E402
 from test_delta_gpu import F, TOL, check, wanted  # noqa: E402
-from test_sequence_gpu import BF16, F16, F32, delta_inputs, randn, rel  # noqa: E402
+from test_sequence_gpu import BF16, F16, F32, delta_inputs, half, randn, rel  # noqa: E402
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
@@ -129,3 +130,36 @@ def test_one_of_queries_and_keys_small_or_zero(dtype, which):
         a = list(delta_inputs(9, 1, 150, 1, 2, 64, 40, dtype))
         a[which] = a[which] * f if which == 0 else a[which] * min(f, 1.0)
         check(a)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [(1, 128, 1, 2, 64, 64), (1, 150, 2, 2, 128, 128),
+                                   (2, 100, 1, 2, 40, 24)])
+def test_tokens_of_different_magnitudes(dtype, shape):
+    """q, k, v and dout scaled by a power of two of 2^-24..1 for each token
+    and checked token by token: operands have 22 bits down to 2^-17 of the
+    largest of a chunk and that absolute error below it, so an output is off
+    by F of its terms' size, or by F 2^-17 of the largest token's.  Terms are
+    sums of up to 128 products of either sign: their size is up to 12 times
+    the output's norm."""
+    log(f"case magnitudes {dtype} {shape}")
+    a = list(delta_inputs(sum(shape), *shape, dtype))
+    b, n, hk, hv, dk, dv = shape
+    dout, ds1 = randn(9, b, n, hv, dv, dtype=dtype), randn(10, b, hv, dk, dv, scale=0.1)
+    gen = torch.Generator().manual_seed(11)
+
+    def spread(t):
+        return t * 2.0 ** -torch.randint(0, 25, (b, n, 1, 1), generator=gen).cuda().to(dtype)
+
+    a[0], a[1], a[2], dout = (spread(t) for t in (a[0], a[1], a[2], dout))
+    got = dwc.delta_rule(*a)[:1] + dwc.delta_rule_bwd(dout, ds1, *a)[:3]
+    sync()
+    wo, _, wg = wanted(a, dout, ds1)
+    for name, g, w in zip(("o", "dq", "dk", "dv"), got, [wo] + list(wg[:3])):
+        off, size = (g.double() - w).norm(dim=-1), w.norm(dim=-1)
+        # the largest token of a head in its chunk
+        top = torch.stack([size[:, t // 64 * 64:t // 64 * 64 + 64].amax(1) for t in range(n)], 1)
+        bound = 12 * F * (size + 2.0 ** -17 * top) + half(g.dtype) * (g.dtype != F32) * size
+        worst = (off / bound).max().item()
+        log(f"{name}: {worst:.3g} of the bound")
+        assert torch.isfinite(g).all() and worst <= 1.0, (name, worst)
