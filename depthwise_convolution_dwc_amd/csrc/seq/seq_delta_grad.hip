@@ -24,10 +24,10 @@
 // memory to exactly one wave's registers; the operands that all waves share
 // lie in LDS.
 //
-// Bound: waits, at two waves a SIMD.  MI355X, 8x2048 tokens of 16 heads,
-// 128x128 states, bf16: 446 us; moving its 0.8 GB would take 165 us.  Twice
-// the waves took 396 us, with registers spilled to memory, which no kernel
-// here does.
+// Bound: waits (57% of the waves' time), at two waves a SIMD.  MI355X, 8x2048
+// tokens of 16 heads, 128x128 states, bf16: 510 us; moving its 1.2 GB would
+// take 250 us.  (With q . dq - v . dv for dg 446 us; that form with twice the
+// waves 396 us, with registers spilled to memory, which no kernel here does.)
 #include "../dwc_device.h"
 #include "seq_chunk.h"
 

@@ -12,16 +12,16 @@
 // refilled for the next chunk once this chunk is done with it, so that no
 // exchange waits for memory.  (Issued before an exchange they hold up the
 // wave's partner, after it the products that follow: forward the former is
-// faster, 194 against 207 us at 8x2048 tokens of 16 heads; beside the stores
-// of the backward scans the latter, 455 against 505 us.)
+// faster, 194 against 207 us at 8x2048 tokens of 16 heads with one fp16
+// number an operand of o; beside the stores of the backward scans the latter,
+// 455 against 505 us.)
 //
 // Bound: the chain of products and exchanges of a chunk (a wave issues half
-// of its cycles, three quarters of that vector instructions, 13% matrix
-// ones), times the chunks of the longest sequence.  MI355X, 128x128 states,
-// bf16: 2.5 us a chunk at one workgroup a compute unit (4096 tokens of 32
-// heads: 164 us), 6 us where every SIMD has a wave with 32 columns (8x2048
-// tokens of 16 heads: 194 us; with every load and store at the first chunk,
-// 170 us).
+// of its cycles, three quarters of that vector instructions; the matrix
+// cores are busy 16% of the time), times the chunks of the longest sequence.
+// MI355X, 128x128 states, bf16: 2.8 us a chunk at one workgroup a compute unit
+// (4096 tokens of 32 heads: 181 us), 6.8 us where every SIMD has a wave with
+// 32 columns (8x2048 tokens of 16 heads: 217 us).
 #include "../dwc_device.h"
 #include "seq_chunk.h"
 
