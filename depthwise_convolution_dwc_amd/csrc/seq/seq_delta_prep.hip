@@ -7,8 +7,9 @@
 //
 // Bound: memory where chunks are many (8x2048 tokens of 16 heads, 128
 // dimensions, bf16: 134 MB in, 308 MB out in 105 us, for the backward pass
-// 442 MB out in 130 us), else one workgroup's chain of phases, 15 us.  The triangular solve by 16x16 blocks took it there
-// from 202 us with a solve row by row.
+// 442 MB out in 130 us), else one workgroup's chain of phases, 15 us.  The
+// triangular solve by 16x16 blocks took it there from 202 us with a solve row
+// by row.
 #include "../dwc_device.h"
 #include "seq_chunk.h"
 
