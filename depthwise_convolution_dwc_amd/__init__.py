@@ -40,6 +40,10 @@ EXPORTED = (
     "dwc_layer_norm", "dwc_layer_norm_bwd_workspace_size", "dwc_layer_norm_bwd", "dwc_dropout",
     "dwc_dropout_at",
     "dwc_delta_step", "dwc_delta_workspace_size", "dwc_delta_fwd", "dwc_delta_bwd",
+    "dwc_causal_conv", "dwc_causal_conv_step", "dwc_causal_conv_bwd_workspace_size",
+    "dwc_causal_conv_bwd", "dwc_scan_step", "dwc_scan_workspace_size", "dwc_scan_fwd",
+    "dwc_scan_bwd", "dwc_residual_norm", "dwc_residual_norm_bwd_workspace_size",
+    "dwc_residual_norm_bwd",
 )
 
 
@@ -91,6 +95,7 @@ def lib() -> ctypes.CDLL:
         l.dwc_bwd_filter.argtypes = [P, vp, vp, vp, vp, ctypes.c_size_t, vp]
         l.dwc_bwd_filter_noalloc.argtypes = [P, vp, vp, vp, vp]
         sequence.bind(l)
+        space.bind(l)
         for name in EXPORTED:
             if name not in ("dwc_status_string", "dwc_last_error"):
                 getattr(l, name).restype = ctypes.c_int
@@ -327,6 +332,8 @@ def bwd_filter_noalloc(x: torch.Tensor, dy: torch.Tensor, f_hw: Sequence[int], s
     return out
 
 
-from . import sequence  # noqa: E402  (needs the names above)
+from . import sequence, space  # noqa: E402  (need the names above)
 from .sequence import (delta_rule, delta_rule_bwd, delta_rule_step, dropout,  # noqa: E402,F401
                        layer_norm, layer_norm_bwd)
+from .space import (causal_conv, causal_conv_bwd, causal_conv_step, residual_norm,  # noqa: E402,F401
+                    residual_norm_bwd, selective_scan, selective_scan_bwd, selective_scan_step)

@@ -67,6 +67,14 @@ def _units():
               ["-mllvm", "-amdgpu-mfma-vgpr-form"]))
     u.append(("hip", "seq/seq_delta_grad.hip", "seq_delta_grad.o",
               ["-mllvm", "-amdgpu-mfma-vgpr-form"]))
+    # short causal convolution, selective scan and residual norm
+    u.append(("hip", "seq/seq_columns.hip", "seq_columns.o", []))
+    u.append(("hip", "seq/seq_conv.hip", "seq_conv.o", []))
+    u.append(("hip", "seq/seq_scan_fwd.hip", "seq_scan_fwd.o", []))
+    u.append(("hip", "seq/seq_scan_token.hip", "seq_scan_token.o", []))
+    u.append(("hip", "seq/seq_scan_grad.hip", "seq_scan_grad.o", []))
+    u.append(("hip", "seq/seq_resnorm.hip", "seq_resnorm.o", []))
+    u.append(("hip", "seq/seq_space_api.cpp", "seq_space_api.o", ["-x", "hip"]))
     u.append(("hip", "seq/seq_api.cpp", "seq_api.o", ["-x", "hip"]))
     u.append(("hip", "dwc_api.cpp", "dwc_api.o", ["-x", "hip"]))
     u.append(("cxx", "dwc_plan.cpp", "dwc_plan.o", []))

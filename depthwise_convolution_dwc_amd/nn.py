@@ -20,7 +20,9 @@ dtype) and returns dX and dW in the dtypes of X and W.
 
 Layer norm, dropout and the gated delta rule have autograd wrappers here too,
 and ``GatedDeltaMixer`` is the sequence layer that runs them together with a
-causal depthwise convolution.
+causal depthwise convolution.  So have the short causal convolution over
+tokens, the selective scan and the residual norm; ``SelectiveScanMixer`` and
+``SelectiveScanLayers`` run those together.
 """
 
 from __future__ import annotations
@@ -28,12 +30,12 @@ from __future__ import annotations
 import functools
 import itertools
 import math
-from typing import NamedTuple, Optional, Tuple, Union
+from typing import List, NamedTuple, Optional, Tuple, Union
 
 import torch
 import torch.nn.functional as F
 
-from . import bwd_data, bwd_filter, fwd, sequence
+from . import bwd_data, bwd_filter, fwd, sequence, space
 
 IntPair = Union[int, Tuple[int, int]]
 
@@ -181,7 +183,8 @@ class _Gradients(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, *grads):
-        raise RuntimeError("layer_norm and delta_rule are differentiable once")
+        raise RuntimeError("layer_norm, delta_rule, causal_conv, selective_scan and "
+                           "residual_norm are differentiable once")
 
 
 def _gradients(call, *tensors):
@@ -455,3 +458,268 @@ class GatedDeltaMixer(torch.nn.Module):
     def extra_repr(self) -> str:
         return (f"heads={self.heads}, key_heads={self.key_heads}, key_dim={self.key_dim}, "
                 f"value_dim={self.value_dim}, kernel_size={self.kernel_size}, p={self.p}")
+
+
+def _typed(grad, like):
+    """An fp32 gradient as the parameter's type has it."""
+    return grad.to(like.dtype) if grad is not None else None
+
+
+class CausalConvFunction(torch.autograd.Function):
+    """``space.causal_conv`` and its gradients; only the inputs are saved.
+    Differentiable once."""
+
+    @staticmethod
+    def forward(ctx, x, w, bias, s0, lengths, act):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(x, w, bias, s0, lengths)
+        ctx.act = act
+        return space.causal_conv(x, w, bias, s0, lengths, act)
+
+    @staticmethod
+    def backward(ctx, gy, gs):
+        x, w, bias, s0, lengths = ctx.saved_tensors
+        gy = torch.zeros_like(x, memory_format=torch.contiguous_format) if gy is None \
+            else gy.contiguous()
+        gs = gs.contiguous() if gs is not None else None
+        dx, dw, dbias, ds0 = _gradients(functools.partial(space.causal_conv_bwd, act=ctx.act), gy,
+                                        gs, x, w, bias, s0, lengths)
+        return dx, _typed(dw, w), _typed(dbias, bias), ds0, None, None
+
+
+def causal_conv(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                s0: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+                act: str = "none") -> Tuple[torch.Tensor, torch.Tensor]:
+    """Short causal depthwise convolution over tokens with autograd: (y, s1).
+    Shapes as ``space.causal_conv``."""
+    return CausalConvFunction.apply(x, w, bias, s0, lengths, act)
+
+
+class SelectiveScanFunction(torch.autograd.Function):
+    """``space.selective_scan`` and its gradients; only the inputs are saved.
+    Differentiable once."""
+
+    @staticmethod
+    def forward(ctx, u, delta, A, B, C, D, z, delta_bias, s0, lengths, softplus):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(u, delta, A, B, C, D, z, delta_bias, s0, lengths)
+        ctx.softplus = softplus
+        return space.selective_scan(u, delta, A, B, C, D, z, delta_bias, s0, lengths, softplus)
+
+    @staticmethod
+    def backward(ctx, gy, gs):
+        saved = ctx.saved_tensors
+        gy = torch.zeros_like(saved[0], memory_format=torch.contiguous_format) if gy is None \
+            else gy.contiguous()
+        gs = gs.contiguous() if gs is not None else None
+        return _gradients(functools.partial(space.selective_scan_bwd, softplus=ctx.softplus), gy,
+                          gs, *saved) + (None, None)
+
+
+def selective_scan(u: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                   C: torch.Tensor, D: Optional[torch.Tensor] = None,
+                   z: Optional[torch.Tensor] = None, delta_bias: Optional[torch.Tensor] = None,
+                   s0: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+                   softplus: bool = False) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The selective state space scan over whole sequences with autograd:
+    (y, s1).  Shapes as ``space.selective_scan``; A, D, delta_bias and the
+    states are fp32."""
+    return SelectiveScanFunction.apply(u, delta, A, B, C, D, z, delta_bias, s0, lengths, softplus)
+
+
+class ResidualNormFunction(torch.autograd.Function):
+    """``space.residual_norm`` and its gradients; the inputs and a value a row
+    of each norm are saved.  Differentiable once."""
+
+    @staticmethod
+    def forward(ctx, x, y, gate, scale, w_post, w_pre, eps, post, pre, act):
+        ctx.set_materialize_grads(False)
+        r, h, q1, q2 = space.residual_norm(x, y, gate, scale, w_post, w_pre, eps, post, pre, act)
+        ctx.save_for_backward(x, y, q1, q2, gate, scale, w_post, w_pre)
+        ctx.how = dict(post=post, pre=pre, act=act)
+        return r, h
+
+    @staticmethod
+    def backward(ctx, gr, gh):
+        x, y, q1, q2, gate, scale, w_post, w_pre = ctx.saved_tensors
+        if gr is None and gh is None:
+            return (None,) * 10
+        gr = gr.contiguous() if gr is not None else None
+        gh = gh.contiguous() if gh is not None else None
+        dx, dy, dgate, *sums = _gradients(functools.partial(space.residual_norm_bwd, **ctx.how),
+                                          gr, gh, x, y, q1, q2, gate, scale, w_post, w_pre)
+        return (dx, dy, dgate, *map(_typed, sums, (scale, w_post, w_pre)), None, None, None, None)
+
+
+def _rows(t):
+    """A matrix with a row stride as it is, other views made contiguous."""
+    if t is None or (t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= t.shape[1]):
+        return t
+    return t.contiguous()
+
+
+def residual_norm(x: Optional[torch.Tensor], y: torch.Tensor,
+                  gate: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                  w_post: Optional[torch.Tensor] = None, w_pre: Optional[torch.Tensor] = None,
+                  eps: float = 1e-5, post: bool = True, pre: bool = True, act: str = "none"
+                  ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """r = x + scale act(gate) norm(y) w_post and h = norm(r) w_pre over the
+    last axis with autograd: (r, h), as ``space.residual_norm``."""
+    return ResidualNormFunction.apply(_rows(x), _rows(y), _rows(gate), scale, w_post, w_pre, eps,
+                                      post, pre, act)
+
+
+def rms_norm(y: torch.Tensor, w: Optional[torch.Tensor] = None,
+             gate: Optional[torch.Tensor] = None, eps: float = 1e-5,
+             act: str = "silu") -> torch.Tensor:
+    """y / sqrt(mean(y^2) + eps) w over the last axis, times act(gate) where a
+    gate is given, with autograd."""
+    return residual_norm(None, y, gate, None, w, None, eps, pre=False, act=act)[0]
+
+
+class ScanState(NamedTuple):
+    """What a ``SelectiveScanMixer`` carries from token to token: the last
+    kernel_size - 1 inputs of its convolution (b x taps x inner) and the
+    states of the scan (b x inner x states, fp32)."""
+
+    taps: torch.Tensor
+    states: torch.Tensor
+
+
+class SelectiveScanMixer(torch.nn.Module):
+    """A selective state space mixer on b x l x channels:
+
+      x, z = h W_in;  u = SiLU(causal depthwise convolution(x))
+      low, B, C = u W_x;  delta = low W_dt
+      y = selective_scan(u, softplus(delta + bias), -exp(a), B, C, D, gate z) W_out
+
+    ``forward`` takes whole sequences (``lengths`` where they are unequal: y
+    past a length is 0) and returns (y, ScanState); ``step`` takes one or a
+    few tokens of each sequence and updates the state in place."""
+
+    def __init__(self, channels: int, inner: Optional[int] = None, states: int = 16,
+                 kernel_size: int = 4, rank: Optional[int] = None, groups: int = 1, device=None,
+                 dtype=torch.float32):
+        super().__init__()
+        self.inner = int(2 * channels if inner is None else inner)
+        self.states, self.kernel_size, self.groups = int(states), int(kernel_size), int(groups)
+        self.rank = max(1, -(-int(channels) // 16)) if rank is None else int(rank)
+        if not 1 <= self.states <= 256:
+            raise ValueError("states must be 1..256")
+        if not 1 <= self.kernel_size <= 8:
+            raise ValueError("kernel_size must be 1..8")
+        if self.groups < 1 or self.inner % self.groups:
+            raise ValueError("inner must be a multiple of groups")
+        if self.rank < 1:
+            raise ValueError("rank must be at least 1")
+        kw = dict(device=device, dtype=dtype)
+        self.w_in = torch.nn.Linear(channels, 2 * self.inner, bias=False, **kw)
+        self.w_x = torch.nn.Linear(self.inner, self.rank + 2 * self.groups * self.states,
+                                   bias=False, **kw)
+        self.w_dt = torch.nn.Linear(self.rank, self.inner, bias=False, **kw)
+        self.w_out = torch.nn.Linear(self.inner, channels, bias=False, **kw)
+        self.conv_weight = torch.nn.Parameter(torch.empty(self.kernel_size, self.inner, **kw))
+        self.conv_bias = torch.nn.Parameter(torch.zeros(self.inner, **kw))
+        f32 = dict(device=device, dtype=torch.float32)
+        self.a = torch.nn.Parameter(
+            torch.arange(1, self.states + 1, **f32).log().repeat(self.inner, 1))
+        self.D = torch.nn.Parameter(torch.ones(self.inner, **f32))
+        # steps from 0.001 to 0.1, even in their logarithm, where delta is 0
+        step = torch.exp(torch.rand(self.inner, **f32) * math.log(100.0) + math.log(1e-3))
+        self.delta_bias = torch.nn.Parameter(step + torch.log(-torch.expm1(-step)))
+        bound = 1.0 / math.sqrt(self.kernel_size)
+        with torch.no_grad():
+            self.conv_weight.uniform_(-bound, bound)
+
+    def _operands(self, u):
+        """delta, A, B, C of the convolution's output."""
+        g, n = self.groups, self.states
+        mixed = self.w_x(u)
+        delta = self.w_dt(mixed[..., :self.rank])
+        B = mixed[..., self.rank:self.rank + g * n].unflatten(-1, (g, n))
+        C = mixed[..., self.rank + g * n:].unflatten(-1, (g, n))
+        return delta, -torch.exp(self.a), B, C
+
+    def forward(self, h: torch.Tensor, state: Optional[ScanState] = None,
+                lengths: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, ScanState]:
+        if lengths is not None:
+            live = torch.arange(h.shape[1], device=h.device) < lengths[:, None]
+            # what stands past a length is not used, not even times a zero gradient
+            h = torch.where(live[..., None], h, 0.0)
+        xz = self.w_in(h)
+        taps, states = state if state is not None else (None, None)
+        u, taps = causal_conv(xz[..., :self.inner], self.conv_weight, self.conv_bias, taps,
+                              lengths, "silu")
+        y, states = selective_scan(u, *self._operands(u), self.D, xz[..., self.inner:],
+                                   self.delta_bias, states, lengths, softplus=True)
+        return self.w_out(y), ScanState(taps, states)
+
+    @torch.no_grad()
+    def step(self, h: torch.Tensor, state: ScanState) -> torch.Tensor:
+        """One or a few tokens of each sequence (b x l x channels); ``state``
+        is updated in place."""
+        xz = self.w_in(h)
+        u, _ = space.causal_conv_step(xz[..., :self.inner], self.conv_weight, self.conv_bias,
+                                      state.taps, act="silu", out_state=state.taps)
+        y, _ = space.selective_scan_step(u, *self._operands(u), self.D, xz[..., self.inner:],
+                                         self.delta_bias, state.states, softplus=True,
+                                         out_state=state.states)
+        return self.w_out(y)
+
+    def extra_repr(self) -> str:
+        return (f"inner={self.inner}, states={self.states}, kernel_size={self.kernel_size}, "
+                f"rank={self.rank}, groups={self.groups}")
+
+
+class SelectiveScanLayers(torch.nn.Module):
+    """Selective state space mixers on a residual stream of b x l x channels,
+    with RMS norms before and behind each:
+
+      h = norm(x);  for each layer:  y = mixer(h)
+      x = x + scale norm(y) w_post,  h = norm(x) w_pre of the next layer
+
+    the last two in one pass (``residual_norm``).  ``forward`` returns (the
+    last h, 0 past a length, and the states of each layer); ``step`` takes one
+    or a few tokens and updates the states in place.  The stream keeps x's type, fp32 or the
+    mixers'."""
+
+    def __init__(self, channels: int, layers: int, eps: float = 1e-5, scale: float = 1.0,
+                 device=None, dtype=torch.float32, **mixer):
+        super().__init__()
+        self.eps = float(eps)
+        self.mixers = torch.nn.ModuleList(
+            SelectiveScanMixer(channels, device=device, dtype=dtype, **mixer)
+            for _ in range(layers))
+        new = lambda k, v: torch.nn.Parameter(  # noqa: E731
+            torch.full((k, channels), v, device=device, dtype=torch.float32))
+        self.w_pre, self.w_post = new(layers + 1, 1.0), new(layers, 1.0)
+        self.scale = new(layers, float(scale))
+
+    def _run(self, x, call):
+        dt = self.mixers[0].w_in.weight.dtype if len(self.mixers) else x.dtype
+        # unbind: the gradients of the rows are joined by one operation
+        pre, post, scale = self.w_pre.unbind(), self.w_post.unbind(), self.scale.unbind()
+        h = rms_norm(x, pre[0], eps=self.eps).to(dt)
+        for i in range(len(self.mixers)):
+            x, h = residual_norm(x, call(i, h), None, scale[i], post[i], pre[i + 1], self.eps)
+        return h
+
+    def forward(self, x: torch.Tensor, state: Optional[List[ScanState]] = None,
+                lengths: Optional[torch.Tensor] = None
+                ) -> Tuple[torch.Tensor, List[ScanState]]:
+        after: List[ScanState] = []
+        if lengths is not None:
+            live = torch.arange(x.shape[1], device=x.device) < lengths[:, None]
+            # (the norms' gradients see no row past a length)
+            x = torch.where(live[..., None], x, 0.0)
+
+        def call(i, h):
+            y, s = self.mixers[i](h, state[i] if state is not None else None, lengths)
+            after.append(s)
+            return y
+
+        return self._run(x, call), after
+
+    @torch.no_grad()
+    def step(self, x: torch.Tensor, state: List[ScanState]) -> torch.Tensor:
+        return self._run(x, lambda i, h: self.mixers[i].step(h, state[i]))

@@ -406,6 +406,176 @@ int dwc_delta_bwd(const dwc_delta_problem* p, const void* dout,
                   float* ds0, void* workspace, size_t workspace_bytes,
                   void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators of a selective state space layer: its short causal convolution,
+ * its scan, and the norms behind one block and before the next fused with the
+ * gate, the residual scale and the residual sum.  Types, sums, ownership and
+ * errors as above.
+ * ------------------------------------------------------------------------ */
+
+/* Short causal depthwise convolution over the tokens of b x l x d:
+ *   pre_t = bias + sum_{j < taps} w_j x_{t - taps + 1 + j}
+ *   y_t = pre_t, or pre_t sigmoid(pre_t) with act = DWC_ACT_SILU
+ * x before the first token is s0 (its last row the token just before), or
+ * zero; s1 is the last taps - 1 inputs, so that calls on consecutive pieces
+ * of a sequence give what one call on the whole gives.
+ *   x : b x l x d of dtype, strides in elements (batch, token), the last
+ *       axis dense
+ *   w : taps x d, bias : d, of w_dtype; bias may be NULL
+ *   s0, s1 : b x (taps - 1) x d of dtype, dense; either may be NULL
+ *   lengths : b int32 in device memory, or NULL: sequence i ends after
+ *       lengths[i] tokens (clamped to 0..l).  What stands in x past it is not
+ *       used, y there is 0, s1 is of the tokens before it
+ *   y : b x l x d of dtype, dense */
+typedef struct {
+    int64_t b, l, d;        /* b, l >= 0, d >= 1                            */
+    int64_t x_stride[2];
+    int64_t dy_stride[2];   /* gradient of y, bwd only                      */
+    int32_t taps;           /* 1..8                                         */
+    int32_t dtype, w_dtype;
+    int32_t act;            /* DWC_ACT_NONE or DWC_ACT_SILU                 */
+} dwc_causal_conv_problem;
+
+int dwc_causal_conv(const dwc_causal_conv_problem* p, const void* x,
+                    const void* w, const void* bias, const void* s0,
+                    const int32_t* lengths, void* y, void* s1, void* stream);
+
+/* The form for one or a few new tokens of each sequence (l up to 2^20): s1
+ * may be s0 itself, the state is then updated in place. */
+int dwc_causal_conv_step(const dwc_causal_conv_problem* p, const void* x,
+                         const void* w, const void* bias, const void* s0,
+                         const int32_t* lengths, void* y, void* s1,
+                         void* stream);
+
+/* Bytes of workspace of dwc_causal_conv_bwd (partial sums). */
+int dwc_causal_conv_bwd_workspace_size(const dwc_causal_conv_problem* p,
+                                       size_t* bytes);
+
+/* Gradients from dy (of dtype, dy_stride) and ds1 (as s1, dense, or NULL for
+ * zero):
+ *   dx : b x l x d of dtype, dense, zeros past a length
+ *   dw : taps x d fp32; dbias : d fp32, or NULL
+ *   ds0 : as s0, or NULL if not wanted
+ * Sums run in a fixed order: the same bits on every call. */
+int dwc_causal_conv_bwd(const dwc_causal_conv_problem* p, const void* dy,
+                        const void* ds1, const void* x, const void* w,
+                        const void* bias, const void* s0,
+                        const int32_t* lengths, void* dx, float* dw,
+                        float* dbias, void* ds0, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* Selective state space scan.  Per sequence and channel, with a state h of n
+ * values that starts at s0 (or zero):
+ *   dt_t = softplus(delta_t + bias), or delta_t + bias with softplus = 0
+ *   h_t = exp(dt_t A) h_{t-1} + dt_t u_t B_t
+ *   y_t = (C_t . h_t + D u_t) z_t sigmoid(z_t)
+ *   u, delta, z : b x l x d of dtype, strides in elements (batch, token), the
+ *       last axis dense; z may be NULL (no gate)
+ *   A : d x n fp32; D, bias : d fp32, either may be NULL (zeros)
+ *   B, C : b x l x g x n of dtype, strides (batch, token, group), the last
+ *       axis dense; channel c uses group c / (d / g)
+ *   s0, s1 : b x d x n fp32, dense; s0 may be NULL
+ *   lengths : as above: what stands in u, delta, z, B and C past a length is
+ *       not used, y there is 0, s1 is the state after the last token
+ *   y : b x l x d of dtype, dense
+ * Infinities and NaN act as arithmetic has it. */
+typedef struct {
+    int64_t b, l;           /* >= 0                                         */
+    int64_t u_stride[2], delta_stride[2], z_stride[2],
+        dy_stride[2];       /* dy_stride: gradient of y, bwd only           */
+    int64_t b_stride[3], c_stride[3];
+    int32_t d, n, g;        /* n 1..256, d a multiple of g                  */
+    int32_t dtype;
+    int32_t softplus;       /* 0 or 1                                       */
+    int32_t reserved;
+} dwc_scan_problem;
+
+/* Token by token, the form for one or a few new tokens of each sequence.
+ * s1 may be s0 itself (the state updated in place). */
+int dwc_scan_step(const dwc_scan_problem* p, const void* u, const void* delta,
+                  const float* A, const void* B, const void* C, const float* D,
+                  const void* z, const float* bias, const float* s0,
+                  const int32_t* lengths, void* y, float* s1, void* stream);
+
+#define DWC_SCAN_FWD 0
+#define DWC_SCAN_BWD 1
+/* Bytes of workspace of dwc_scan_fwd or dwc_scan_bwd (may be 0). */
+int dwc_scan_workspace_size(const dwc_scan_problem* p, int op, size_t* bytes);
+
+/* Whole sequences, in chunks of tokens side by side where there are few
+ * channels.  workspace: dwc_scan_workspace_size(p, DWC_SCAN_FWD) bytes,
+ * 256-byte aligned. */
+int dwc_scan_fwd(const dwc_scan_problem* p, const void* u, const void* delta,
+                 const float* A, const void* B, const void* C, const float* D,
+                 const void* z, const float* bias, const float* s0,
+                 const int32_t* lengths, void* y, float* s1, void* workspace,
+                 size_t workspace_bytes, void* stream);
+
+/* Gradients of the above from dy (of dtype, dy_stride) and ds1 (gradient of
+ * s1, dense fp32, or NULL for zero):
+ *   du, ddelta, dz : b x l x d of dtype, dense; dz with z only
+ *   dA : d x n, dD, dbias : d, fp32; dD and dbias NULL if not wanted
+ *   dB, dC : b x l x g x n of dtype, dense (summed over the channels that
+ *       share them)
+ *   ds0 : as s0, or NULL if not wanted
+ * Tokens past a length get zeros.  Nothing of the forward call is needed.
+ * Sums run in a fixed order: the same bits on every call. */
+int dwc_scan_bwd(const dwc_scan_problem* p, const void* dy, const float* ds1,
+                 const void* u, const void* delta, const float* A,
+                 const void* B, const void* C, const float* D, const void* z,
+                 const float* bias, const float* s0, const int32_t* lengths,
+                 void* du, void* ddelta, float* dA, void* dB, void* dC,
+                 float* dD, void* dz, float* dbias, float* ds0,
+                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* The norm behind a block, its gate and scale, the residual sum and the norm
+ * before the next block, over rows of c values:
+ *   q1 = 1 / sqrt(mean(y^2) + eps), p = y q1 w_post   (post = 0: p = y)
+ *   r = x + scale act(gate) p
+ *   q2 = 1 / sqrt(mean(r^2) + eps), h = r q2 w_pre    (pre = 0: no h)
+ * h is made of r before r is rounded.  So the call with x = NULL, pre = 0 is
+ * a norm with a gate, with x = NULL, gate = scale = NULL, pre = 0 the norm
+ * alone. */
+#define DWC_GATE_NONE 0    /* act(g) = g                                    */
+#define DWC_GATE_SILU 1    /* g sigmoid(g)                                  */
+#define DWC_GATE_SIGMOID 2 /* sigmoid(g)                                    */
+typedef struct {
+    int64_t rows, c;       /* rows >= 0, c >= 1                             */
+    int64_t x_stride, y_stride, gate_stride, dr_stride,
+        dh_stride;         /* elements between rows, >= c; the last two bwd */
+    int32_t x_dtype;       /* x, r, dr, dx: DWC_F32 or y_dtype              */
+    int32_t y_dtype;       /* y, gate, h, dh, dy, dgate                     */
+    int32_t w_dtype;       /* scale, w_post, w_pre                          */
+    int32_t act;           /* DWC_GATE_*                                    */
+    int32_t post, pre;     /* 0 or 1                                        */
+    float eps;             /* >= 0                                          */
+    int32_t reserved;
+} dwc_resnorm_problem;
+
+/* x, gate, scale, w_post and w_pre may be NULL (0, 1, 1, 1, 1); w_post needs
+ * post, w_pre and h need pre.  r, h: rows x c, dense; post_rstd (q1) and
+ * pre_rstd (q2): rows fp32 values, either NULL if not wanted. */
+int dwc_residual_norm(const dwc_resnorm_problem* p, const void* x,
+                      const void* y, const void* gate, const void* scale,
+                      const void* w_post, const void* w_pre, void* r, void* h,
+                      float* post_rstd, float* pre_rstd, void* stream);
+
+/* Bytes of workspace of dwc_residual_norm_bwd (column partials); c < 2^24. */
+int dwc_residual_norm_bwd_workspace_size(const dwc_resnorm_problem* p,
+                                         size_t* bytes);
+
+/* Gradients from dr and dh (one may be NULL for zero): dx, dy, dgate rows x
+ * c, dense (dx and dgate NULL if not wanted); dscale, dw_post, dw_pre c fp32
+ * values each, NULL if not wanted, summed over the rows in a fixed order. */
+int dwc_residual_norm_bwd(const dwc_resnorm_problem* p, const void* dr,
+                          const void* dh, const void* x, const void* y,
+                          const float* post_rstd, const float* pre_rstd,
+                          const void* gate, const void* scale,
+                          const void* w_post, const void* w_pre, void* dx,
+                          void* dy, void* dgate, float* dscale,
+                          float* dw_post, float* dw_pre, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
