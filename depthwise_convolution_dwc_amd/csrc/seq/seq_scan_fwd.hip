@@ -69,39 +69,49 @@ __device__ __forceinline__ Where where(const ScanArgs& a, int blk, uint32_t i, i
 
 template <int SPL>
 __device__ __forceinline__ void load_a(const ScanArgs& a, const Where& w, float (&v)[SPL]) {
+  const float* p = a.a + w.g0 * a.n;
+  const uint32_t at = w.in * (uint32_t)a.n;  // d n is below 2^32
 #pragma unroll
-  for (int s = 0; s < SPL; ++s) {
+  for (int s = 0; s < SPL; ++s) {  // (loads of all states under way together)
     const int i = w.blk * SPL + s;
-    v[s] = i < a.n ? kLog2e * a.a[(int64_t)w.c * a.n + i] : 0.f;
+    v[s] = (p + (i < a.n ? i : 0))[at];
   }
+#pragma unroll
+  for (int s = 0; s < SPL; ++s) v[s] = w.blk * SPL + s < a.n ? kLog2e * v[s] : 0.f;
 }
 
 constexpr int kAhead = 4;  // tokens whose loads are under way together
 
-// Raw operands of kAhead tokens from t on; tokens from end on give the last
-// one's again.
-template <int T, int N>
+// Raw operands of N tensors: U tokens from t on, those from end on give the
+// last one's again.  p: addresses that are the same in all lanes, of the
+// group's first channel.
+template <int T, int N, int U>
 struct Ahead {
-  Raw<T> v[N][kAhead];
-  // p: addresses that are the same in all lanes, of the group's first channel
+  Raw<T> v[N][U];
   __device__ __forceinline__ void load(const void* const (&p)[N], const int64_t (&step)[N],
                                        uint32_t in, int64_t t, int64_t end) {
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
+    for (int i = 0; i < U; ++i) {
       const int64_t at = t + i < end ? t + i : end - 1;
 #pragma unroll
-      for (int k = 0; k < N; ++k)
-        if (p[k]) v[k][i] = ((const Raw<T>*)p[k] + at * step[k])[in];
+      for (int k = 0; k < N; ++k) v[k][i] = ((const Raw<T>*)p[k] + at * step[k])[in];
     }
   }
 };
 
+template <int T>
+__device__ __forceinline__ float step_of(const ScanArgs& a, Raw<T> delta, float bias) {
+  const float x = value<T>(delta) + bias, s = softplus(x);
+  return a.softplus ? s : x;  // (a select: a branch would split the tokens' code)
+}
+
 // Each chunk's state from zero and the sum of its steps.  With BWD also, from
 // zero at its end, the gradient that it hands to the state before it:
 //   sum_t (a_t0 ... a_t) C_t do_t,  do = dy silu(z).
-template <int T, int SPL, bool BWD>
+template <int T, int SPL, bool BWD, bool GATE>
 __global__ void __launch_bounds__(64) scan_chunk(ScanArgs a) {
   const Where w = where(a, 0, blockIdx.x, a.nblk);
+  if (!w.on) return;
   const int64_t end = w.t1 < w.len ? w.t1 : w.len;
   float a2[SPL], h[SPL], p[SPL], r[SPL];
   load_a<SPL>(a, w, a2);
@@ -113,7 +123,7 @@ __global__ void __launch_bounds__(64) scan_chunk(ScanArgs a) {
   double sum = 0.0;
   if (w.t0 < end) {
     const float bias = a.bias ? a.bias[w.c] : 0.f;
-    constexpr int N = BWD ? 4 : 2;
+    constexpr int N = BWD ? (GATE ? 4 : 3) : 2;
     const int64_t e = sizeof(Raw<T>);
     const void* ptr[N];
     int64_t step[N];
@@ -124,55 +134,60 @@ __global__ void __launch_bounds__(64) scan_chunk(ScanArgs a) {
     if constexpr (BWD) {
       ptr[2] = (const char*)a.dy + (w.b * a.dy_stride[0] + w.g0) * e;
       step[2] = a.dy_stride[1];
-      ptr[3] = a.z ? (const char*)a.z + (w.b * a.z_stride[0] + w.g0) * e : nullptr;
-      step[3] = a.z_stride[1];
+      if constexpr (GATE) {
+        ptr[3] = (const char*)a.z + (w.b * a.z_stride[0] + w.g0) * e;
+        step[3] = a.z_stride[1];
+      }
     }
     const int64_t line = (int64_t)a.g * a.nblk * 2 * SPL;
     const float* bc = a.bc + (w.b * a.l + w.t0) * line + (w.g * a.nblk + w.blk) * 2 * SPL;
-    Ahead<T, N> now, next;
-    now.load(ptr, step, w.in, w.t0, end);
-    for (int64_t t = w.t0; t < end; t += kAhead) {
-      next.load(ptr, step, w.in, t + kAhead, end);
+    const auto token = [&](const auto& x, int i) {
+      const auto bb = load_scalar<SPL>(bc);
+      const float dt = step_of<T>(a, x.v[1][i], bias), du = dt * value<T>(x.v[0][i]);
+      sum += dt;
+      float k[SPL];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (t + i >= end) break;
-        const auto bb = load_scalar<SPL>(bc);
-        float dt = value<T>(now.v[1][i]) + bias;
-        if (a.softplus) dt = softplus(dt);
-        sum += dt;
-        const float du = dt * value<T>(now.v[0][i]);
-        float go = 0.f;
-        typename VecOf<SPL>::type cc;
-        if constexpr (BWD) {
-          cc = load_scalar<SPL>(bc + SPL);
-          go = value<T>(now.v[2][i]);
-          if (a.z) {
-            const float z = value<T>(now.v[3][i]);
-            go *= z * sigmoid(z);
-          }
+      for (int s = 0; s < SPL; ++s) {
+        k[s] = exp2_of(dt * a2[s]);
+        h[s] = fmaf(k[s], h[s], du * bb[s]);
+      }
+      if constexpr (BWD) {
+        const auto cc = load_scalar<SPL>(bc + SPL);
+        float go = value<T>(x.v[2][i]);
+        if constexpr (GATE) {
+          const float z = value<T>(x.v[3][i]);
+          go *= z * sigmoid(z);
         }
 #pragma unroll
         for (int s = 0; s < SPL; ++s) {
-          const float k = exp2_of(dt * a2[s]);
-          h[s] = fmaf(k, h[s], du * bb[s]);
-          if constexpr (BWD) {
-            p[s] *= k;
-            r[s] = fmaf(p[s], cc[s] * go, r[s]);
-          }
+          p[s] *= k[s];
+          r[s] = fmaf(p[s], cc[s] * go, r[s]);
         }
-        bc += line;
       }
+      bc += line;
+    };
+    Ahead<T, N, kAhead> now, next;
+    now.load(ptr, step, w.in, w.t0, end);
+    int64_t t = w.t0;
+    for (; t + kAhead <= end; t += kAhead) {
+      next.load(ptr, step, w.in, t + kAhead, end);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) token(now, i);
       now = next;
     }
+    for (; t < end; ++t) {
+      Ahead<T, N, 1> one;
+      one.load(ptr, step, w.in, t, end);
+      token(one, 0);
+    }
   }
-  if (!w.on) return;
-  const int64_t at = ((w.b * a.nc + w.chunk) * a.nblk + w.blk) * SPL * a.d + w.c;
+  const int64_t at = ((w.b * a.nc + w.chunk) * a.nblk + w.blk) * SPL * a.d + w.g0;
 #pragma unroll
   for (int s = 0; s < SPL; ++s) {
-    a.states[at + (int64_t)s * a.d] = h[s];
-    if constexpr (BWD) a.rstates[at + (int64_t)s * a.d] = r[s];
+    (a.states + at + (int64_t)s * a.d)[w.in] = h[s];
+    if constexpr (BWD) (a.rstates + at + (int64_t)s * a.d)[w.in] = r[s];
   }
-  if (w.blk == 0) a.dts[(w.b * a.nc + w.chunk) * a.d + w.c] = (float)sum;
+  if (w.blk == 0) (a.dts + (w.b * a.nc + w.chunk) * a.d + w.g0)[w.in] = (float)sum;
 }
 
 // From each chunk's own part to the state that it starts from; blockIdx.y = 1:
@@ -215,93 +230,128 @@ __global__ void __launch_bounds__(256) scan_combine(ScanArgs a) {
 // Outputs, a chunk from its first state on.  With MULTI a workgroup's waves
 // hold the blocks of one channel block's states and their parts of C . h are
 // joined in LDS, token i of each four by wave i.
-template <int T, int SPL, bool MULTI>
+template <int T, int SPL, bool GATE, bool MULTI>
 __global__ void __launch_bounds__(MULTI ? 1024 : 64) scan_out(ScanArgs a) {
   __shared__ float lds[MULTI ? 2 : 1][MULTI ? 16 : 1][kAhead][64];
   const int wave = MULTI ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
   const int lane = threadIdx.x & 63;
   const Where w = where(a, wave, blockIdx.x, 1);
+  if (!w.on) return;  // (no whole wave: barriers still count all)
   const int64_t end = w.t1 < w.len ? w.t1 : w.len;
   float a2[SPL], h[SPL];
   load_a<SPL>(a, w, a2);
+  if (a.nc > 1) {
+    const float* p = a.states + ((w.b * a.nc + w.chunk) * a.nblk + w.blk) * SPL * a.d + w.g0;
 #pragma unroll
-  for (int s = 0; s < SPL; ++s) {
-    const int i = w.blk * SPL + s;
-    h[s] = 0.f;
-    if (a.nc > 1)
-      h[s] = a.states[(((w.b * a.nc + w.chunk) * a.nblk + w.blk) * SPL + s) * a.d + w.c];
-    else if (a.s0 && i < a.n)
-      h[s] = a.s0[(w.b * a.d + w.c) * a.n + i];
+    for (int s = 0; s < SPL; ++s) h[s] = (p + (int64_t)s * a.d)[w.in];
+  } else if (a.s0) {
+    const float* p = a.s0 + (w.b * a.d + w.g0) * a.n;
+#pragma unroll
+    for (int s = 0; s < SPL; ++s) {
+      const int i = w.blk * SPL + s;
+      h[s] = (p + (i < a.n ? i : 0))[w.in * (uint32_t)a.n];
+    }
+#pragma unroll
+    for (int s = 0; s < SPL; ++s) h[s] = w.blk * SPL + s < a.n ? h[s] : 0.f;
+  } else {
+#pragma unroll
+    for (int s = 0; s < SPL; ++s) h[s] = 0.f;
   }
   Raw<T>* const out = (Raw<T>*)a.y + w.b * a.l * a.d + w.g0;
-  if (w.t0 < end) {
+  int64_t t = w.t0;
+  if (t < end) {
     const float bias = a.bias ? a.bias[w.c] : 0.f, skip = a.skip ? a.skip[w.c] : 0.f;
     const int64_t e = sizeof(Raw<T>);
-    const void* ptr[3] = {(const char*)a.u + (w.b * a.u_stride[0] + w.g0) * e,
-                          (const char*)a.delta + (w.b * a.delta_stride[0] + w.g0) * e,
-                          a.z ? (const char*)a.z + (w.b * a.z_stride[0] + w.g0) * e : nullptr};
-    const int64_t step[3] = {a.u_stride[1], a.delta_stride[1], a.z_stride[1]};
+    constexpr int N = GATE ? 3 : 2;
+    const void* ptr[N];
+    int64_t step[N];
+    ptr[0] = (const char*)a.u + (w.b * a.u_stride[0] + w.g0) * e;
+    step[0] = a.u_stride[1];
+    ptr[1] = (const char*)a.delta + (w.b * a.delta_stride[0] + w.g0) * e;
+    step[1] = a.delta_stride[1];
+    if constexpr (GATE) {
+      ptr[2] = (const char*)a.z + (w.b * a.z_stride[0] + w.g0) * e;
+      step[2] = a.z_stride[1];
+    }
     const int64_t line = (int64_t)a.g * a.nblk * 2 * SPL;
     const float* bc = a.bc + (w.b * a.l + w.t0) * line + (w.g * a.nblk + w.blk) * 2 * SPL;
-    const auto finish = [&](int64_t t, float y, float u, Raw<T> rz) {
-      y = fmaf(skip, u, y);
-      if (a.z) {
-        const float z = value<T>(rz);
+    const auto token = [&](const auto& x, int i) {
+      const auto bb = load_scalar<SPL>(bc);
+      const auto cc = load_scalar<SPL>(bc + SPL);
+      const float dt = step_of<T>(a, x.v[1][i], bias), du = dt * value<T>(x.v[0][i]);
+      float y = 0.f;
+#pragma unroll
+      for (int s = 0; s < SPL; ++s) {
+        h[s] = fmaf(exp2_of(dt * a2[s]), h[s], du * bb[s]);
+        y = fmaf(cc[s], h[s], y);
+      }
+      bc += line;
+      return y;
+    };
+    const auto finish = [&](const auto& x, int i, int64_t at, float y) {
+      y = fmaf(skip, value<T>(x.v[0][i]), y);
+      if constexpr (GATE) {
+        const float z = value<T>(x.v[2][i]);
         y *= z * sigmoid(z);
       }
-      if (w.on) store1<T>(out + t * a.d, w.in, y);
+      store1<T>(out + at * a.d, w.in, y);
     };
-    Ahead<T, 3> now, next;
-    now.load(ptr, step, w.in, w.t0, end);
+    Ahead<T, N, kAhead> now, next;
+    now.load(ptr, step, w.in, t, end);
     int side = 0;
-    for (int64_t t = w.t0; t < end; t += kAhead) {
+    for (; t + kAhead <= end; t += kAhead) {
       next.load(ptr, step, w.in, t + kAhead, end);
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        if (t + i >= end) break;
-        const auto bb = load_scalar<SPL>(bc);
-        const auto cc = load_scalar<SPL>(bc + SPL);
-        float dt = value<T>(now.v[1][i]) + bias;
-        if (a.softplus) dt = softplus(dt);
-        const float u = value<T>(now.v[0][i]), du = dt * u;
-        float y = 0.f;
-#pragma unroll
-        for (int s = 0; s < SPL; ++s) {
-          h[s] = fmaf(exp2_of(dt * a2[s]), h[s], du * bb[s]);
-          y = fmaf(cc[s], h[s], y);
-        }
+        const float y = token(now, i);
         if constexpr (MULTI) lds[side][wave][i][lane] = y;
-        else finish(t + i, y, u, now.v[2][i]);
-        bc += line;
+        else finish(now, i, t + i, y);
       }
       if constexpr (MULTI) {
         __syncthreads();  // (two sides: one barrier keeps readers and writers apart)
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-          if (i % a.nblk == wave && t + i < end) {
+          if (i % a.nblk == wave) {
             float y = 0.f;
             for (int k = 0; k < a.nblk; ++k) y += lds[side][k][i][lane];
-            finish(t + i, y, value<T>(now.v[0][i]), now.v[2][i]);
+            finish(now, i, t + i, y);
           }
         }
         side ^= 1;
       }
       now = next;
     }
+    for (; t < end; ++t) {
+      Ahead<T, N, 1> one;
+      one.load(ptr, step, w.in, t, end);
+      float y = token(one, 0);
+      if constexpr (MULTI) {
+        lds[side][wave][0][lane] = y;
+        __syncthreads();
+        if (wave == 0) {
+          y = 0.f;
+          for (int k = 0; k < a.nblk; ++k) y += lds[side][k][0][lane];
+          finish(one, 0, t, y);
+        }
+        side ^= 1;
+      } else {
+        finish(one, 0, t, y);
+      }
+    }
   }
-  if (!w.on) return;
   if (wave == 0)
-    for (int64_t t = end > w.t0 ? end : w.t0; t < w.t1; ++t) store1<T>(out + t * a.d, w.in, 0.f);
+    for (; t < w.t1; ++t) store1<T>(out + t * a.d, w.in, 0.f);
   if (w.chunk + 1 == a.nc) {
+    float* p = a.s1 + (w.b * a.d + w.g0) * a.n;
 #pragma unroll
     for (int s = 0; s < SPL; ++s) {
       const int i = w.blk * SPL + s;
-      if (i < a.n) a.s1[(w.b * a.d + w.c) * a.n + i] = h[s];
+      if (i < a.n) (p + i)[w.in * (uint32_t)a.n] = h[s];
     }
   }
 }
 
-template <int T, int SPL, bool BWD>
+template <int T, int SPL, bool BWD, bool GATE>
 void prepare(const ScanArgs& a, hipStream_t st) {
   if (a.l > 0) {
     const int64_t vals = a.b * a.l * a.g * a.nblk * 2 * a.spl;
@@ -309,30 +359,42 @@ void prepare(const ScanArgs& a, hipStream_t st) {
   }
   if (a.nc > 1) {
     const dim3 grid((uint32_t)(a.b * a.nc * a.g * a.cblk * a.nblk));
-    hipLaunchKernelGGL((scan_chunk<T, SPL, BWD>), grid, dim3(64), 0, st, a);
+    hipLaunchKernelGGL((scan_chunk<T, SPL, BWD, GATE>), grid, dim3(64), 0, st, a);
     const int64_t vals = a.b * a.nblk * a.spl * a.d;
     hipLaunchKernelGGL(scan_combine, dim3((uint32_t)((vals + 255) / 256), BWD ? 2 : 1), dim3(256),
                        0, st, a);
   }
 }
 
-template <int T, int SPL>
+template <int T, int SPL, bool GATE>
 void go(const ScanArgs& a, hipStream_t st) {
-  prepare<T, SPL, false>(a, st);
+  prepare<T, SPL, false, false>(a, st);
   const dim3 grid((uint32_t)(a.b * a.nc * a.g * a.cblk));
   if (a.nblk > 1) {
     if constexpr (SPL == 16)
-      hipLaunchKernelGGL((scan_out<T, 16, true>), grid, dim3(64 * a.nblk), 0, st, a);
+      hipLaunchKernelGGL((scan_out<T, 16, GATE, true>), grid, dim3(64 * a.nblk), 0, st, a);
   } else {
-    hipLaunchKernelGGL((scan_out<T, SPL, false>), grid, dim3(64), 0, st, a);
+    hipLaunchKernelGGL((scan_out<T, SPL, GATE, false>), grid, dim3(64), 0, st, a);
   }
+}
+
+template <int T, int SPL>
+void go_gate(const ScanArgs& a, hipStream_t st) {
+  if (a.z) go<T, SPL, true>(a, st);
+  else go<T, SPL, false>(a, st);
 }
 
 template <int T>
 void go_states(const ScanArgs& a, hipStream_t st) {
-  if (a.spl == 4) go<T, 4>(a, st);
-  else if (a.spl == 8) go<T, 8>(a, st);
-  else go<T, 16>(a, st);
+  if (a.spl == 4) go_gate<T, 4>(a, st);
+  else if (a.spl == 8) go_gate<T, 8>(a, st);
+  else go_gate<T, 16>(a, st);
+}
+
+template <int T>
+void prepare_bwd(const ScanArgs& a, hipStream_t st) {
+  if (a.z) prepare<T, 16, true, true>(a, st);
+  else prepare<T, 16, true, false>(a, st);
 }
 
 }  // namespace scan
@@ -359,9 +421,9 @@ void scan_split(ScanArgs* a, bool bwd) {
 }
 
 hipError_t launch_scan_prepare_bwd(const ScanArgs& a, hipStream_t st) {
-  if (a.type == T_F32) scan::prepare<T_F32, 16, true>(a, st);
-  else if (a.type == T_BF16) scan::prepare<T_BF16, 16, true>(a, st);
-  else scan::prepare<T_F16, 16, true>(a, st);
+  if (a.type == T_F32) scan::prepare_bwd<T_F32>(a, st);
+  else if (a.type == T_BF16) scan::prepare_bwd<T_BF16>(a, st);
+  else scan::prepare_bwd<T_F16>(a, st);
   return hipGetLastError();
 }
 

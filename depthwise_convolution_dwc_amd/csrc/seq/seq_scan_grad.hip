@@ -58,76 +58,85 @@ __device__ __forceinline__ float fold2(float a, float b, int lane) {
   return v + row_move<0x4E>(v);
 }
 
-// One token of two neighbouring channels.  base: the index of the first
-// channel of the group at batch b and token t (the same in all lanes of
-// scan_grad, so that lanes add a 32-bit offset to a scalar address).
-template <int T>
-struct Token {
-  float u[2], dt[2], slope[2], go[2], dz[2];  // slope of dt in delta; dy silu'(z)
+// Raw operands of one token of NC neighbouring channels.  first: the index of
+// the group's first channel (the same in all lanes of scan_grad, as b and t
+// are, so that lanes add a 32-bit offset to a scalar address).
+template <int T, int NC, bool GATE>
+struct RawToken {
+  Raw<T> u[NC], delta[NC], dy[NC], z[NC];
   __device__ __forceinline__ void load(const ScanArgs& a, int64_t b, int64_t t, int64_t first,
-                                       uint32_t in, bool live, const bool (&on)[2],
-                                       const float (&bias)[2]) {
+                                       const uint32_t (&in)[NC]) {
     typedef const Raw<T>* ptr;
     const ptr pu = (ptr)a.u + (b * a.u_stride[0] + t * a.u_stride[1] + first);
     const ptr pd = (ptr)a.delta + (b * a.delta_stride[0] + t * a.delta_stride[1] + first);
     const ptr py = (ptr)a.dy + (b * a.dy_stride[0] + t * a.dy_stride[1] + first);
-    const ptr pz = (ptr)a.z + (b * a.z_stride[0] + t * a.z_stride[1] + first);
-    Raw<T> ru[2], rd[2], ry[2], rz[2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (live && on[k]) {
-        ru[k] = pu[in + k];
-        rd[k] = pd[in + k];
-        ry[k] = py[in + k];
-        if (a.z) rz[k] = pz[in + k];
-      }
+    for (int k = 0; k < NC; ++k) {
+      u[k] = pu[in[k]];
+      delta[k] = pd[in[k]];
+      dy[k] = py[in[k]];
+    }
+    if constexpr (GATE) {
+      const ptr pz = (ptr)a.z + (b * a.z_stride[0] + t * a.z_stride[1] + first);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      u[k] = dt[k] = slope[k] = go[k] = dz[k] = 0.f;
-      if (live && on[k]) {
-        u[k] = value<T>(ru[k]);
-        dt[k] = value<T>(rd[k]) + bias[k];
-        slope[k] = 1.f;
-        if (a.softplus) {
-          slope[k] = sigmoid(dt[k]);
-          dt[k] = softplus(dt[k]);
-        }
-        go[k] = value<T>(ry[k]);
-        if (a.z) {
-          const float z = value<T>(rz[k]), s = sigmoid(z);
-          dz[k] = go[k] * fmaf(z * s, 1.f - s, s);
-          go[k] *= z * s;
-        }
-      }
+      for (int k = 0; k < NC; ++k) z[k] = pz[in[k]];
     }
   }
 };
 
+// What they say: the step, its slope in delta, do and dy silu'(z).  Zeros
+// where the token or the channel is not there.
+struct Token {
+  float u, dt, slope, go, dz;
+};
+template <int T, int NC, bool GATE>
+__device__ __forceinline__ Token token_of(const ScanArgs& a, const RawToken<T, NC, GATE>& r, int k,
+                                          float bias, bool live) {
+  Token v;
+  v.u = value<T>(r.u[k]);
+  const float x = value<T>(r.delta[k]) + bias, s = softplus(x);
+  v.dt = a.softplus ? s : x;  // (selects: branches would split the code)
+  v.slope = a.softplus ? sigmoid(x) : 1.f;
+  v.go = value<T>(r.dy[k]);
+  v.dz = 0.f;
+  if constexpr (GATE) {
+    const float z = value<T>(r.z[k]), g = sigmoid(z);
+    v.dz = v.go * fmaf(z * g, 1.f - g, g);
+    v.go *= z * g;
+  }
+  v.u = live ? v.u : 0.f;
+  v.dt = live ? v.dt : 0.f;
+  v.slope = live ? v.slope : 0.f;
+  v.go = live ? v.go : 0.f;
+  v.dz = live ? v.dz : 0.f;
+  return v;
+}
+
 // Outputs of one token of one channel from its sums over the states: of
 // G B, of A q (in units of 1 / log2 e) and of C h.
-template <int T>
-__device__ __forceinline__ void finish(const ScanArgs& a, int64_t at, uint32_t in, float gb, float aq,
-                                       float ch, float u, float dt, float slope, float go,
-                                       float dz, float skip, float& dskip, float& dbias) {
-  const float dd = fmaf(u, gb, kLn2 * aq) * slope;
-  store1<T>((Raw<T>*)a.du + at, in, fmaf(dt, gb, skip * go));
+template <int T, bool GATE>
+__device__ __forceinline__ void finish(const ScanArgs& a, int64_t at, uint32_t in, float gb,
+                                       float aq, float ch, const Token& v, float skip,
+                                       float& dskip, float& dbias) {
+  const float dd = fmaf(v.u, gb, kLn2 * aq) * v.slope;
+  store1<T>((Raw<T>*)a.du + at, in, fmaf(v.dt, gb, skip * v.go));
   store1<T>((Raw<T>*)a.ddelta + at, in, dd);
-  if (a.z) store1<T>((Raw<T>*)a.dz + at, in, dz * fmaf(skip, u, ch));
-  dskip = fmaf(go, u, dskip);
+  if constexpr (GATE) store1<T>((Raw<T>*)a.dz + at, in, v.dz * fmaf(skip, v.u, ch));
+  dskip = fmaf(v.go, v.u, dskip);
   dbias += dd;
+}
+
+// Zeros behind a sequence's last token.
+template <int T, bool GATE>
+__device__ __forceinline__ void finish_none(const ScanArgs& a, int64_t at, uint32_t in) {
+  store1<T>((Raw<T>*)a.du + at, in, 0.f);
+  store1<T>((Raw<T>*)a.ddelta + at, in, 0.f);
+  if constexpr (GATE) store1<T>((Raw<T>*)a.dz + at, in, 0.f);
 }
 
 enum { DT = 0, U, GO, SLOPE, DZ, kOf };  // of a token and channel, in LDS
 
-// Zeros behind a sequence's last token.
-template <int T>
-__device__ __forceinline__ void finish_none(const ScanArgs& a, int64_t at, uint32_t in) {
-  store1<T>((Raw<T>*)a.du + at, in, 0.f);
-  store1<T>((Raw<T>*)a.ddelta + at, in, 0.f);
-  if (a.z) store1<T>((Raw<T>*)a.dz + at, in, 0.f);
-}
-
-template <int T, bool MULTI>
+template <int T, bool GATE, bool MULTI>
 __global__ void __launch_bounds__(256, 2) scan_grad(ScanArgs a) {
   constexpr int NW = 4, SPL = 4 * NW;
   __shared__ float of[kOf][kEight][kPair];
@@ -147,32 +156,52 @@ __global__ void __launch_bounds__(256, 2) scan_grad(ScanArgs a) {
   const int64_t len = length_of(a, b), t0 = (int64_t)chunk * kGradChunk;
   const int64_t t1 = t0 + kGradChunk < a.l ? t0 + kGradChunk : a.l;
   const int64_t end = t1 < len ? t1 : len;
-  const uint32_t in = (uint32_t)(block * kPair + 2 * lane);  // of the group's channels
-  const int64_t g0 = (int64_t)g * a.dg;
-  bool on[2];
-  float dskip[2], dbias[2], a2[2][4], da[2][4], carry[2][4], h[2][4];
-  const int64_t row = b * a.nc + chunk;
+  const int64_t g0 = (int64_t)g * a.dg, row = b * a.nc + chunk;
+  // channels of the group; lanes past its end read its first one again
+  const uint32_t c0 = (uint32_t)(block * kPair + 2 * lane);
+  const bool on[2] = {(int)c0 < a.dg, (int)c0 + 1 < a.dg};
+  const uint32_t in[2] = {on[0] ? c0 : 0, on[1] ? c0 + 1 : 0};
+  float dskip[2] = {0.f, 0.f}, dbias[2] = {0.f, 0.f};
+  float a2[2][4], da[2][4], carry[2][4], h[2][4];
+  const int n0 = blk * SPL + 4 * wave;
+  // (all loads under way together, then what is not there made zero)
+  {
+    const auto states = [&](const float* p, float(&v)[2][4]) {  // of d x n
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    on[k] = (int)in + k < a.dg;
-    dskip[k] = dbias[k] = 0.f;
+      for (int k = 0; k < 2; ++k)
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int n = blk * SPL + 4 * wave + s;
-      a2[k][s] = da[k][s] = carry[k][s] = h[k][s] = 0.f;
-      if (on[k] && n < a.n) {
-        const int64_t own = (b * a.d + g0) * a.n + n, at = (row * a.nblk * SPL + n) * a.d + g0;
-        const uint32_t lanes = (in + k) * (uint32_t)a.n;  // d n is below 2^32
-        a2[k][s] = kLog2e * (a.a + (g0 * a.n + n))[lanes];
-        if (a.nc > 1) {
-          h[k][s] = (a.states + at)[in + k];
-          carry[k][s] = (a.rstates + at)[in + k];
-        } else {
-          if (a.s0) h[k][s] = (a.s0 + own)[lanes];
-          if (a.ds1) carry[k][s] = (a.ds1 + own)[lanes];
+        for (int s = 0; s < 4; ++s)
+          v[k][s] = (p + (n0 + s < a.n ? n0 + s : 0))[in[k] * (uint32_t)a.n];
+    };
+    states(a.a + g0 * a.n, a2);
+    if (a.nc > 1) {
+      const int64_t at = (row * a.nblk * SPL + n0) * a.d + g0;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          h[k][s] = (a.states + at + (int64_t)s * a.d)[in[k]];
+          carry[k][s] = (a.rstates + at + (int64_t)s * a.d)[in[k]];
         }
-      }
+    } else {
+      const int64_t at = (b * a.d + g0) * a.n;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) h[k][s] = carry[k][s] = 0.f;
+      if (a.s0) states(a.s0 + at, h);
+      if (a.ds1) states(a.ds1 + at, carry);
     }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const bool is = on[k] && n0 + s < a.n;
+        a2[k][s] = is ? kLog2e * a2[k][s] : 0.f;
+        h[k][s] = is ? h[k][s] : 0.f;
+        carry[k][s] = is ? carry[k][s] : 0.f;
+        da[k][s] = 0.f;
+      }
   }
   const int64_t line = (int64_t)a.g * a.nblk * 2 * SPL;
   const int64_t lines = (int64_t)(g * a.nblk + blk) * 2 * SPL;
@@ -180,26 +209,40 @@ __global__ void __launch_bounds__(256, 2) scan_grad(ScanArgs a) {
   // rows of B and C past the last token are not there
   const auto bc_at = [&](int64_t t) { return bc + (t < a.l ? t : a.l - 1) * line; };
 
-  // a wave's own tokens of an eight: wave and 4 + wave
-  const auto share = [&](int64_t ts, int j, bool all) {
-    // (read again for each eight: registers are short)
-    const float bias[2] = {a.bias && on[0] ? (a.bias + g0)[in] : 0.f,
-                           a.bias && on[1] ? (a.bias + g0)[in + 1] : 0.f};
-    Token<T> x;
-    x.load(a, b, ts + j, g0, in, ts + j < end, on, bias);
+  // a wave's own tokens of an eight: wave and 4 + wave; a token past the last
+  // one is read as the last
+  RawToken<T, 2, GATE> raw[2];
+  const auto fetch = [&](int64_t ts) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      of[DT][j][2 * lane + k] = x.dt[k];
-      of[U][j][2 * lane + k] = x.u[k];
-      if (all) {
-        of[GO][j][2 * lane + k] = x.go[k];
-        of[SLOPE][j][2 * lane + k] = x.slope[k];
-        of[DZ][j][2 * lane + k] = x.dz[k];
+    for (int j = 0; j < 2; ++j) {
+      const int64_t t = ts + 4 * j + wave;
+      raw[j].load(a, b, t < end ? t : (end > 0 ? end - 1 : 0), g0, in);
+    }
+  };
+  const auto share = [&](int64_t ts, bool all) {
+    // (the bias is read again for each eight: registers are short)
+    const float* pb = a.bias ? a.bias + g0 : nullptr;
+    const float bias[2] = {pb ? pb[in[0]] : 0.f, pb ? pb[in[1]] : 0.f};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int at = 4 * j + wave;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const Token v = token_of(a, raw[j], k, bias[k], on[k] && ts + at < end);
+        of[DT][at][2 * lane + k] = v.dt;
+        of[U][at][2 * lane + k] = v.u;
+        if (all) {
+          of[GO][at][2 * lane + k] = v.go;
+          of[SLOPE][at][2 * lane + k] = v.slope;
+          of[DZ][at][2 * lane + k] = v.dz;
+        }
       }
     }
   };
 
   // the states before the eights
+  const bool some = t0 < a.l;
+  if (some) fetch(t0);
 #pragma unroll 1
   for (int sub = 0; sub < kSubs; ++sub) {
     const int64_t ts = t0 + sub * kEight;
@@ -209,8 +252,8 @@ __global__ void __launch_bounds__(256, 2) scan_grad(ScanArgs a) {
       for (int s = 0; s < 4; ++s) first[sub][4 * k + s][threadIdx.x] = h[k][s];
     if (sub + 1 == kSubs || ts >= end) continue;  // (the same in all waves)
     __syncthreads();
-    share(ts, wave, false);
-    share(ts, 4 + wave, false);
+    share(ts, false);
+    fetch(ts + kEight);
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kEight; ++j) {
@@ -224,13 +267,13 @@ __global__ void __launch_bounds__(256, 2) scan_grad(ScanArgs a) {
     }
   }
 
+  const int last = some ? (int)((t1 - t0 - 1) / kEight) : -1;
+  if (some) fetch(t0 + last * kEight);
 #pragma unroll 1
-  for (int sub = kSubs - 1; sub >= 0; --sub) {
+  for (int sub = last; sub >= 0; --sub) {
     const int64_t ts = t0 + sub * kEight;
-    if (ts >= t1) continue;  // (the same in all waves)
     __syncthreads();
-    share(ts, wave, true);
-    share(ts, 4 + wave, true);
+    share(ts, true);
     __syncthreads();
     float h[kEight + 1][2][4], decay[kEight][2][4];
 #pragma unroll
@@ -253,6 +296,8 @@ __global__ void __launch_bounds__(256, 2) scan_grad(ScanArgs a) {
 #pragma unroll
     for (int half = 1; half >= 0; --half) {
       __builtin_amdgcn_sched_barrier(0);
+      // (half of the eight's registers are free again)
+      if (half == 0 && sub > 0) fetch(ts - kEight);
       float folded = 0.f;
 #pragma unroll
       for (int q = 3; q >= 0; --q) {
@@ -314,15 +359,16 @@ __global__ void __launch_bounds__(256, 2) scan_grad(ScanArgs a) {
         const int64_t at = (b * a.l + t) * a.d + g0, all = a.b * a.l * a.d;
         if constexpr (MULTI) {
           float* out = a.sums + blk * 3 * all + at;
-          out[in + k] = gb;
-          (out + all)[in + k] = aq;
-          (out + 2 * all)[in + k] = ch;
+          out[in[k]] = gb;
+          (out + all)[in[k]] = aq;
+          (out + 2 * all)[in[k]] = ch;
         } else if (t < end) {
-          finish<T>(a, at, in + k, gb, aq, ch, of[U][j][2 * lane + k], of[DT][j][2 * lane + k],
-                    of[SLOPE][j][2 * lane + k], of[GO][j][2 * lane + k], of[DZ][j][2 * lane + k],
-                    a.skip ? (a.skip + g0)[in + k] : 0.f, dskip[k], dbias[k]);
+          const int i = 2 * lane + k;
+          const Token v = {of[U][j][i], of[DT][j][i], of[SLOPE][j][i], of[GO][j][i], of[DZ][j][i]};
+          finish<T, GATE>(a, at, in[k], gb, aq, ch, v, a.skip ? (a.skip + g0)[in[k]] : 0.f,
+                          dskip[k], dbias[k]);
         } else {
-          finish_none<T>(a, at, in + k);
+          finish_none<T, GATE>(a, at, in[k]);
         }
       }
       __syncthreads();
@@ -332,10 +378,10 @@ __global__ void __launch_bounds__(256, 2) scan_grad(ScanArgs a) {
   for (int k = 0; k < 2; ++k)
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const int n = blk * SPL + 4 * wave + s;
-      if (on[k]) (a.apart + ((row * a.nblk * SPL + n) * a.d + g0))[in + k] = da[k][s];
+      const int n = n0 + s;
+      if (on[k]) (a.apart + ((row * a.nblk * SPL + n) * a.d + g0))[in[k]] = da[k][s];
       if (on[k] && n < a.n && chunk == 0 && a.ds0)
-        (a.ds0 + ((b * a.d + g0) * a.n + n))[(in + k) * (uint32_t)a.n] = carry[k][s];
+        (a.ds0 + ((b * a.d + g0) * a.n + n))[in[k] * (uint32_t)a.n] = carry[k][s];
     }
   if constexpr (!MULTI) {
     // dD and dbias over the waves' tokens
@@ -355,8 +401,8 @@ __global__ void __launch_bounds__(256, 2) scan_grad(ScanArgs a) {
           y += sums[1][0][m][2 * lane + k];
         }
         if (on[k]) {
-          (a.dpart + (row * 2 * a.d + g0))[in + k] = x;
-          (a.dpart + ((row * 2 + 1) * a.d + g0))[in + k] = y;
+          (a.dpart + (row * 2 * a.d + g0))[in[k]] = x;
+          (a.dpart + ((row * 2 + 1) * a.d + g0))[in[k]] = y;
         }
       }
     }
@@ -365,38 +411,35 @@ __global__ void __launch_bounds__(256, 2) scan_grad(ScanArgs a) {
 
 // States in more than one block: the blocks' sums joined, one lane a channel
 // of a chunk.
-template <int T>
+template <int T, bool GATE>
 __global__ void __launch_bounds__(256) scan_finish(ScanArgs a) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t row = i / a.d;
   if (row >= a.b * a.nc) return;
-  const uint32_t c = (uint32_t)(i - row * a.d);
-  const bool on[2] = {true, false};
+  const uint32_t c[1] = {(uint32_t)(i - row * a.d)};
   const int64_t b = row / a.nc, len = length_of(a, b), t0 = (row - b * a.nc) * kGradChunk;
   const int64_t t1 = t0 + kGradChunk < a.l ? t0 + kGradChunk : a.l;
-  const float bias[2] = {a.bias ? a.bias[c] : 0.f, 0.f};
-  const float skip = a.skip ? a.skip[c] : 0.f;
+  const float bias = a.bias ? a.bias[c[0]] : 0.f, skip = a.skip ? a.skip[c[0]] : 0.f;
   const int64_t all = a.b * a.l * a.d;
   float dskip = 0.f, dbias = 0.f;
   for (int64_t t = t0; t < t1; ++t) {
     const int64_t at = (b * a.l + t) * a.d;
     if (t < len) {
-      Token<T> x;
-      x.load(a, b, t, 0, c, true, on, bias);
+      RawToken<T, 1, GATE> r;
+      r.load(a, b, t, 0, c);
       float gb = 0.f, aq = 0.f, ch = 0.f;
       for (int k = 0; k < a.nblk; ++k) {
-        gb += a.sums[3 * k * all + at + c];
-        aq += a.sums[(3 * k + 1) * all + at + c];
-        ch += a.sums[(3 * k + 2) * all + at + c];
+        gb += a.sums[3 * k * all + at + c[0]];
+        aq += a.sums[(3 * k + 1) * all + at + c[0]];
+        ch += a.sums[(3 * k + 2) * all + at + c[0]];
       }
-      finish<T>(a, at, c, gb, aq, ch, x.u[0], x.dt[0], x.slope[0], x.go[0], x.dz[0], skip, dskip,
-                dbias);
+      finish<T, GATE>(a, at, c[0], gb, aq, ch, token_of(a, r, 0, bias, true), skip, dskip, dbias);
     } else {
-      finish_none<T>(a, at, c);
+      finish_none<T, GATE>(a, at, c[0]);
     }
   }
-  a.dpart[row * 2 * a.d + c] = dskip;
-  a.dpart[(row * 2 + 1) * a.d + c] = dbias;
+  a.dpart[row * 2 * a.d + c[0]] = dskip;
+  a.dpart[(row * 2 + 1) * a.d + c[0]] = dbias;
 }
 
 // dB and dC from the channel blocks' parts, in order.
@@ -421,17 +464,23 @@ __global__ void __launch_bounds__(256) scan_bc_sum(ScanArgs a) {
   store1<T>(second ? a.dc : a.db, i, v);
 }
 
-template <int T>
-void go_grad(const ScanArgs& a, hipStream_t st) {
+template <int T, bool GATE>
+void go_gate(const ScanArgs& a, hipStream_t st) {
   const int pairs = (a.dg + kPair - 1) / kPair;
   const dim3 grid((uint32_t)(a.b * a.nc * a.g * pairs * a.nblk));
   if (a.nblk > 1) {
-    hipLaunchKernelGGL((scan_grad<T, true>), grid, dim3(256), 0, st, a);
-    hipLaunchKernelGGL((scan_finish<T>), dim3((uint32_t)((a.b * a.nc * a.d + 255) / 256)),
+    hipLaunchKernelGGL((scan_grad<T, GATE, true>), grid, dim3(256), 0, st, a);
+    hipLaunchKernelGGL((scan_finish<T, GATE>), dim3((uint32_t)((a.b * a.nc * a.d + 255) / 256)),
                        dim3(256), 0, st, a);
   } else {
-    hipLaunchKernelGGL((scan_grad<T, false>), grid, dim3(256), 0, st, a);
+    hipLaunchKernelGGL((scan_grad<T, GATE, false>), grid, dim3(256), 0, st, a);
   }
+}
+
+template <int T>
+void go_grad(const ScanArgs& a, hipStream_t st) {
+  if (a.z) go_gate<T, true>(a, st);
+  else go_gate<T, false>(a, st);
   const int64_t vals = 2 * a.b * a.l * a.g * a.n;
   if (vals > 0)
     hipLaunchKernelGGL((scan_bc_sum<T>), dim3((uint32_t)((vals + 255) / 256)), dim3(256), 0, st, a);
