@@ -40,6 +40,13 @@ __device__ __forceinline__ float value(Raw<T> v) {
   else return from16<T>(v);
 }
 
+// Where a line of bc holds B and C of state s.  The gradients' waves have four
+// states each and take both with one load.
+template <int SPL, bool BWD>
+constexpr int b_at(int s) { return BWD ? s / 4 * 8 + s % 4 : s; }
+template <int SPL, bool BWD>
+constexpr int c_at(int s) { return BWD ? s / 4 * 8 + 4 + s % 4 : SPL + s; }
+
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
 __device__ __forceinline__ float sigmoid(float x) {

@@ -16,20 +16,21 @@ namespace dwc {
 namespace seq {
 namespace scan {
 
-template <int T>
+template <int T, bool BWD>
 __global__ void __launch_bounds__(256) scan_prep(ScanArgs a) {
-  const int w = 2 * a.spl, line = a.nblk * w;
+  const int w = 2 * a.spl;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t token = i / ((int64_t)a.g * line);  // of b l
-  if (token >= a.b * a.l) return;
-  const int at = (int)(i - token * a.g * line), g = at / line, k = at - g * line;
-  const int blk = k / w, j = k - blk * w, s = blk * a.spl + j % a.spl;
-  const int64_t b = token / a.l, t = token - b * a.l;
+  const int64_t line = i / w, row = line / a.lp, t = line - row * a.lp;  // row: of b g nblk
+  const int64_t gr = row / a.nblk, b = gr / a.g;
+  if (b >= a.b) return;
+  const int j = (int)(i - line * w), blk = (int)(row - gr * a.nblk), g = (int)(gr - b * a.g);
+  // states in order, or by fours with B and C in turn
+  const bool second = BWD ? j & 4 : j >= a.spl;
+  const int s = blk * a.spl + (BWD ? j / 8 * 4 + j % 4 : (second ? j - a.spl : j));
   float v = 0.f;
   if (s < a.n && t < length_of(a, b))
-    v = j < a.spl
-            ? load1<T>(a.bm, b * a.b_stride[0] + t * a.b_stride[1] + g * a.b_stride[2] + s)
-            : load1<T>(a.cm, b * a.c_stride[0] + t * a.c_stride[1] + g * a.c_stride[2] + s);
+    v = second ? load1<T>(a.cm, b * a.c_stride[0] + t * a.c_stride[1] + g * a.c_stride[2] + s)
+               : load1<T>(a.bm, b * a.b_stride[0] + t * a.b_stride[1] + g * a.b_stride[2] + s);
   a.bc[i] = v;
 }
 
@@ -80,24 +81,39 @@ __device__ __forceinline__ void load_a(const ScanArgs& a, const Where& w, float 
   for (int s = 0; s < SPL; ++s) v[s] = w.blk * SPL + s < a.n ? kLog2e * v[s] : 0.f;
 }
 
+// B and C of the chunk's first token.
+template <int SPL>
+__device__ __forceinline__ const float* lines(const ScanArgs& a, const Where& w) {
+  return a.bc + (((w.b * a.g + w.g) * a.nblk + w.blk) * a.lp + w.t0) * (2 * SPL);
+}
+
 constexpr int kAhead = 4;  // tokens whose loads are under way together
 
-// Raw operands of N tensors: U tokens from t on, those from end on give the
-// last one's again.  p: addresses that are the same in all lanes, of the
-// group's first channel.
+// Raw operands of N tensors, U tokens of them.  p: addresses of the next
+// token that are the same in all lanes, of the group's first channel; step:
+// bytes between tokens.
 template <int T, int N, int U>
 struct Ahead {
   Raw<T> v[N][U];
-  __device__ __forceinline__ void load(const void* const (&p)[N], const int64_t (&step)[N],
-                                       uint32_t in, int64_t t, int64_t end) {
+  __device__ __forceinline__ void load(const char* (&p)[N], const int64_t (&step)[N],
+                                       uint32_t in) {
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int64_t at = t + i < end ? t + i : end - 1;
+    for (int i = 0; i < U; ++i)
 #pragma unroll
-      for (int k = 0; k < N; ++k) v[k][i] = ((const Raw<T>*)p[k] + at * step[k])[in];
-    }
+      for (int k = 0; k < N; ++k) {
+        v[k][i] = ((const Raw<T>*)p[k])[in];
+        p[k] += step[k];
+      }
   }
 };
+
+// Address of token t0 of a tensor.
+template <int T>
+__device__ __forceinline__ const char* from(const void* p, const int64_t (&stride)[2],
+                                            const Where& w, int64_t& step) {
+  step = stride[1] * (int64_t)sizeof(Raw<T>);
+  return (const char*)((const Raw<T>*)p + (w.b * stride[0] + w.t0 * stride[1] + w.g0));
+}
 
 template <int T>
 __device__ __forceinline__ float step_of(const ScanArgs& a, Raw<T> delta, float bias) {
@@ -124,35 +140,28 @@ __global__ void __launch_bounds__(64) scan_chunk(ScanArgs a) {
   if (w.t0 < end) {
     const float bias = a.bias ? a.bias[w.c] : 0.f;
     constexpr int N = BWD ? (GATE ? 4 : 3) : 2;
-    const int64_t e = sizeof(Raw<T>);
-    const void* ptr[N];
+    const char* ptr[N];
     int64_t step[N];
-    ptr[0] = (const char*)a.u + (w.b * a.u_stride[0] + w.g0) * e;
-    step[0] = a.u_stride[1];
-    ptr[1] = (const char*)a.delta + (w.b * a.delta_stride[0] + w.g0) * e;
-    step[1] = a.delta_stride[1];
+    ptr[0] = from<T>(a.u, a.u_stride, w, step[0]);
+    ptr[1] = from<T>(a.delta, a.delta_stride, w, step[1]);
     if constexpr (BWD) {
-      ptr[2] = (const char*)a.dy + (w.b * a.dy_stride[0] + w.g0) * e;
-      step[2] = a.dy_stride[1];
-      if constexpr (GATE) {
-        ptr[3] = (const char*)a.z + (w.b * a.z_stride[0] + w.g0) * e;
-        step[3] = a.z_stride[1];
-      }
+      ptr[2] = from<T>(a.dy, a.dy_stride, w, step[2]);
+      if constexpr (GATE) ptr[3] = from<T>(a.z, a.z_stride, w, step[3]);
     }
-    const int64_t line = (int64_t)a.g * a.nblk * 2 * SPL;
-    const float* bc = a.bc + (w.b * a.l + w.t0) * line + (w.g * a.nblk + w.blk) * 2 * SPL;
+    const float* bc = lines<SPL>(a, w);
     const auto token = [&](const auto& x, int i) {
-      const auto bb = load_scalar<SPL>(bc);
+      // (forward only B is read)
+      const auto lo = load_scalar<SPL>(bc), hi = load_scalar<SPL>(bc + (BWD ? SPL : 0));
+      const auto at = [&](int k) { return k < SPL ? lo[k < SPL ? k : 0] : hi[k < SPL ? 0 : k - SPL]; };
       const float dt = step_of<T>(a, x.v[1][i], bias), du = dt * value<T>(x.v[0][i]);
       sum += dt;
       float k[SPL];
 #pragma unroll
       for (int s = 0; s < SPL; ++s) {
         k[s] = exp2_of(dt * a2[s]);
-        h[s] = fmaf(k[s], h[s], du * bb[s]);
+        h[s] = fmaf(k[s], h[s], du * at(b_at<SPL, BWD>(s)));
       }
       if constexpr (BWD) {
-        const auto cc = load_scalar<SPL>(bc + SPL);
         float go = value<T>(x.v[2][i]);
         if constexpr (GATE) {
           const float z = value<T>(x.v[3][i]);
@@ -161,23 +170,23 @@ __global__ void __launch_bounds__(64) scan_chunk(ScanArgs a) {
 #pragma unroll
         for (int s = 0; s < SPL; ++s) {
           p[s] *= k[s];
-          r[s] = fmaf(p[s], cc[s] * go, r[s]);
+          r[s] = fmaf(p[s], at(c_at<SPL, BWD>(s)) * go, r[s]);
         }
       }
-      bc += line;
+      bc += 2 * SPL;
     };
     Ahead<T, N, kAhead> now, next;
-    now.load(ptr, step, w.in, w.t0, end);
     int64_t t = w.t0;
+    if (t + kAhead <= end) now.load(ptr, step, w.in);
     for (; t + kAhead <= end; t += kAhead) {
-      next.load(ptr, step, w.in, t + kAhead, end);
+      if (t + 2 * kAhead <= end) next.load(ptr, step, w.in);
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) token(now, i);
       now = next;
     }
     for (; t < end; ++t) {
       Ahead<T, N, 1> one;
-      one.load(ptr, step, w.in, t, end);
+      one.load(ptr, step, w.in);
       token(one, 0);
     }
   }
@@ -257,24 +266,17 @@ __global__ void __launch_bounds__(MULTI ? 1024 : 64) scan_out(ScanArgs a) {
 #pragma unroll
     for (int s = 0; s < SPL; ++s) h[s] = 0.f;
   }
-  Raw<T>* const out = (Raw<T>*)a.y + w.b * a.l * a.d + w.g0;
+  Raw<T>* out = (Raw<T>*)a.y + ((w.b * a.l + w.t0) * a.d + w.g0);  // of token t
   int64_t t = w.t0;
   if (t < end) {
     const float bias = a.bias ? a.bias[w.c] : 0.f, skip = a.skip ? a.skip[w.c] : 0.f;
-    const int64_t e = sizeof(Raw<T>);
     constexpr int N = GATE ? 3 : 2;
-    const void* ptr[N];
+    const char* ptr[N];
     int64_t step[N];
-    ptr[0] = (const char*)a.u + (w.b * a.u_stride[0] + w.g0) * e;
-    step[0] = a.u_stride[1];
-    ptr[1] = (const char*)a.delta + (w.b * a.delta_stride[0] + w.g0) * e;
-    step[1] = a.delta_stride[1];
-    if constexpr (GATE) {
-      ptr[2] = (const char*)a.z + (w.b * a.z_stride[0] + w.g0) * e;
-      step[2] = a.z_stride[1];
-    }
-    const int64_t line = (int64_t)a.g * a.nblk * 2 * SPL;
-    const float* bc = a.bc + (w.b * a.l + w.t0) * line + (w.g * a.nblk + w.blk) * 2 * SPL;
+    ptr[0] = from<T>(a.u, a.u_stride, w, step[0]);
+    ptr[1] = from<T>(a.delta, a.delta_stride, w, step[1]);
+    if constexpr (GATE) ptr[2] = from<T>(a.z, a.z_stride, w, step[2]);
+    const float* bc = lines<SPL>(a, w);
     const auto token = [&](const auto& x, int i) {
       const auto bb = load_scalar<SPL>(bc);
       const auto cc = load_scalar<SPL>(bc + SPL);
@@ -285,27 +287,27 @@ __global__ void __launch_bounds__(MULTI ? 1024 : 64) scan_out(ScanArgs a) {
         h[s] = fmaf(exp2_of(dt * a2[s]), h[s], du * bb[s]);
         y = fmaf(cc[s], h[s], y);
       }
-      bc += line;
+      bc += 2 * SPL;
       return y;
     };
-    const auto finish = [&](const auto& x, int i, int64_t at, float y) {
+    const auto finish = [&](const auto& x, int i, float y) {
       y = fmaf(skip, value<T>(x.v[0][i]), y);
       if constexpr (GATE) {
         const float z = value<T>(x.v[2][i]);
         y *= z * sigmoid(z);
       }
-      store1<T>(out + at * a.d, w.in, y);
+      store1<T>(out + (int64_t)i * a.d, w.in, y);
     };
     Ahead<T, N, kAhead> now, next;
-    now.load(ptr, step, w.in, t, end);
+    if (t + kAhead <= end) now.load(ptr, step, w.in);
     int side = 0;
     for (; t + kAhead <= end; t += kAhead) {
-      next.load(ptr, step, w.in, t + kAhead, end);
+      if (t + 2 * kAhead <= end) next.load(ptr, step, w.in);
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const float y = token(now, i);
         if constexpr (MULTI) lds[side][wave][i][lane] = y;
-        else finish(now, i, t + i, y);
+        else finish(now, i, y);
       }
       if constexpr (MULTI) {
         __syncthreads();  // (two sides: one barrier keeps readers and writers apart)
@@ -314,16 +316,17 @@ __global__ void __launch_bounds__(MULTI ? 1024 : 64) scan_out(ScanArgs a) {
           if (i % a.nblk == wave) {
             float y = 0.f;
             for (int k = 0; k < a.nblk; ++k) y += lds[side][k][i][lane];
-            finish(now, i, t + i, y);
+            finish(now, i, y);
           }
         }
         side ^= 1;
       }
       now = next;
+      out += (int64_t)kAhead * a.d;
     }
     for (; t < end; ++t) {
       Ahead<T, N, 1> one;
-      one.load(ptr, step, w.in, t, end);
+      one.load(ptr, step, w.in);
       float y = token(one, 0);
       if constexpr (MULTI) {
         lds[side][wave][0][lane] = y;
@@ -331,16 +334,17 @@ __global__ void __launch_bounds__(MULTI ? 1024 : 64) scan_out(ScanArgs a) {
         if (wave == 0) {
           y = 0.f;
           for (int k = 0; k < a.nblk; ++k) y += lds[side][k][0][lane];
-          finish(one, 0, t, y);
+          finish(one, 0, y);
         }
         side ^= 1;
       } else {
-        finish(one, 0, t, y);
+        finish(one, 0, y);
       }
+      out += a.d;
     }
   }
   if (wave == 0)
-    for (; t < w.t1; ++t) store1<T>(out + t * a.d, w.in, 0.f);
+    for (; t < w.t1; ++t, out += a.d) store1<T>(out, w.in, 0.f);
   if (w.chunk + 1 == a.nc) {
     float* p = a.s1 + (w.b * a.d + w.g0) * a.n;
 #pragma unroll
@@ -354,8 +358,8 @@ __global__ void __launch_bounds__(MULTI ? 1024 : 64) scan_out(ScanArgs a) {
 template <int T, int SPL, bool BWD, bool GATE>
 void prepare(const ScanArgs& a, hipStream_t st) {
   if (a.l > 0) {
-    const int64_t vals = a.b * a.l * a.g * a.nblk * 2 * a.spl;
-    hipLaunchKernelGGL((scan_prep<T>), dim3((uint32_t)((vals + 255) / 256)), dim3(256), 0, st, a);
+    const int64_t vals = a.b * a.lp * a.g * a.nblk * 2 * a.spl;
+    hipLaunchKernelGGL((scan_prep<T, BWD>), dim3((uint32_t)((vals + 255) / 256)), dim3(256), 0, st, a);
   }
   if (a.nc > 1) {
     const dim3 grid((uint32_t)(a.b * a.nc * a.g * a.cblk * a.nblk));
@@ -405,8 +409,9 @@ void scan_split(ScanArgs* a, bool bwd) {
   a->spl = bwd ? 16 : (a->n <= 4 ? 4 : (a->n <= 8 ? 8 : 16));
   a->nblk = (a->n + a->spl - 1) / a->spl;
   a->cblk = (a->dg + 63) / 64;
+  a->lp = (a->l + kGradChunk - 1) / kGradChunk * kGradChunk;
   if (bwd) {
-    a->tc = 32;
+    a->tc = kGradChunk;
   } else {
     const int64_t waves = a->b * a->g * a->cblk * a->nblk;
     int64_t nc = waves >= 2048 || a->b == 0 ? 1 : 4096 / waves;

@@ -24,7 +24,8 @@ hipError_t launch_scan_prepare_bwd(const ScanArgs& a, hipStream_t st);
 
 namespace scan {
 
-constexpr int kEight = 8, kSubs = 4, kGradChunk = kEight * kSubs, kPair = 128;
+constexpr int kEight = 8, kSubs = kGradChunk / kEight;
+constexpr int NC = kGradChannels / 64, kPair = kGradChannels;  // channels a lane, a workgroup
 
 // a = sums of the halves of a (lanes 0 to 31) and of b (32 to 63), the same
 // by rows of 16, by halves of a row and by its fours.
@@ -58,31 +59,33 @@ __device__ __forceinline__ float fold2(float a, float b, int lane) {
   return v + row_move<0x4E>(v);
 }
 
-// Raw operands of one token of NC neighbouring channels.  first: the index of
-// the group's first channel (the same in all lanes of scan_grad, as b and t
-// are, so that lanes add a 32-bit offset to a scalar address).
+// Raw operands of one token of NC channels: u, delta, dy and, with a gate, z.
 template <int T, int NC, bool GATE>
 struct RawToken {
-  Raw<T> u[NC], delta[NC], dy[NC], z[NC];
-  __device__ __forceinline__ void load(const ScanArgs& a, int64_t b, int64_t t, int64_t first,
-                                       const uint32_t (&in)[NC]) {
-    typedef const Raw<T>* ptr;
-    const ptr pu = (ptr)a.u + (b * a.u_stride[0] + t * a.u_stride[1] + first);
-    const ptr pd = (ptr)a.delta + (b * a.delta_stride[0] + t * a.delta_stride[1] + first);
-    const ptr py = (ptr)a.dy + (b * a.dy_stride[0] + t * a.dy_stride[1] + first);
+  static constexpr int N = GATE ? 4 : 3;
+  Raw<T> v[N][NC];
+  // p: addresses that are the same in all lanes
+  __device__ __forceinline__ void load(const char* const (&p)[N], const uint32_t (&in)[NC]) {
 #pragma unroll
-    for (int k = 0; k < NC; ++k) {
-      u[k] = pu[in[k]];
-      delta[k] = pd[in[k]];
-      dy[k] = py[in[k]];
-    }
-    if constexpr (GATE) {
-      const ptr pz = (ptr)a.z + (b * a.z_stride[0] + t * a.z_stride[1] + first);
+    for (int i = 0; i < N; ++i)
 #pragma unroll
-      for (int k = 0; k < NC; ++k) z[k] = pz[in[k]];
-    }
+      for (int k = 0; k < NC; ++k) v[i][k] = ((const Raw<T>*)p[i])[in[k]];
   }
 };
+
+// Addresses of token t, channel `first`, and the bytes between tokens.
+template <int T, int N>
+__device__ __forceinline__ void addresses(const ScanArgs& a, int64_t b, int64_t t, int64_t first,
+                                          const char* (&p)[N], int64_t (&step)[N]) {
+  const auto set = [&](int i, const void* q, const int64_t (&stride)[2]) {
+    p[i] = (const char*)((const Raw<T>*)q + (b * stride[0] + t * stride[1] + first));
+    step[i] = stride[1] * (int64_t)sizeof(Raw<T>);
+  };
+  set(0, a.u, a.u_stride);
+  set(1, a.delta, a.delta_stride);
+  set(2, a.dy, a.dy_stride);
+  if constexpr (N > 3) set(3, a.z, a.z_stride);
+}
 
 // What they say: the step, its slope in delta, do and dy silu'(z).  Zeros
 // where the token or the channel is not there.
@@ -93,14 +96,14 @@ template <int T, int NC, bool GATE>
 __device__ __forceinline__ Token token_of(const ScanArgs& a, const RawToken<T, NC, GATE>& r, int k,
                                           float bias, bool live) {
   Token v;
-  v.u = value<T>(r.u[k]);
-  const float x = value<T>(r.delta[k]) + bias, s = softplus(x);
+  v.u = value<T>(r.v[0][k]);
+  const float x = value<T>(r.v[1][k]) + bias, s = softplus(x);
   v.dt = a.softplus ? s : x;  // (selects: branches would split the code)
   v.slope = a.softplus ? sigmoid(x) : 1.f;
-  v.go = value<T>(r.dy[k]);
+  v.go = value<T>(r.v[2][k]);
   v.dz = 0.f;
   if constexpr (GATE) {
-    const float z = value<T>(r.z[k]), g = sigmoid(z);
+    const float z = value<T>(r.v[GATE ? 3 : 0][k]), g = sigmoid(z);
     v.dz = v.go * fmaf(z * g, 1.f - g, g);
     v.go *= z * g;
   }
@@ -114,8 +117,8 @@ __device__ __forceinline__ Token token_of(const ScanArgs& a, const RawToken<T, N
 
 // Outputs of one token of one channel from its sums over the states: of
 // G B, of A q (in units of 1 / log2 e) and of C h.
-template <int T, bool GATE>
-__device__ __forceinline__ void finish(const ScanArgs& a, int64_t at, uint32_t in, float gb,
+template <int T, bool GATE, class Args>
+__device__ __forceinline__ void finish(const Args& a, int64_t at, uint32_t in, float gb,
                                        float aq, float ch, const Token& v, float skip,
                                        float& dskip, float& dbias) {
   const float dd = fmaf(v.u, gb, kLn2 * aq) * v.slope;
@@ -127,21 +130,30 @@ __device__ __forceinline__ void finish(const ScanArgs& a, int64_t at, uint32_t i
 }
 
 // Zeros behind a sequence's last token.
-template <int T, bool GATE>
-__device__ __forceinline__ void finish_none(const ScanArgs& a, int64_t at, uint32_t in) {
+template <int T, bool GATE, class Args>
+__device__ __forceinline__ void finish_none(const Args& a, int64_t at, uint32_t in) {
   store1<T>((Raw<T>*)a.du + at, in, 0.f);
   store1<T>((Raw<T>*)a.ddelta + at, in, 0.f);
   if constexpr (GATE) store1<T>((Raw<T>*)a.dz + at, in, 0.f);
 }
 
+// The kernel's arguments, read again from their segment: held in registers
+// over the whole kernel they push others out to memory.
+typedef const __attribute__((address_space(4))) ScanArgs FreshArgs;
+__device__ __forceinline__ FreshArgs& fresh_args() {
+  FreshArgs* p = (FreshArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *p;
+}
+
 enum { DT = 0, U, GO, SLOPE, DZ, kOf };  // of a token and channel, in LDS
 
 template <int T, bool GATE, bool MULTI>
-__global__ void __launch_bounds__(256, 2) scan_grad(ScanArgs a) {
+__global__ void __launch_bounds__(256, NC == 1 ? 4 : 2) scan_grad(ScanArgs a) {
   constexpr int NW = 4, SPL = 4 * NW;
   __shared__ float of[kOf][kEight][kPair];
   __shared__ float sums[3][4][NW][kPair];     // over a wave's states
-  __shared__ float first[kSubs][2 * 4][256];  // states before the eights
+  __shared__ float first[kSubs][NC * 4][256];  // states before the eights
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int pairs = (a.dg + kPair - 1) / kPair;
   uint32_t i = blockIdx.x;
@@ -158,17 +170,23 @@ __global__ void __launch_bounds__(256, 2) scan_grad(ScanArgs a) {
   const int64_t end = t1 < len ? t1 : len;
   const int64_t g0 = (int64_t)g * a.dg, row = b * a.nc + chunk;
   // channels of the group; lanes past its end read its first one again
-  const uint32_t c0 = (uint32_t)(block * kPair + 2 * lane);
-  const bool on[2] = {(int)c0 < a.dg, (int)c0 + 1 < a.dg};
-  const uint32_t in[2] = {on[0] ? c0 : 0, on[1] ? c0 + 1 : 0};
-  float dskip[2] = {0.f, 0.f}, dbias[2] = {0.f, 0.f};
-  float a2[2][4], da[2][4], carry[2][4], h[2][4];
+  const uint32_t c0 = (uint32_t)(block * kPair + NC * lane);
+  bool on[NC];
+  uint32_t in[NC];
+  float dskip[NC], dbias[NC];
+#pragma unroll
+  for (int k = 0; k < NC; ++k) {
+    on[k] = (int)c0 + k < a.dg;
+    in[k] = on[k] ? c0 + k : 0;
+    dskip[k] = dbias[k] = 0.f;
+  }
+  float a2[NC][4], da[NC][4], carry[NC][4], h[NC][4];
   const int n0 = blk * SPL + 4 * wave;
   // (all loads under way together, then what is not there made zero)
   {
-    const auto states = [&](const float* p, float(&v)[2][4]) {  // of d x n
+    const auto states = [&](const float* p, float(&v)[NC][4]) {  // of d x n
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int k = 0; k < NC; ++k)
 #pragma unroll
         for (int s = 0; s < 4; ++s)
           v[k][s] = (p + (n0 + s < a.n ? n0 + s : 0))[in[k] * (uint32_t)a.n];
@@ -177,7 +195,7 @@ __global__ void __launch_bounds__(256, 2) scan_grad(ScanArgs a) {
     if (a.nc > 1) {
       const int64_t at = (row * a.nblk * SPL + n0) * a.d + g0;
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int k = 0; k < NC; ++k)
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           h[k][s] = (a.states + at + (int64_t)s * a.d)[in[k]];
@@ -186,14 +204,14 @@ __global__ void __launch_bounds__(256, 2) scan_grad(ScanArgs a) {
     } else {
       const int64_t at = (b * a.d + g0) * a.n;
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int k = 0; k < NC; ++k)
 #pragma unroll
         for (int s = 0; s < 4; ++s) h[k][s] = carry[k][s] = 0.f;
       if (a.s0) states(a.s0 + at, h);
       if (a.ds1) states(a.ds1 + at, carry);
     }
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int k = 0; k < NC; ++k)
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         const bool is = on[k] && n0 + s < a.n;
@@ -203,64 +221,82 @@ __global__ void __launch_bounds__(256, 2) scan_grad(ScanArgs a) {
         da[k][s] = 0.f;
       }
   }
-  const int64_t line = (int64_t)a.g * a.nblk * 2 * SPL;
-  const int64_t lines = (int64_t)(g * a.nblk + blk) * 2 * SPL;
-  const float* bc = a.bc + b * a.l * line + lines + 4 * wave;
-  // rows of B and C past the last token are not there
-  const auto bc_at = [&](int64_t t) { return bc + (t < a.l ? t : a.l - 1) * line; };
+  // B and C of the wave's states, tokens 2 SPL apart; rows up to whole chunks
+  // are there
+  const int64_t lines = (((b * a.g + g) * a.nblk + blk) * a.lp + t0) * (2 * SPL);
+  const float* const bc = a.bc + lines + 8 * wave;
+  float* const bcpart = a.bcpart + block * (a.b * a.g * a.nblk * a.lp * 2 * SPL) + lines + 8 * wave;
 
-  // a wave's own tokens of an eight: wave and 4 + wave; a token past the last
-  // one is read as the last
-  RawToken<T, 2, GATE> raw[2];
-  const auto fetch = [&](int64_t ts) {
+  // a wave's own tokens of an eight, wave and 4 + wave; a token past the last
+  // one is read as the chunk's first
+  constexpr int N = GATE ? 4 : 3;
+  RawToken<T, NC, GATE> raw[2];
+  const char *first_at[N], *at[N];
+  int64_t step[N];
+  addresses<T, N>(a, b, t0, g0, first_at, step);
+#pragma unroll
+  for (int i = 0; i < N; ++i) at[i] = first_at[i] + wave * step[i];
+  const auto fetch = [&](int sub) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int64_t t = ts + 4 * j + wave;
-      raw[j].load(a, b, t < end ? t : (end > 0 ? end - 1 : 0), g0, in);
+      const bool there = t0 + sub * kEight + 4 * j + wave < end;
+      const char* p[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        p[i] = there ? at[i] + (sub * kEight + 4 * j) * step[i] : first_at[i];
+      raw[j].load(p, in);
     }
   };
   const auto share = [&](int64_t ts, bool all) {
     // (the bias is read again for each eight: registers are short)
     const float* pb = a.bias ? a.bias + g0 : nullptr;
-    const float bias[2] = {pb ? pb[in[0]] : 0.f, pb ? pb[in[1]] : 0.f};
+    float bias[NC];
+#pragma unroll
+    for (int k = 0; k < NC; ++k) bias[k] = pb ? pb[in[k]] : 0.f;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int at = 4 * j + wave;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < NC; ++k) {
         const Token v = token_of(a, raw[j], k, bias[k], on[k] && ts + at < end);
-        of[DT][at][2 * lane + k] = v.dt;
-        of[U][at][2 * lane + k] = v.u;
+        of[DT][at][NC * lane + k] = v.dt;
+        of[U][at][NC * lane + k] = v.u;
         if (all) {
-          of[GO][at][2 * lane + k] = v.go;
-          of[SLOPE][at][2 * lane + k] = v.slope;
-          of[DZ][at][2 * lane + k] = v.dz;
+          of[GO][at][NC * lane + k] = v.go;
+          of[SLOPE][at][NC * lane + k] = v.slope;
+          of[DZ][at][NC * lane + k] = v.dz;
         }
       }
     }
   };
 
+  // where fold2 leaves this lane's value: B of state s, C of it four further,
+  // the second token's a line further
+  const uint32_t out_at = (uint32_t)((lane >> 5) + 2 * (lane >> 4 & 1) + (lane & 8 ? 4 : 0) +
+                                     (lane & 4 ? 2 * SPL : 0));
+
   // the states before the eights
   const bool some = t0 < a.l;
-  if (some) fetch(t0);
+  if (some) fetch(0);
 #pragma unroll 1
   for (int sub = 0; sub < kSubs; ++sub) {
     const int64_t ts = t0 + sub * kEight;
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int k = 0; k < NC; ++k)
 #pragma unroll
       for (int s = 0; s < 4; ++s) first[sub][4 * k + s][threadIdx.x] = h[k][s];
     if (sub + 1 == kSubs || ts >= end) continue;  // (the same in all waves)
     __syncthreads();
     share(ts, false);
-    fetch(ts + kEight);
+    fetch(sub + 1);
     __syncthreads();
+    const float* const rows = bc + sub * (kEight * 2 * SPL);
 #pragma unroll
     for (int j = 0; j < kEight; ++j) {
-      const f32x4 bb = load_scalar<4>(bc_at(ts + j));
+      const f32x4 bb = load_scalar<4>(rows + j * (2 * SPL));
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float dt = of[DT][j][2 * lane + k], du = dt * of[U][j][2 * lane + k];
+      for (int k = 0; k < NC; ++k) {
+        const float dt = of[DT][j][NC * lane + k], du = dt * of[U][j][NC * lane + k];
 #pragma unroll
         for (int s = 0; s < 4; ++s) h[k][s] = fmaf(exp2_of(dt * a2[k][s]), h[k][s], du * bb[s]);
       }
@@ -268,48 +304,54 @@ __global__ void __launch_bounds__(256, 2) scan_grad(ScanArgs a) {
   }
 
   const int last = some ? (int)((t1 - t0 - 1) / kEight) : -1;
-  if (some) fetch(t0 + last * kEight);
+  if (some) fetch(last);
 #pragma unroll 1
   for (int sub = last; sub >= 0; --sub) {
     const int64_t ts = t0 + sub * kEight;
     __syncthreads();
     share(ts, true);
     __syncthreads();
-    float h[kEight + 1][2][4], decay[kEight][2][4];
+    const float* const rows = bc + sub * (kEight * 2 * SPL);
+    float* const rows_out = bcpart + sub * (kEight * 2 * SPL);
+    float h[kEight + 1][NC][4], decay[kEight][NC][4];
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int k = 0; k < NC; ++k)
 #pragma unroll
       for (int s = 0; s < 4; ++s) h[0][k][s] = first[sub][4 * k + s][threadIdx.x];
 #pragma unroll
     for (int j = 0; j < kEight; ++j) {
-      const f32x4 bb = load_scalar<4>(bc_at(ts + j));
+      const f32x4 bb = load_scalar<4>(rows + j * (2 * SPL));
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float dt = of[DT][j][2 * lane + k], du = dt * of[U][j][2 * lane + k];
+      for (int k = 0; k < NC; ++k) {
+        const float dt = of[DT][j][NC * lane + k], du = dt * of[U][j][NC * lane + k];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           decay[j][k][s] = exp2_of(dt * a2[k][s]);
           h[j + 1][k][s] = fmaf(decay[j][k][s], h[j][k][s], du * bb[s]);
         }
       }
+      if (j % 2) __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int half = 1; half >= 0; --half) {
       __builtin_amdgcn_sched_barrier(0);
       // (half of the eight's registers are free again)
-      if (half == 0 && sub > 0) fetch(ts - kEight);
+      if (half == 0 && sub > 0) fetch(sub - 1);
       float folded = 0.f;
 #pragma unroll
       for (int q = 3; q >= 0; --q) {
+        __builtin_amdgcn_sched_barrier(0);
         const int j = 4 * half + q;
-        const f32x4 bb = load_scalar<4>(bc_at(ts + j)), cc = load_scalar<4>(bc_at(ts + j) + SPL);
-        float v[8], gb[2], aq[2], ch[2];
+        const auto bbcc = load_scalar<8>(rows + j * (2 * SPL));
+        const float bb[4] = {bbcc[0], bbcc[1], bbcc[2], bbcc[3]};
+        const float cc[4] = {bbcc[4], bbcc[5], bbcc[6], bbcc[7]};
+        float v[8], gb[NC], aq[NC], ch[NC];
 #pragma unroll
         for (int s = 0; s < 8; ++s) v[s] = 0.f;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float dt = of[DT][j][2 * lane + k], du = dt * of[U][j][2 * lane + k];
-          const float go = of[GO][j][2 * lane + k];
+        for (int k = 0; k < NC; ++k) {
+          const float dt = of[DT][j][NC * lane + k], du = dt * of[U][j][NC * lane + k];
+          const float go = of[GO][j][NC * lane + k];
           gb[k] = aq[k] = ch[k] = 0.f;
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
@@ -325,10 +367,10 @@ __global__ void __launch_bounds__(256, 2) scan_grad(ScanArgs a) {
           }
         }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          sums[0][q][wave][2 * lane + k] = gb[k];
-          sums[1][q][wave][2 * lane + k] = aq[k];
-          sums[2][q][wave][2 * lane + k] = ch[k];
+        for (int k = 0; k < NC; ++k) {
+          sums[0][q][wave][NC * lane + k] = gb[k];
+          sums[1][q][wave][NC * lane + k] = aq[k];
+          sums[2][q][wave][NC * lane + k] = ch[k];
         }
         const float f = fold8(v, lane);
         if (q & 1) {
@@ -336,46 +378,43 @@ __global__ void __launch_bounds__(256, 2) scan_grad(ScanArgs a) {
         } else {
           // tokens j (lanes without 4) and j + 1
           const float x = fold2(f, folded, lane);
-          const int64_t t = ts + j + (lane >> 2 & 1);
-          const int s = (lane >> 5) + 2 * (lane >> 4 & 1);
-          if ((lane & 3) == 0 && t < t1)
-            a.bcpart[((int64_t)block * a.b + b) * a.l * line + t * line + lines + 4 * wave + s +
-                     (lane & 8 ? SPL : 0)] = x;
+          if ((lane & 3) == 0) rows_out[out_at + j * (2 * SPL)] = x;
         }
       }
       __syncthreads();
+      FreshArgs& f = fresh_args();
       const int j = 4 * half + wave;
       const int64_t t = ts + j;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < NC; ++k) {
         float gb = 0.f, aq = 0.f, ch = 0.f;
 #pragma unroll
         for (int m = 0; m < NW; ++m) {
-          gb += sums[0][wave][m][2 * lane + k];
-          aq += sums[1][wave][m][2 * lane + k];
-          ch += sums[2][wave][m][2 * lane + k];
+          gb += sums[0][wave][m][NC * lane + k];
+          aq += sums[1][wave][m][NC * lane + k];
+          ch += sums[2][wave][m][NC * lane + k];
         }
         if (!on[k] || t >= t1) continue;
-        const int64_t at = (b * a.l + t) * a.d + g0, all = a.b * a.l * a.d;
+        const int64_t at = (b * f.l + t) * f.d + g0, all = f.b * f.l * f.d;
         if constexpr (MULTI) {
-          float* out = a.sums + blk * 3 * all + at;
+          float* out = f.sums + blk * 3 * all + at;
           out[in[k]] = gb;
           (out + all)[in[k]] = aq;
           (out + 2 * all)[in[k]] = ch;
         } else if (t < end) {
-          const int i = 2 * lane + k;
+          const int i = NC * lane + k;
           const Token v = {of[U][j][i], of[DT][j][i], of[SLOPE][j][i], of[GO][j][i], of[DZ][j][i]};
-          finish<T, GATE>(a, at, in[k], gb, aq, ch, v, a.skip ? (a.skip + g0)[in[k]] : 0.f,
+          finish<T, GATE>(f, at, in[k], gb, aq, ch, v, f.skip ? (f.skip + g0)[in[k]] : 0.f,
                           dskip[k], dbias[k]);
         } else {
-          finish_none<T, GATE>(a, at, in[k]);
+          finish_none<T, GATE>(f, at, in[k]);
         }
       }
       __syncthreads();
     }
   }
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
+  for (int k = 0; k < NC; ++k)
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const int n = n0 + s;
@@ -386,19 +425,19 @@ __global__ void __launch_bounds__(256, 2) scan_grad(ScanArgs a) {
   if constexpr (!MULTI) {
     // dD and dbias over the waves' tokens
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      sums[0][0][wave][2 * lane + k] = dskip[k];
-      sums[1][0][wave][2 * lane + k] = dbias[k];
+    for (int k = 0; k < NC; ++k) {
+      sums[0][0][wave][NC * lane + k] = dskip[k];
+      sums[1][0][wave][NC * lane + k] = dbias[k];
     }
     __syncthreads();
     if (wave == 0) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < NC; ++k) {
         float x = 0.f, y = 0.f;
 #pragma unroll
         for (int m = 0; m < NW; ++m) {
-          x += sums[0][0][m][2 * lane + k];
-          y += sums[1][0][m][2 * lane + k];
+          x += sums[0][0][m][NC * lane + k];
+          y += sums[1][0][m][NC * lane + k];
         }
         if (on[k]) {
           (a.dpart + (row * 2 * a.d + g0))[in[k]] = x;
@@ -425,8 +464,12 @@ __global__ void __launch_bounds__(256) scan_finish(ScanArgs a) {
   for (int64_t t = t0; t < t1; ++t) {
     const int64_t at = (b * a.l + t) * a.d;
     if (t < len) {
+      constexpr int N = GATE ? 4 : 3;
       RawToken<T, 1, GATE> r;
-      r.load(a, b, t, 0, c);
+      const char* p[N];
+      int64_t step[N];
+      addresses<T, N>(a, b, t, 0, p, step);
+      r.load(p, c);
       float gb = 0.f, aq = 0.f, ch = 0.f;
       for (int k = 0; k < a.nblk; ++k) {
         gb += a.sums[3 * k * all + at + c[0]];
@@ -456,9 +499,10 @@ __global__ void __launch_bounds__(256) scan_bc_sum(ScanArgs a) {
   const int pairs = (a.dg + kPair - 1) / kPair;
   float v = 0.f;
   if (t < length_of(a, b)) {
-    const int64_t size = a.b * a.l * a.g * a.nblk * 2 * a.spl;
-    const float* p = a.bcpart + (row * a.nblk + blk) * 2 * a.spl + s - blk * a.spl +
-                     (second ? a.spl : 0);
+    const int64_t size = a.b * a.lp * a.g * a.nblk * 2 * a.spl;
+    const int in = s - blk * a.spl, g = (int)(row - token * a.g);
+    const float* p = a.bcpart + (((b * a.g + g) * a.nblk + blk) * a.lp + t) * 2 * a.spl +
+                     (in / 4 * 8 + in % 4 + (second ? 4 : 0));
     for (int k = 0; k < pairs; ++k) v += p[k * size];
   }
   store1<T>(second ? a.dc : a.db, i, v);

@@ -61,15 +61,17 @@ struct ScanArgs {
   // that many, cblk blocks of 64 channels a group, nc chunks of tc tokens
   int dg, spl, nblk, cblk, tc, nc;
   // workspace
-  float* bc;       // [b][l][g][nblk][2 spl]: B and C in fp32, zeros past n and past a length
+  int64_t lp;      // l up to whole chunks of the gradients
+  float* bc;       // [b][g][nblk][lp][2 spl]: B and C in fp32, zeros past n and past a length
   float* states;   // [b][nc][nblk spl][d]
   float* rstates;  // the same, of the gradients
   float* dts;      // [b][nc][d]: sum of the steps
-  float* bcpart;   // [channel blocks a group][b][l][g][nblk][2 spl]
+  float* bcpart;   // [channel blocks a group][b][g][nblk][lp][2 spl]
   float* apart;    // [b nc][nblk spl][d]
   float* dpart;    // [b nc][2][d]
   float* sums;     // [nblk][3][b l d]
 };
+constexpr int kGradChannels = 64, kGradChunk = 32;  // of a workgroup of the gradients
 // Fills the split of the work.
 void scan_split(ScanArgs* a, bool bwd);
 hipError_t launch_scan_token(const ScanArgs& a, hipStream_t st);

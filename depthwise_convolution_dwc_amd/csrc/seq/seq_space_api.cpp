@@ -173,8 +173,8 @@ ScanArgs scan_args(const dwc_scan_problem* p, const void* u, const void* delta, 
 int scan_layout(ScanArgs* a, bool bwd, char* base, size_t* bytes) {
   scan_split(a, bwd);
   const int64_t line = (int64_t)a->nblk * 2 * a->spl, np = (int64_t)a->nblk * a->spl;
-  const int64_t tokens = a->b * a->l, rows = a->b * a->nc;
-  const int64_t pairs = (a->dg + 127) / 128;
+  const int64_t tokens = a->b * a->lp, rows = a->b * a->nc;
+  const int64_t pairs = (a->dg + kGradChannels - 1) / kGradChannels;
   // threads of the widest launches, and the index range
   if (tokens > kMost / (a->g * line) || tokens * a->g * line >= kLanes ||
       rows >= kLanes / 64 / ((int64_t)a->g * a->cblk * a->nblk) || a->b * np * a->d >= kLanes / 2 ||
