@@ -148,6 +148,22 @@ __device__ __forceinline__ FreshArgs& fresh_args() {
 
 enum { DT = 0, U, GO, SLOPE, DZ, kOf };  // of a token and channel, in LDS
 
+// What the way back needs of one token.
+struct OneToken {
+  f32x8 bc;
+  float dt[NC], u[NC], go[NC];
+  __device__ __forceinline__ void load(const float* p, const float (&of)[kOf][kEight][kPair], int j,
+                                       int lane) {
+    bc = load_scalar<8>(p);
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+      dt[k] = of[DT][j][NC * lane + k];
+      u[k] = of[U][j][NC * lane + k];
+      go[k] = of[GO][j][NC * lane + k];
+    }
+  }
+};
+
 template <int T, bool GATE, bool MULTI>
 __global__ void __launch_bounds__(256, NC == 1 ? 4 : 2) scan_grad(ScanArgs a) {
   constexpr int NW = 4, SPL = 4 * NW;
@@ -166,8 +182,9 @@ __global__ void __launch_bounds__(256, NC == 1 ? 4 : 2) scan_grad(ScanArgs a) {
   const int chunk = (int)(i % (uint32_t)a.nc);
   const int64_t b = i / (uint32_t)a.nc;
   const int64_t len = length_of(a, b), t0 = (int64_t)chunk * kGradChunk;
-  const int64_t t1 = t0 + kGradChunk < a.l ? t0 + kGradChunk : a.l;
-  const int64_t end = t1 < len ? t1 : len;
+  // tokens of the chunk, and of those inside the sequence's length
+  const int tokens = a.l - t0 < kGradChunk ? (int)(a.l - t0) : kGradChunk;
+  const int live = len <= t0 ? 0 : (len - t0 < tokens ? (int)(len - t0) : tokens);
   const int64_t g0 = (int64_t)g * a.dg, row = b * a.nc + chunk;
   // channels of the group; lanes past its end read its first one again
   const uint32_t c0 = (uint32_t)(block * kPair + NC * lane);
@@ -227,27 +244,38 @@ __global__ void __launch_bounds__(256, NC == 1 ? 4 : 2) scan_grad(ScanArgs a) {
   const float* const bc = a.bc + lines + 8 * wave;
   float* const bcpart = a.bcpart + block * (a.b * a.g * a.nblk * a.lp * 2 * SPL) + lines + 8 * wave;
 
-  // a wave's own tokens of an eight, wave and 4 + wave; a token past the last
-  // one is read as the chunk's first
+  // a wave's own tokens of an eight, wave and 4 + wave; next[] is the address
+  // of the first of them in the eight to be read.  Chunks cut short read a
+  // token past the last one as the chunk's first.
   constexpr int N = GATE ? 4 : 3;
   RawToken<T, NC, GATE> raw[2];
-  const char *first_at[N], *at[N];
-  int64_t step[N];
-  addresses<T, N>(a, b, t0, g0, first_at, step);
+  const bool whole = live == kGradChunk;
+  const char* next[N];
+  int64_t four[N];
+  addresses<T, N>(a, b, t0 + (whole ? wave : 0), g0, next, four);
 #pragma unroll
-  for (int i = 0; i < N; ++i) at[i] = first_at[i] + wave * step[i];
-  const auto fetch = [&](int sub) {
+  for (int i = 0; i < N; ++i) four[i] *= 4;
+  const auto fetch = [&](int sub, int turn) {
+    const char* p[N];
+    if (whole) {
+      raw[0].load(next, in);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const bool there = t0 + sub * kEight + 4 * j + wave < end;
-      const char* p[N];
+      for (int i = 0; i < N; ++i) {
+        p[i] = next[i] + four[i];
+        next[i] += 2 * turn * four[i];
+      }
+      raw[1].load(p, in);
+    } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        p[i] = there ? at[i] + (sub * kEight + 4 * j) * step[i] : first_at[i];
-      raw[j].load(p, in);
+      for (int j = 0; j < 2; ++j) {
+        const int t = sub * kEight + 4 * j + wave;
+#pragma unroll
+        for (int i = 0; i < N; ++i) p[i] = next[i] + (t < live ? t : 0) * (four[i] / 4);
+        raw[j].load(p, in);
+      }
     }
   };
-  const auto share = [&](int64_t ts, bool all) {
+  const auto share = [&](int sub, bool all) {
     // (the bias is read again for each eight: registers are short)
     const float* pb = a.bias ? a.bias + g0 : nullptr;
     float bias[NC];
@@ -258,7 +286,7 @@ __global__ void __launch_bounds__(256, NC == 1 ? 4 : 2) scan_grad(ScanArgs a) {
       const int at = 4 * j + wave;
 #pragma unroll
       for (int k = 0; k < NC; ++k) {
-        const Token v = token_of(a, raw[j], k, bias[k], on[k] && ts + at < end);
+        const Token v = token_of(a, raw[j], k, bias[k], on[k] && sub * kEight + at < live);
         of[DT][at][NC * lane + k] = v.dt;
         of[U][at][NC * lane + k] = v.u;
         if (all) {
@@ -270,25 +298,26 @@ __global__ void __launch_bounds__(256, NC == 1 ? 4 : 2) scan_grad(ScanArgs a) {
     }
   };
 
+  const int64_t row_out = (b * a.l + t0) * a.d + g0;  // of du, ddelta and dz
+
   // where fold2 leaves this lane's value: B of state s, C of it four further,
   // the second token's a line further
   const uint32_t out_at = (uint32_t)((lane >> 5) + 2 * (lane >> 4 & 1) + (lane & 8 ? 4 : 0) +
                                      (lane & 4 ? 2 * SPL : 0));
 
   // the states before the eights
-  const bool some = t0 < a.l;
-  if (some) fetch(0);
+  const int last = (tokens + kEight - 1) / kEight - 1;  // of the eights; -1 without tokens
+  if (last >= 0) fetch(0, 1);
 #pragma unroll 1
   for (int sub = 0; sub < kSubs; ++sub) {
-    const int64_t ts = t0 + sub * kEight;
 #pragma unroll
     for (int k = 0; k < NC; ++k)
 #pragma unroll
       for (int s = 0; s < 4; ++s) first[sub][4 * k + s][threadIdx.x] = h[k][s];
-    if (sub + 1 == kSubs || ts >= end) continue;  // (the same in all waves)
+    if (sub >= last) break;  // (the same in all waves)
     __syncthreads();
-    share(ts, false);
-    fetch(sub + 1);
+    share(sub, false);
+    fetch(sub + 1, sub + 1 < last ? 1 : -1);
     __syncthreads();
     const float* const rows = bc + sub * (kEight * 2 * SPL);
 #pragma unroll
@@ -303,13 +332,10 @@ __global__ void __launch_bounds__(256, NC == 1 ? 4 : 2) scan_grad(ScanArgs a) {
     }
   }
 
-  const int last = some ? (int)((t1 - t0 - 1) / kEight) : -1;
-  if (some) fetch(last);
 #pragma unroll 1
   for (int sub = last; sub >= 0; --sub) {
-    const int64_t ts = t0 + sub * kEight;
     __syncthreads();
-    share(ts, true);
+    share(sub, true);
     __syncthreads();
     const float* const rows = bc + sub * (kEight * 2 * SPL);
     float* const rows_out = bcpart + sub * (kEight * 2 * SPL);
@@ -332,26 +358,28 @@ __global__ void __launch_bounds__(256, NC == 1 ? 4 : 2) scan_grad(ScanArgs a) {
       }
       if (j % 2) __builtin_amdgcn_sched_barrier(0);
     }
+    OneToken ahead;
+    ahead.load(rows + (kEight - 1) * (2 * SPL), of, kEight - 1, lane);
 #pragma unroll
     for (int half = 1; half >= 0; --half) {
       __builtin_amdgcn_sched_barrier(0);
       // (half of the eight's registers are free again)
-      if (half == 0 && sub > 0) fetch(sub - 1);
+      if (half == 0 && sub > 0) fetch(sub - 1, -1);
       float folded = 0.f;
 #pragma unroll
       for (int q = 3; q >= 0; --q) {
         __builtin_amdgcn_sched_barrier(0);
         const int j = 4 * half + q;
-        const auto bbcc = load_scalar<8>(rows + j * (2 * SPL));
-        const float bb[4] = {bbcc[0], bbcc[1], bbcc[2], bbcc[3]};
-        const float cc[4] = {bbcc[4], bbcc[5], bbcc[6], bbcc[7]};
+        const OneToken now = ahead;  // (read while the token before it was computed)
+        if (j > 0) ahead.load(rows + (j - 1) * (2 * SPL), of, j - 1, lane);
+        const float bb[4] = {now.bc[0], now.bc[1], now.bc[2], now.bc[3]};
+        const float cc[4] = {now.bc[4], now.bc[5], now.bc[6], now.bc[7]};
         float v[8], gb[NC], aq[NC], ch[NC];
 #pragma unroll
         for (int s = 0; s < 8; ++s) v[s] = 0.f;
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
-          const float dt = of[DT][j][NC * lane + k], du = dt * of[U][j][NC * lane + k];
-          const float go = of[GO][j][NC * lane + k];
+          const float dt = now.dt[k], du = dt * now.u[k], go = now.go[k];
           gb[k] = aq[k] = ch[k] = 0.f;
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
@@ -384,7 +412,8 @@ __global__ void __launch_bounds__(256, NC == 1 ? 4 : 2) scan_grad(ScanArgs a) {
       __syncthreads();
       FreshArgs& f = fresh_args();
       const int j = 4 * half + wave;
-      const int64_t t = ts + j;
+      const int t = sub * kEight + j;
+      const int64_t at = row_out + (int64_t)t * f.d;
 #pragma unroll
       for (int k = 0; k < NC; ++k) {
         float gb = 0.f, aq = 0.f, ch = 0.f;
@@ -394,14 +423,14 @@ __global__ void __launch_bounds__(256, NC == 1 ? 4 : 2) scan_grad(ScanArgs a) {
           aq += sums[1][wave][m][NC * lane + k];
           ch += sums[2][wave][m][NC * lane + k];
         }
-        if (!on[k] || t >= t1) continue;
-        const int64_t at = (b * f.l + t) * f.d + g0, all = f.b * f.l * f.d;
+        if (!on[k] || t >= tokens) continue;
         if constexpr (MULTI) {
+          const int64_t all = f.b * f.l * f.d;
           float* out = f.sums + blk * 3 * all + at;
           out[in[k]] = gb;
           (out + all)[in[k]] = aq;
           (out + 2 * all)[in[k]] = ch;
-        } else if (t < end) {
+        } else if (t < live) {
           const int i = NC * lane + k;
           const Token v = {of[U][j][i], of[DT][j][i], of[SLOPE][j][i], of[GO][j][i], of[DZ][j][i]};
           finish<T, GATE>(f, at, in[k], gb, aq, ch, v, f.skip ? (f.skip + g0)[in[k]] : 0.f,
