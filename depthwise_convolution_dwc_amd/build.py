@@ -71,6 +71,7 @@ def _units():
     u.append(("hip", "seq/seq_columns.hip", "seq_columns.o", []))
     u.append(("hip", "seq/seq_conv.hip", "seq_conv.o", []))
     u.append(("hip", "seq/seq_scan_fwd.hip", "seq_scan_fwd.o", []))
+    u.append(("hip", "seq/seq_scan_wide.hip", "seq_scan_wide.o", []))
     u.append(("hip", "seq/seq_scan_token.hip", "seq_scan_token.o", []))
     u.append(("hip", "seq/seq_scan_grad.hip", "seq_scan_grad.o", []))
     u.append(("hip", "seq/seq_resnorm.hip", "seq_resnorm.o", []))

@@ -63,6 +63,12 @@ __device__ __forceinline__ float softplus(float x) {
   return fmaxf(x, 0.f) + (d == 0.f ? e : l);
 }
 
+// (A select: a branch would split the code of several tokens.)
+__device__ __forceinline__ float step_of(int soft, float x) {
+  const float s = softplus(x);
+  return soft ? s : x;
+}
+
 __device__ __forceinline__ int64_t length_of(const ScanArgs& a, int64_t b) {
   if (!a.lengths) return a.l;
   const int64_t n = a.lengths[b];

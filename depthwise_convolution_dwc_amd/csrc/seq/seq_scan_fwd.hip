@@ -14,9 +14,11 @@
 
 namespace dwc {
 namespace seq {
+void launch_scan_wide(const ScanArgs& a, hipStream_t st);
+
 namespace scan {
 
-template <int T, bool BWD>
+template <int T, bool FOURS>
 __global__ void __launch_bounds__(256) scan_prep(ScanArgs a) {
   const int w = 2 * a.spl;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -25,8 +27,8 @@ __global__ void __launch_bounds__(256) scan_prep(ScanArgs a) {
   if (b >= a.b) return;
   const int j = (int)(i - line * w), blk = (int)(row - gr * a.nblk), g = (int)(gr - b * a.g);
   // states in order, or by fours with B and C in turn
-  const bool second = BWD ? j & 4 : j >= a.spl;
-  const int s = blk * a.spl + (BWD ? j / 8 * 4 + j % 4 : (second ? j - a.spl : j));
+  const bool second = FOURS ? j & 4 : j >= a.spl;
+  const int s = blk * a.spl + (FOURS ? j / 8 * 4 + j % 4 : (second ? j - a.spl : j));
   float v = 0.f;
   if (s < a.n && t < length_of(a, b))
     v = second ? load1<T>(a.cm, b * a.c_stride[0] + t * a.c_stride[1] + g * a.c_stride[2] + s)
@@ -115,12 +117,6 @@ __device__ __forceinline__ const char* from(const void* p, const int64_t (&strid
   return (const char*)((const Raw<T>*)p + (w.b * stride[0] + w.t0 * stride[1] + w.g0));
 }
 
-template <int T>
-__device__ __forceinline__ float step_of(const ScanArgs& a, Raw<T> delta, float bias) {
-  const float x = value<T>(delta) + bias, s = softplus(x);
-  return a.softplus ? s : x;  // (a select: a branch would split the tokens' code)
-}
-
 // Each chunk's state from zero and the sum of its steps.  With BWD also, from
 // zero at its end, the gradient that it hands to the state before it:
 //   sum_t (a_t0 ... a_t) C_t do_t,  do = dy silu(z).
@@ -153,7 +149,7 @@ __global__ void __launch_bounds__(64) scan_chunk(ScanArgs a) {
       // (forward only B is read)
       const auto lo = load_scalar<SPL>(bc), hi = load_scalar<SPL>(bc + (BWD ? SPL : 0));
       const auto at = [&](int k) { return k < SPL ? lo[k < SPL ? k : 0] : hi[k < SPL ? 0 : k - SPL]; };
-      const float dt = step_of<T>(a, x.v[1][i], bias), du = dt * value<T>(x.v[0][i]);
+      const float dt = step_of(a.softplus, value<T>(x.v[1][i]) + bias), du = dt * value<T>(x.v[0][i]);
       sum += dt;
       float k[SPL];
 #pragma unroll
@@ -200,37 +196,64 @@ __global__ void __launch_bounds__(64) scan_chunk(ScanArgs a) {
 }
 
 // From each chunk's own part to the state that it starts from; blockIdx.y = 1:
-// to the gradient that reaches its last state.
-__global__ void __launch_bounds__(256) scan_combine(ScanArgs a) {
-  const int np = a.nblk * a.spl;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= a.b * np * a.d) return;
-  const int64_t row = i / a.d, b = row / np;
-  const int c = (int)(i - row * a.d), s = (int)(row - b * np);
+// to the gradient that reaches its last state.  RUNS waves take as many runs
+// of up to kRun chunks of the same 64 channels: each sums its run from zero,
+// all find their first value from the runs before, and each goes over its run
+// again, which is still in its registers.
+constexpr int kRun = 16;
+template <int RUNS>
+__global__ void __launch_bounds__(64 * RUNS) scan_combine(ScanArgs a) {
+  __shared__ float part[2][RUNS][2][64];
+  const int np = a.nblk * a.spl, blocks = (a.d + 63) / 64;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t row = blockIdx.x / (uint32_t)blocks;  // of b np
+  const int c0 = (int)(blockIdx.x - row * (uint32_t)blocks) * 64 + lane;
+  const int c = c0 < a.d ? c0 : a.d - 1;  // (lanes past the end repeat the last channel)
+  const int64_t b = row / (uint32_t)np;
+  const int s = (int)(row - (uint32_t)b * np);
   const bool back = blockIdx.y == 1, in = s < a.n;
-  const int64_t own = (b * a.d + c) * a.n + s, step = (int64_t)np * a.d;
+  const int64_t own = (b * a.d + c) * a.n + (in ? s : 0), step = (int64_t)np * a.d;
   const float a2 = in ? kLog2e * a.a[(int64_t)c * a.n + s] : 0.f;
   const float* from = back ? a.ds1 : a.s0;
   float carry = from && in ? from[own] : 0.f;
   float* x = (back ? a.rstates : a.states) + (b * a.nc * np + s) * a.d + c;
   const float* dts = a.dts + b * a.nc * a.d + c;
-  constexpr int U = 8;
-  for (int k = 0; k < a.nc; k += U) {
-    float v[U], p[U];
+  const int run = a.nc >= kRun * RUNS ? kRun : (a.nc + RUNS - 1) / RUNS;
+  int side = 0;
+  for (int k0 = 0; k0 < a.nc; k0 += run * RUNS, side ^= 1) {
+    const int first = k0 + wave * run;
+    float v[kRun], p[kRun];
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int q = back ? a.nc - 1 - k - j : k + j;
-      if (k + j < a.nc) {
+    for (int j = 0; j < kRun; ++j) {
+      const int k = first + j, q = back ? a.nc - 1 - k : k;
+      v[j] = p[j] = 0.f;  // (a chunk that is not there changes nothing)
+      if (j < run && k < a.nc) {
         v[j] = x[q * step];
         p[j] = dts[(int64_t)q * a.d];
       }
     }
+    float sum = 0.f, keep = 1.f;
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int q = back ? a.nc - 1 - k - j : k + j;
-      if (k + j < a.nc) {
-        x[q * step] = carry;
-        carry = fmaf(exp2_of(a2 * p[j]), carry, v[j]);
+    for (int j = 0; j < kRun; ++j) {
+      p[j] = exp2_of(a2 * p[j]);
+      sum = fmaf(p[j], sum, v[j]);
+      keep *= p[j];
+    }
+    part[side][wave][0][lane] = sum;
+    part[side][wave][1][lane] = keep;
+    __syncthreads();  // (two sides: one barrier keeps readers and writers apart)
+    float mine = carry;
+#pragma unroll
+    for (int i = 0; i < RUNS; ++i) {
+      if (i == wave) mine = carry;
+      carry = fmaf(part[side][i][1][lane], carry, part[side][i][0][lane]);
+    }
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+      const int k = first + j, q = back ? a.nc - 1 - k : k;
+      if (j < run && k < a.nc) {
+        if (c0 < a.d) x[q * step] = mine;
+        mine = fmaf(p[j], mine, v[j]);
       }
     }
   }
@@ -280,7 +303,7 @@ __global__ void __launch_bounds__(MULTI ? 1024 : 64) scan_out(ScanArgs a) {
     const auto token = [&](const auto& x, int i) {
       const auto bb = load_scalar<SPL>(bc);
       const auto cc = load_scalar<SPL>(bc + SPL);
-      const float dt = step_of<T>(a, x.v[1][i], bias), du = dt * value<T>(x.v[0][i]);
+      const float dt = step_of(a.softplus, value<T>(x.v[1][i]) + bias), du = dt * value<T>(x.v[0][i]);
       float y = 0.f;
 #pragma unroll
       for (int s = 0; s < SPL; ++s) {
@@ -355,18 +378,25 @@ __global__ void __launch_bounds__(MULTI ? 1024 : 64) scan_out(ScanArgs a) {
   }
 }
 
+template <int T, bool FOURS>
+void lay_out(const ScanArgs& a, hipStream_t st) {
+  const int64_t vals = a.b * a.lp * a.g * a.nblk * 2 * a.spl;
+  if (vals > 0)
+    hipLaunchKernelGGL((scan_prep<T, FOURS>), dim3((uint32_t)((vals + 255) / 256)), dim3(256), 0,
+                       st, a);
+}
+
 template <int T, int SPL, bool BWD, bool GATE>
 void prepare(const ScanArgs& a, hipStream_t st) {
-  if (a.l > 0) {
-    const int64_t vals = a.b * a.lp * a.g * a.nblk * 2 * a.spl;
-    hipLaunchKernelGGL((scan_prep<T, BWD>), dim3((uint32_t)((vals + 255) / 256)), dim3(256), 0, st, a);
-  }
+  lay_out<T, BWD>(a, st);
   if (a.nc > 1) {
     const dim3 grid((uint32_t)(a.b * a.nc * a.g * a.cblk * a.nblk));
     hipLaunchKernelGGL((scan_chunk<T, SPL, BWD, GATE>), grid, dim3(64), 0, st, a);
-    const int64_t vals = a.b * a.nblk * a.spl * a.d;
-    hipLaunchKernelGGL(scan_combine, dim3((uint32_t)((vals + 255) / 256), BWD ? 2 : 1), dim3(256),
-                       0, st, a);
+    const int64_t rows = a.b * a.nblk * a.spl * ((a.d + 63) / 64);
+    const dim3 blocks((uint32_t)rows, BWD ? 2 : 1);
+    // one wave over all chunks where that fills the device
+    if (rows >= 4096) hipLaunchKernelGGL(scan_combine<1>, blocks, dim3(64), 0, st, a);
+    else hipLaunchKernelGGL(scan_combine<8>, blocks, dim3(512), 0, st, a);
   }
 }
 
@@ -390,7 +420,10 @@ void go_gate(const ScanArgs& a, hipStream_t st) {
 
 template <int T>
 void go_states(const ScanArgs& a, hipStream_t st) {
-  if (a.spl == 4) go_gate<T, 4>(a, st);
+  if (a.waves > 0) {
+    lay_out<T, true>(a, st);
+    launch_scan_wide(a, st);
+  } else if (a.spl == 4) go_gate<T, 4>(a, st);
   else if (a.spl == 8) go_gate<T, 8>(a, st);
   else go_gate<T, 16>(a, st);
 }
@@ -403,18 +436,32 @@ void prepare_bwd(const ScanArgs& a, hipStream_t st) {
 
 }  // namespace scan
 
+// Whether one pass over the tokens, a block's 64 channels shared by waves with
+// four states each, is done before the chunks' three.  One pass takes about
+// kOne for a token while each SIMD has one such wave, the chunks kTwo for a
+// token of each of the waves and kFixed besides.
+static int one_pass(const ScanArgs& a) {
+  if (a.n <= 8 || a.n > 64) return 0;
+  const int waves = a.n <= 16 ? 4 : (a.n <= 32 ? 8 : 16);
+  const double each = (double)(a.b * a.g * a.cblk * waves) / 1024;
+  constexpr double kOne = 0.075, kTwo = 0.15, kFixed = 20.0;  // us
+  const double one = kOne * (double)a.l * (each > 1.0 ? each : 1.0);
+  return one < kFixed + kTwo * (double)a.l * each ? waves : 0;
+}
+
 void scan_split(ScanArgs* a, bool bwd) {
   a->dg = a->d / a->g;
-  // (the gradients' workgroups hold 16 states, four a wave)
-  a->spl = bwd ? 16 : (a->n <= 4 ? 4 : (a->n <= 8 ? 8 : 16));
-  a->nblk = (a->n + a->spl - 1) / a->spl;
   a->cblk = (a->dg + 63) / 64;
+  a->waves = bwd ? 0 : one_pass(*a);
+  // (the gradients' and the one pass' waves take fours of blocks of 16)
+  a->spl = bwd || a->waves > 0 ? 16 : (a->n <= 4 ? 4 : (a->n <= 8 ? 8 : 16));
+  a->nblk = (a->n + a->spl - 1) / a->spl;
   a->lp = (a->l + kGradChunk - 1) / kGradChunk * kGradChunk;
   if (bwd) {
     a->tc = kGradChunk;
   } else {
     const int64_t waves = a->b * a->g * a->cblk * a->nblk;
-    int64_t nc = waves >= 2048 || a->b == 0 ? 1 : 4096 / waves;
+    int64_t nc = waves >= 2048 || a->b == 0 || a->waves > 0 ? 1 : 4096 / waves;
     const int64_t most = (a->l + 31) / 32;
     if (nc > most) nc = most;
     if (nc < 1) nc = 1;

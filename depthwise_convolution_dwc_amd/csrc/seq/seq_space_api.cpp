@@ -177,7 +177,7 @@ int scan_layout(ScanArgs* a, bool bwd, char* base, size_t* bytes) {
   const int64_t pairs = (a->dg + kGradChannels - 1) / kGradChannels;
   // threads of the widest launches, and the index range
   if (tokens > kMost / (a->g * line) || tokens * a->g * line >= kLanes ||
-      rows >= kLanes / 64 / ((int64_t)a->g * a->cblk * a->nblk) || a->b * np * a->d >= kLanes / 2 ||
+      rows >= kLanes / 64 / ((int64_t)a->g * a->cblk * a->nblk) || a->b * np * ((a->d + 63) / 64) >= kLanes / 1024 ||
       (bwd && (rows >= kLanes / 256 / ((int64_t)a->g * pairs * a->nblk) ||
                (int64_t)a->n * a->d * 64 >= kLanes / 2 || rows >= kLanes / a->d)))
     return fail(DWC_ERR_UNSUPPORTED, "scan sizes past the launch range");
