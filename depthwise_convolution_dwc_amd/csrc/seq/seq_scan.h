@@ -29,10 +29,20 @@ __device__ __forceinline__ typename VecOf<N>::type load_scalar(const float* p) {
   return *(cvec*)(uintptr_t)p;
 }
 
-template <int T> struct RawOf { typedef uint16_t type; };
-template <> struct RawOf<T_F32> { typedef float type; };
+// An element as it stands in memory (Elem) and in a register (Raw: a whole one,
+// or the compiler packs elements in pairs, which waits for their loads).
+template <int T> struct RawOf {
+  typedef uint16_t elem;
+  typedef uint32_t reg;
+};
+template <> struct RawOf<T_F32> {
+  typedef float elem;
+  typedef float reg;
+};
 template <int T>
-using Raw = typename RawOf<T>::type;
+using Elem = typename RawOf<T>::elem;
+template <int T>
+using Raw = typename RawOf<T>::reg;
 
 template <int T>
 __device__ __forceinline__ float value(Raw<T> v) {

@@ -103,7 +103,7 @@ struct Ahead {
     for (int i = 0; i < U; ++i)
 #pragma unroll
       for (int k = 0; k < N; ++k) {
-        v[k][i] = ((const Raw<T>*)p[k])[in];
+        v[k][i] = ((const Elem<T>*)p[k])[in];
         p[k] += step[k];
       }
   }
@@ -113,8 +113,8 @@ struct Ahead {
 template <int T>
 __device__ __forceinline__ const char* from(const void* p, const int64_t (&stride)[2],
                                             const Where& w, int64_t& step) {
-  step = stride[1] * (int64_t)sizeof(Raw<T>);
-  return (const char*)((const Raw<T>*)p + (w.b * stride[0] + w.t0 * stride[1] + w.g0));
+  step = stride[1] * (int64_t)sizeof(Elem<T>);
+  return (const char*)((const Elem<T>*)p + (w.b * stride[0] + w.t0 * stride[1] + w.g0));
 }
 
 // Each chunk's state from zero and the sum of its steps.  With BWD also, from
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(MULTI ? 1024 : 64) scan_out(ScanArgs a) {
 #pragma unroll
     for (int s = 0; s < SPL; ++s) h[s] = 0.f;
   }
-  Raw<T>* out = (Raw<T>*)a.y + ((w.b * a.l + w.t0) * a.d + w.g0);  // of token t
+  Elem<T>* out = (Elem<T>*)a.y + ((w.b * a.l + w.t0) * a.d + w.g0);  // of token t
   int64_t t = w.t0;
   if (t < end) {
     const float bias = a.bias ? a.bias[w.c] : 0.f, skip = a.skip ? a.skip[w.c] : 0.f;
@@ -420,7 +420,7 @@ void go_gate(const ScanArgs& a, hipStream_t st) {
 
 template <int T>
 void go_states(const ScanArgs& a, hipStream_t st) {
-  if (a.waves > 0) {
+  if (a.one) {
     lay_out<T, true>(a, st);
     launch_scan_wide(a, st);
   } else if (a.spl == 4) go_gate<T, 4>(a, st);
@@ -436,32 +436,38 @@ void prepare_bwd(const ScanArgs& a, hipStream_t st) {
 
 }  // namespace scan
 
-// Whether one pass over the tokens, a block's 64 channels shared by waves with
-// four states each, is done before the chunks' three.  One pass takes about
-// kOne for a token while each SIMD has one such wave, the chunks kTwo for a
-// token of each of the waves and kFixed besides.
-static int one_pass(const ScanArgs& a) {
-  if (a.n <= 8 || a.n > 64) return 0;
-  const int waves = a.n <= 16 ? 4 : (a.n <= 32 ? 8 : 16);
-  const double each = (double)(a.b * a.g * a.cblk * waves) / 1024;
-  constexpr double kOne = 0.075, kTwo = 0.15, kFixed = 20.0;  // us
-  const double one = kOne * (double)a.l * (each > 1.0 ? each : 1.0);
-  return one < kFixed + kTwo * (double)a.l * each ? waves : 0;
+// Whether one pass over all tokens is done before the chunks' three.  It takes
+// kOne a token while its workgroups (64 channels each) have SIMDs to themselves, then kMore a token and workgroup;
+// the chunks' three passes take kTwo a token and workgroup and kFixed besides,
+// for their launches and the states between them.  bf16, us: 256 tokens of
+// 2048 channels, 16 states: 34 and 51 in chunks; 1024 tokens: 110 and 56; 16
+// sequences of 2048 tokens: 326 and 501; 32 states, 4 sequences of 700 tokens
+// of 512 channels: 102 and 72, 16 such: 108 and 160.
+static bool one_pass(const ScanArgs& a) {
+  if (a.n > 64) return false;
+  const int blocks = (a.n + 15) / 16;
+  const double groups = (double)(a.b * a.g * a.cblk);
+  const double kOne = a.n <= 16 ? 0.103 : (a.n <= 32 ? 0.146 : 0.22);
+  const double kMore = 0.00027 * blocks;
+  const double kTwo = 0.00043 * (blocks == 1 ? 1 : 1 + blocks), kFixed = 40.0;
+  const double token = kMore * groups > kOne ? kMore * groups : kOne;
+  return token * (double)a.l < kFixed + kTwo * groups * (double)a.l;
 }
 
 void scan_split(ScanArgs* a, bool bwd) {
   a->dg = a->d / a->g;
   a->cblk = (a->dg + 63) / 64;
-  a->waves = bwd ? 0 : one_pass(*a);
+  a->one = !bwd && one_pass(*a);
   // (the gradients' and the one pass' waves take fours of blocks of 16)
-  a->spl = bwd || a->waves > 0 ? 16 : (a->n <= 4 ? 4 : (a->n <= 8 ? 8 : 16));
+  a->spl = bwd || a->one ? 16 : (a->n <= 4 ? 4 : (a->n <= 8 ? 8 : 16));
   a->nblk = (a->n + a->spl - 1) / a->spl;
   a->lp = (a->l + kGradChunk - 1) / kGradChunk * kGradChunk;
   if (bwd) {
     a->tc = kGradChunk;
   } else {
     const int64_t waves = a->b * a->g * a->cblk * a->nblk;
-    int64_t nc = waves >= 2048 || a->b == 0 || a->waves > 0 ? 1 : 4096 / waves;
+    // chunks for 8 waves a SIMD (4 sequences of 2048 tokens: 169 us, 187 us for 4)
+    int64_t nc = waves >= 4096 || a->b == 0 || a->one ? 1 : 8192 / waves;
     const int64_t most = (a->l + 31) / 32;
     if (nc > most) nc = most;
     if (nc < 1) nc = 1;

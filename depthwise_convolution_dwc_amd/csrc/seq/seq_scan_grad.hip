@@ -69,7 +69,7 @@ struct RawToken {
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
-      for (int k = 0; k < NC; ++k) v[i][k] = ((const Raw<T>*)p[i])[in[k]];
+      for (int k = 0; k < NC; ++k) v[i][k] = ((const Elem<T>*)p[i])[in[k]];
   }
 };
 
@@ -78,8 +78,8 @@ template <int T, int N>
 __device__ __forceinline__ void addresses(const ScanArgs& a, int64_t b, int64_t t, int64_t first,
                                           const char* (&p)[N], int64_t (&step)[N]) {
   const auto set = [&](int i, const void* q, const int64_t (&stride)[2]) {
-    p[i] = (const char*)((const Raw<T>*)q + (b * stride[0] + t * stride[1] + first));
-    step[i] = stride[1] * (int64_t)sizeof(Raw<T>);
+    p[i] = (const char*)((const Elem<T>*)q + (b * stride[0] + t * stride[1] + first));
+    step[i] = stride[1] * (int64_t)sizeof(Elem<T>);
   };
   set(0, a.u, a.u_stride);
   set(1, a.delta, a.delta_stride);
@@ -122,9 +122,9 @@ __device__ __forceinline__ void finish(const Args& a, int64_t at, uint32_t in, f
                                        float aq, float ch, const Token& v, float skip,
                                        float& dskip, float& dbias) {
   const float dd = fmaf(v.u, gb, kLn2 * aq) * v.slope;
-  store1<T>((Raw<T>*)a.du + at, in, fmaf(v.dt, gb, skip * v.go));
-  store1<T>((Raw<T>*)a.ddelta + at, in, dd);
-  if constexpr (GATE) store1<T>((Raw<T>*)a.dz + at, in, v.dz * fmaf(skip, v.u, ch));
+  store1<T>((Elem<T>*)a.du + at, in, fmaf(v.dt, gb, skip * v.go));
+  store1<T>((Elem<T>*)a.ddelta + at, in, dd);
+  if constexpr (GATE) store1<T>((Elem<T>*)a.dz + at, in, v.dz * fmaf(skip, v.u, ch));
   dskip = fmaf(v.go, v.u, dskip);
   dbias += dd;
 }
@@ -132,9 +132,9 @@ __device__ __forceinline__ void finish(const Args& a, int64_t at, uint32_t in, f
 // Zeros behind a sequence's last token.
 template <int T, bool GATE, class Args>
 __device__ __forceinline__ void finish_none(const Args& a, int64_t at, uint32_t in) {
-  store1<T>((Raw<T>*)a.du + at, in, 0.f);
-  store1<T>((Raw<T>*)a.ddelta + at, in, 0.f);
-  if constexpr (GATE) store1<T>((Raw<T>*)a.dz + at, in, 0.f);
+  store1<T>((Elem<T>*)a.du + at, in, 0.f);
+  store1<T>((Elem<T>*)a.ddelta + at, in, 0.f);
+  if constexpr (GATE) store1<T>((Elem<T>*)a.dz + at, in, 0.f);
 }
 
 // The kernel's arguments, read again from their segment: held in registers

@@ -1,8 +1,8 @@
 // seq_scan_wide.hip -- the selective scan in one pass over the tokens, for
 // many sequences or channels and for short sequences.
 //
-// A workgroup takes 64 channels of a sequence, wave w states 4 w to 4 w + 3
-// with a channel a lane.  Stages of 16 tokens: the waves share out the tokens'
+// A workgroup takes 64 channels of a sequence, a wave two or four of the
+// states with a channel a lane.  Stages of 16 tokens: the waves share out the tokens'
 // steps, inputs and gates (tokens w, w + NW, ...), all run the stage on their
 // own states, and join the parts of C . h in LDS, where each finishes its own
 // tokens.  B and C go through LDS too, a stage ahead: there are few waves to
@@ -16,12 +16,13 @@ namespace scan {
 
 constexpr int kStage = 16;
 
-template <int T, int NW, bool GATE>
+template <int T, int NW, int S, bool GATE>
 __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
   constexpr int NT = kStage / NW, SPL = 16;  // tokens a wave shares; states a line of bc
+  constexpr int ROW = 2 * S * NW;            // B and C of all states
   __shared__ float of[2][kStage][64];        // dt, u
   __shared__ float parts[kStage][NW][64];    // of C . h
-  __shared__ __align__(16) float rows[2][kStage][8 * NW];  // B and C, four and four of a wave in turn
+  __shared__ __align__(16) float rows[2][kStage][ROW];  // four states' B and their C in turn
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   uint32_t i = blockIdx.x;
   const int block = (int)(i % (uint32_t)a.cblk);
@@ -33,48 +34,50 @@ __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
   const uint32_t c0 = (uint32_t)(block * 64 + lane);
   const bool on = (int)c0 < a.dg;
   const uint32_t in = on ? c0 : 0;  // (lanes past the end repeat the first channel)
-  const int n0 = 4 * wave;
-  float a2[4], h[4];
-  const auto states = [&](const float* p, float(&v)[4]) {  // of d x n
+  const int n0 = S * wave;
+  float a2[S], h[S];
+  const auto states = [&](const float* p, float(&v)[S]) {  // of d x n
 #pragma unroll
-    for (int s = 0; s < 4; ++s) v[s] = (p + (n0 + s < a.n ? n0 + s : 0))[in * (uint32_t)a.n];
+    for (int s = 0; s < S; ++s) v[s] = (p + (n0 + s < a.n ? n0 + s : 0))[in * (uint32_t)a.n];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) v[s] = n0 + s < a.n ? v[s] : 0.f;
+    for (int s = 0; s < S; ++s) v[s] = n0 + s < a.n ? v[s] : 0.f;
   };
   states(a.a + g0 * a.n, a2);
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
+  for (int s = 0; s < S; ++s) {
     a2[s] *= kLog2e;
     h[s] = 0.f;
   }
   if (a.s0) states(a.s0 + (b * a.d + g0) * a.n, h);
   const float bias = a.bias ? (a.bias + g0)[in] : 0.f, skip = a.skip ? (a.skip + g0)[in] : 0.f;
-  // B and C of a stage: two values a thread; rows up to a multiple of the stage
-  // are there, but for blocks of 16 states past the last
-  const int row = threadIdx.x / (4 * NW), at_row = 2 * (threadIdx.x % (4 * NW)), of16 = at_row / 32;
+  // B and C of a stage: S / 2 values a thread; rows up to a multiple of the
+  // stage are there, but for blocks of 16 states past the last
+  constexpr int PER = S / 2, ACROSS = ROW / PER;
+  const int row = threadIdx.x / ACROSS, at_row = PER * (threadIdx.x % ACROSS), of16 = at_row / 32;
   const bool some = of16 < a.nblk;
   const float* bc = a.bc + (((b * a.g + g) * a.nblk + (some ? of16 : 0)) * a.lp + row) * (2 * SPL) +
                     at_row % 32;
-  f32x2 bc_next;
+  float bc_next[PER];
   // the wave's tokens of the next stage: next[] is the address of the first
   constexpr int N = GATE ? 3 : 2;
   const char* next[N];
   int64_t step[N];  // NW tokens
   const auto set = [&](int k, const void* p, const int64_t(&stride)[2]) {
-    next[k] = (const char*)((const Raw<T>*)p + (b * stride[0] + wave * stride[1] + g0));
-    step[k] = NW * stride[1] * (int64_t)sizeof(Raw<T>);
+    next[k] = (const char*)((const Elem<T>*)p + (b * stride[0] + wave * stride[1] + g0));
+    step[k] = NW * stride[1] * (int64_t)sizeof(Elem<T>);
   };
   set(0, a.u, a.u_stride);
   set(1, a.delta, a.delta_stride);
   if constexpr (GATE) set(2, a.z, a.z_stride);
-  Raw<T> raw[N][NT];
-  const auto fetch = [&](int t0) {
+  Raw<T> even[N][NT], odd[N][NT];  // of the next two stages
+  const auto fetch = [&](int t0, Raw<T>(&raw)[N][NT]) {
+    if (t0 >= len) return;
     if (t0 + kStage <= len) {
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-          raw[k][j] = ((const Raw<T>*)next[k])[in];
+          raw[k][j] = ((const Elem<T>*)next[k])[in];
           next[k] += step[k];
         }
     } else {  // a token past the last one is read as the last
@@ -83,21 +86,26 @@ __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
         const int t = t0 + j * NW + wave, back = t < len ? 0 : t - (len - 1);
 #pragma unroll
         for (int k = 0; k < N; ++k)
-          raw[k][j] = ((const Raw<T>*)(next[k] + j * step[k] - back * (step[k] / NW)))[in];
+          raw[k][j] = ((const Elem<T>*)(next[k] + j * step[k] - back * (step[k] / NW)))[in];
       }
     }
-    bc_next = *(const f32x2*)(bc + (int64_t)t0 * (2 * SPL));
+  };
+  const auto fetch_rows = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) bc_next[i] = bc[(int64_t)t0 * (2 * SPL) + i];
   };
   const auto keep = [&](int side) {
-    *(f32x2*)&rows[side][row][at_row] = some ? bc_next : f32x2{0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < PER; ++i) rows[side][row][at_row + i] = some ? bc_next[i] : 0.f;
   };
-  Raw<T>* const out = (Raw<T>*)a.y + (b * a.l * a.d + g0);
+  Elem<T>* const out = (Elem<T>*)a.y + (b * a.l * a.d + g0);
   if (len > 0) {
-    fetch(0);
+    fetch_rows(0);
+    fetch(0, even);
+    fetch(kStage, odd);
     keep(0);
   }
-  int side = 0;
-  for (int t0 = 0; t0 < len; t0 += kStage, side ^= 1) {
+  const auto stage = [&](int t0, int side, Raw<T>(&raw)[N][NT]) {
     // (the stage before has been read: its readers passed the barrier below)
     Raw<T> gate[NT];
     float u[NT];
@@ -112,21 +120,26 @@ __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
       of[1][at][lane] = live ? u[j] : 0.f;
     }
     __syncthreads();
-    if (t0 + kStage < len) fetch(t0 + kStage);
+    // (the rows first: they are waited for first, a stage before the rest)
+    if (t0 + kStage < len) fetch_rows(t0 + kStage);
+    fetch(t0 + 2 * kStage, raw);
     // LDS is read two tokens ahead and the decays are made one ahead: a SIMD
     // may have no other wave to fill the wait
-    f32x4 bb[3], cc[3];
-    float dt[3], du[3], k[2][4];
+    float bb[3][S], cc[3][S], dt[3], du[3], k[2][S];
+    const int b_at = 8 * (n0 / 4) + n0 % 4, c_at = b_at + 4;
     const auto read = [&](int j) {
-      bb[j % 3] = *(const f32x4*)&rows[side][j][8 * wave];
-      cc[j % 3] = *(const f32x4*)&rows[side][j][8 * wave + 4];
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        bb[j % 3][s] = rows[side][j][b_at + s];
+        cc[j % 3][s] = rows[side][j][c_at + s];
+      }
       dt[j % 3] = of[0][j][lane];
       du[j % 3] = of[1][j][lane];
     };
     const auto decays = [&](int j) {
       du[j % 3] *= dt[j % 3];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) k[j % 2][s] = exp2_of(dt[j % 3] * a2[s]);
+      for (int s = 0; s < S; ++s) k[j % 2][s] = exp2_of(dt[j % 3] * a2[s]);
     };
     read(0);
     read(1);
@@ -138,7 +151,7 @@ __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
       if (j + 1 < kStage) decays(j + 1);
       float y = 0.f;
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
+      for (int s = 0; s < S; ++s) {
         h[s] = fmaf(k[j % 2][s], h[s], du[j % 3] * bb[j % 3][s]);
         y = fmaf(cc[j % 3][s], h[s], y);
       }
@@ -159,21 +172,36 @@ __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
       }
       if (on && t0 + at < len) store1<T>(out + (int64_t)(t0 + at) * a.d, in, y);
     }
+  };
+  for (int t0 = 0; t0 < len; t0 += 2 * kStage) {
+    stage(t0, 0, even);
+    if (t0 + kStage < len) stage(t0 + kStage, 1, odd);
   }
   for (int64_t t = len + wave; t < a.l; t += NW)
     if (on) store1<T>(out + t * a.d, in, 0.f);
   float* const s1 = a.s1 + (b * a.d + g0) * a.n;
 #pragma unroll
-  for (int s = 0; s < 4; ++s)
+  for (int s = 0; s < S; ++s)
     if (on && n0 + s < a.n) (s1 + n0 + s)[in * (uint32_t)a.n] = h[s];
+}
+
+template <int T, int NW, int S, bool GATE>
+void go_shape(const ScanArgs& a, hipStream_t st) {
+  hipLaunchKernelGGL((scan_wide<T, NW, S, GATE>), dim3((uint32_t)(a.b * a.g * a.cblk)),
+                     dim3(64 * NW), 0, st, a);
 }
 
 template <int T, bool GATE>
 void go_wide(const ScanArgs& a, hipStream_t st) {
-  const dim3 grid((uint32_t)(a.b * a.g * a.cblk));
-  if (a.waves == 4) hipLaunchKernelGGL((scan_wide<T, 4, GATE>), grid, dim3(256), 0, st, a);
-  else if (a.waves == 8) hipLaunchKernelGGL((scan_wide<T, 8, GATE>), grid, dim3(512), 0, st, a);
-  else hipLaunchKernelGGL((scan_wide<T, 16, GATE>), grid, dim3(1024), 0, st, a);
+  if (a.n <= 8) return go_shape<T, 4, 2, GATE>(a, st);
+  // two states a wave while that leaves no SIMD more than two waves (8 and 16
+  // sequences of 2048 tokens of 2048 channels: 220 and 361 us, with four 249
+  // and 326)
+  if (a.n <= 16)
+    return a.b * a.g * a.cblk <= 256 ? go_shape<T, 8, 2, GATE>(a, st)
+                                     : go_shape<T, 4, 4, GATE>(a, st);
+  if (a.n <= 32) return go_shape<T, 8, 4, GATE>(a, st);
+  go_shape<T, 16, 4, GATE>(a, st);
 }
 
 template <int T>

@@ -60,7 +60,7 @@ struct ScanArgs {
   // how the work is split: dg channels a group; spl states a lane in blocks of
   // that many, cblk blocks of 64 channels a group, nc chunks of tc tokens
   int dg, spl, nblk, cblk, tc, nc;
-  int waves;  // of a workgroup that takes all tokens in one pass; 0: chunks
+  int one;  // one pass over all tokens, no chunks
   // workspace
   int64_t lp;      // l up to whole chunks of the gradients
   float* bc;       // [b][g][nblk][lp][2 spl]: B and C in fp32, zeros past n and past a length
