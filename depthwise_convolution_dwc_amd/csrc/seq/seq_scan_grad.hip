@@ -27,36 +27,41 @@ namespace scan {
 constexpr int kEight = 8, kSubs = kGradChunk / kEight;
 constexpr int NC = kGradChannels / 64, kPair = kGradChannels;  // channels a lane, a workgroup
 
-// a = sums of the halves of a (lanes 0 to 31) and of b (32 to 63), the same
-// by rows of 16, by halves of a row and by its fours.
-__device__ __forceinline__ void swap32(float& a, float& b, float& c, float& d, float& e, float& f,
-                                       float& g, float& h) {
-  asm("s_nop 1\n\tv_permlane32_swap_b32 %0, %1\n\tv_permlane32_swap_b32 %2, %3\n\t"
-      "v_permlane32_swap_b32 %4, %5\n\tv_permlane32_swap_b32 %6, %7"
-      : "+v"(a), "+v"(b), "+v"(c), "+v"(d), "+v"(e), "+v"(f), "+v"(g), "+v"(h));
+// Sums of eight values over the lanes that agree in lane % 4 and lane / 32:
+// first over lanes 8 apart in a row of 16, where the upper half takes the odd
+// value of each pair (an addition that writes two of a row's four banks), then
+// over lanes mirrored in a half row, where every other bank takes the next
+// pair's, then over rows 16 apart.  A lane has value
+//   (lane >> 3 & 1) + 2 (lane >> 2 & 1) + 4 (lane >> 4 & 1).
+// The first wait is for the values, written just before.
+__device__ __forceinline__ float fold8(const float (&v)[8]) {
+  float a, b, c, d;
+  asm("s_nop 1\n\t"
+      "v_add_f32_dpp %0, %4, %4 row_ror:8 row_mask:0xf bank_mask:0xf\n\t"
+      "v_add_f32_dpp %0, %5, %5 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %1, %6, %6 row_ror:8 row_mask:0xf bank_mask:0xf\n\t"
+      "v_add_f32_dpp %1, %7, %7 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %2, %8, %8 row_ror:8 row_mask:0xf bank_mask:0xf\n\t"
+      "v_add_f32_dpp %2, %9, %9 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %3, %10, %10 row_ror:8 row_mask:0xf bank_mask:0xf\n\t"
+      "v_add_f32_dpp %3, %11, %11 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %0, %0, %0 row_half_mirror row_mask:0xf bank_mask:0xf\n\t"
+      "v_add_f32_dpp %2, %2, %2 row_half_mirror row_mask:0xf bank_mask:0xf\n\t"
+      "v_add_f32_dpp %0, %1, %1 row_half_mirror row_mask:0xf bank_mask:0xa\n\t"
+      "v_add_f32_dpp %2, %3, %3 row_half_mirror row_mask:0xf bank_mask:0xa\n\t"
+      "s_nop 1\n\t"
+      "v_permlane16_swap_b32 %0, %2"
+      : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d)
+      : "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "v"(v[4]), "v"(v[5]), "v"(v[6]), "v"(v[7]));
+  return a + c;
 }
-__device__ __forceinline__ void swap16(float& a, float& b, float& c, float& d) {
-  asm("s_nop 1\n\tv_permlane16_swap_b32 %0, %1\n\tv_permlane16_swap_b32 %2, %3"
-      : "+v"(a), "+v"(b), "+v"(c), "+v"(d));
-}
-
-// Sums over the lanes that agree in lane % 8 of eight values; lane has value
-// (lane >> 5) + 2 (lane >> 4 & 1) + 4 (lane >> 3 & 1).
-__device__ __forceinline__ float fold8(float (&v)[8], int lane) {
-  swap32(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
-  float a = v[0] + v[1], b = v[2] + v[3], c = v[4] + v[5], d = v[6] + v[7];
-  swap16(a, b, c, d);
-  const float e = a + b, f = c + d;
-  const float x = e + row_move<0x128>(e), y = f + row_move<0x128>(f);  // rotated by 8
-  return lane & 8 ? y : x;
-}
-// Of two such, the sums over the last eight lanes too; lanes with 4 set have
-// the second one's.
-__device__ __forceinline__ float fold2(float a, float b, int lane) {
-  const float x = a + row_move<0x141>(a), y = b + row_move<0x141>(b);  // mirror of 8
-  float v = lane & 4 ? y : x;
-  v += row_move<0xB1>(v);
-  return v + row_move<0x4E>(v);
+// Of two such, the sums over all lanes of a value; lanes from 32 on have the
+// second one's.
+__device__ __forceinline__ float fold2(float a, float b) {
+  asm("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(a), "+v"(b));
+  a += b;
+  a += row_move<0xB1>(a);
+  return a + row_move<0x4E>(a);
 }
 
 // Raw operands of one token of NC channels: u, delta, dy and, with a gate, z.
@@ -302,8 +307,8 @@ __global__ void __launch_bounds__(256, NC == 1 ? 4 : 2) scan_grad(ScanArgs a) {
 
   // where fold2 leaves this lane's value: B of state s, C of it four further,
   // the second token's a line further
-  const uint32_t out_at = (uint32_t)((lane >> 5) + 2 * (lane >> 4 & 1) + (lane & 8 ? 4 : 0) +
-                                     (lane & 4 ? 2 * SPL : 0));
+  const uint32_t out_at = (uint32_t)((lane >> 3 & 1) + 2 * (lane >> 2 & 1) + 4 * (lane >> 4 & 1) +
+                                     (lane & 32 ? 2 * SPL : 0));
 
   // the states before the eights
   const int last = (tokens + kEight - 1) / kEight - 1;  // of the eights; -1 without tokens
@@ -400,12 +405,12 @@ __global__ void __launch_bounds__(256, NC == 1 ? 4 : 2) scan_grad(ScanArgs a) {
           sums[1][q][wave][NC * lane + k] = aq[k];
           sums[2][q][wave][NC * lane + k] = ch[k];
         }
-        const float f = fold8(v, lane);
+        const float f = fold8(v);
         if (q & 1) {
           folded = f;
         } else {
-          // tokens j (lanes without 4) and j + 1
-          const float x = fold2(f, folded, lane);
+          // tokens j (lanes below 32) and j + 1
+          const float x = fold2(f, folded);
           if ((lane & 3) == 0) rows_out[out_at + j * (2 * SPL)] = x;
         }
       }
