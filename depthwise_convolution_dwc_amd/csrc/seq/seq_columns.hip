@@ -9,11 +9,13 @@ struct ColumnJobs {
   uint32_t end[kColumnJobs];  // workgroups up to and with this job's
 };
 
-// 16 columns x 64 slices of the rows a workgroup: each slice's sum in order,
-// then the slices' sums in order, so that the result has the same bits every
-// time.
-static __global__ void __launch_bounds__(1024) column_sums(ColumnJobs a) {
-  __shared__ float lds[64][17];
+// WIDTH columns x 1024 / WIDTH slices of the rows a workgroup: each slice's sum
+// in order, then the slices' sums in order, so that the result has the same
+// bits every time.
+template <int WIDTH>
+__global__ void __launch_bounds__(1024) column_sums(ColumnJobs a) {
+  constexpr int SLICES = 1024 / WIDTH;
+  __shared__ float lds[SLICES][WIDTH + 1];
   int j = 0;
 #pragma unroll
   for (int i = 0; i + 1 < kColumnJobs; ++i)
@@ -26,33 +28,39 @@ static __global__ void __launch_bounds__(1024) column_sums(ColumnJobs a) {
       s = a.job[i];
       first = a.end[i - 1];
     }
-  const int lane = threadIdx.x & 15, slice = threadIdx.x >> 4;
-  const int64_t col = (int64_t)(blockIdx.x - first) * 16 + lane;
+  const int lane = threadIdx.x % WIDTH, slice = threadIdx.x / WIDTH;
+  const int64_t col = (int64_t)(blockIdx.x - first) * WIDTH + lane;
   float v = 0.f;
   if (col < s.cols) {
 #pragma unroll 8
-    for (int64_t r = slice; r < s.rows; r += 64) v += s.part[r * s.stride + col];
+    for (int64_t r = slice; r < s.rows; r += SLICES) v += s.part[r * s.stride + col];
   }
   lds[slice][lane] = v;
   __syncthreads();
   if (slice == 0 && col < s.cols) {
     v = 0.f;
 #pragma unroll
-    for (int i = 0; i < 64; ++i) v += lds[i][lane];
+    for (int i = 0; i < SLICES; ++i) v += lds[i][lane];
     s.out[s.turn > 0 ? col % s.turn * (s.cols / s.turn) + col / s.turn : col] = v;
   }
 }
 
 hipError_t launch_column_sums(const ColumnSum (&jobs)[kColumnJobs], hipStream_t st) {
+  int64_t cols = 0;
+  for (const ColumnSum& s : jobs)
+    if (s.out) cols += s.cols;
+  if (cols == 0) return hipSuccess;
+  // whole lines of the rows where there are columns enough for the device
+  const int width = cols >= 16384 ? 64 : 16;
   ColumnJobs a{};
   uint32_t blocks = 0;
   for (int i = 0; i < kColumnJobs; ++i) {
     a.job[i] = jobs[i];
-    if (jobs[i].out) blocks += (uint32_t)((jobs[i].cols + 15) / 16);
+    if (jobs[i].out) blocks += (uint32_t)((jobs[i].cols + width - 1) / width);
     a.end[i] = blocks;
   }
-  if (blocks == 0) return hipSuccess;
-  hipLaunchKernelGGL(column_sums, dim3(blocks), dim3(1024), 0, st, a);
+  if (width == 64) hipLaunchKernelGGL(column_sums<64>, dim3(blocks), dim3(1024), 0, st, a);
+  else hipLaunchKernelGGL(column_sums<16>, dim3(blocks), dim3(1024), 0, st, a);
   return hipGetLastError();
 }
 

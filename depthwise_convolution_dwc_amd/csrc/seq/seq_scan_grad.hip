@@ -519,27 +519,29 @@ __global__ void __launch_bounds__(256) scan_finish(ScanArgs a) {
   a.dpart[(row * 2 + 1) * a.d + c[0]] = dbias;
 }
 
-// dB and dC from the channel blocks' parts, in order.
+// dB and dC from the channel blocks' parts, in order: four states' dB or dC a
+// lane.
 template <int T>
 __global__ void __launch_bounds__(256) scan_bc_sum(ScanArgs a) {
-  const int64_t vals = a.b * a.l * a.g * a.n;
-  int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= 2 * vals) return;
-  const bool second = i >= vals;
-  if (second) i -= vals;
-  const int64_t row = i / a.n, token = row / a.g;
-  const int s = (int)(i - row * a.n), blk = s / a.spl;
-  const int64_t b = token / a.l, t = token - b * a.l;
+  const int w = a.nblk * 8;  // fours of a token and group
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = i / w, gr = row / a.l, t = row - gr * a.l, b = gr / a.g;
+  if (b >= a.b) return;
+  const int k = (int)(i - row * w), g = (int)(gr - b * a.g), blk = k / 8, four = k % 8;
+  const int s0 = blk * 16 + four / 2 * 4;
   const int pairs = (a.dg + kPair - 1) / kPair;
-  float v = 0.f;
+  const int64_t size = a.b * a.lp * a.g * a.nblk * 32;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
   if (t < length_of(a, b)) {
-    const int64_t size = a.b * a.lp * a.g * a.nblk * 2 * a.spl;
-    const int in = s - blk * a.spl, g = (int)(row - token * a.g);
-    const float* p = a.bcpart + (((b * a.g + g) * a.nblk + blk) * a.lp + t) * 2 * a.spl +
-                     (in / 4 * 8 + in % 4 + (second ? 4 : 0));
-    for (int k = 0; k < pairs; ++k) v += p[k * size];
+    const float* p = a.bcpart + ((gr * a.nblk + blk) * a.lp + t) * 32 + four * 4;
+#pragma unroll 8
+    for (int j = 0; j < pairs; ++j) v += *(const f32x4*)(p + j * size);
   }
-  store1<T>(second ? a.dc : a.db, i, v);
+  void* const out = four % 2 ? a.dc : a.db;
+  const int64_t at = ((b * a.l + t) * a.g + g) * a.n + s0;
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+    if (s0 + s < a.n) store1<T>(out, at + s, v[s]);
 }
 
 template <int T, bool GATE>
@@ -559,7 +561,7 @@ template <int T>
 void go_grad(const ScanArgs& a, hipStream_t st) {
   if (a.z) go_gate<T, true>(a, st);
   else go_gate<T, false>(a, st);
-  const int64_t vals = 2 * a.b * a.l * a.g * a.n;
+  const int64_t vals = a.b * a.l * a.g * a.nblk * 8;
   if (vals > 0)
     hipLaunchKernelGGL((scan_bc_sum<T>), dim3((uint32_t)((vals + 255) / 256)), dim3(256), 0, st, a);
 }
