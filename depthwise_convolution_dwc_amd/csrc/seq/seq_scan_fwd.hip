@@ -461,6 +461,9 @@ void scan_split(ScanArgs* a, bool bwd) {
   // (the gradients' and the one pass' waves take fours of blocks of 16)
   a->spl = bwd || a->one ? 16 : (a->n <= 4 ? 4 : (a->n <= 8 ? 8 : 16));
   a->nblk = (a->n + a->spl - 1) / a->spl;
+  // a workgroup of the gradients holds 16, 32 or 64 states
+  if (bwd && a->nblk > 2) a->nblk = (a->nblk + 3) / 4 * 4;
+  a->gblk = (a->nblk + 3) / 4;
   a->lp = (a->l + kGradChunk - 1) / kGradChunk * kGradChunk;
   if (bwd) {
     a->tc = kGradChunk;

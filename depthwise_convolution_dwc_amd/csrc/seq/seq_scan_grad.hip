@@ -9,7 +9,7 @@
 //
 // Chunks of 32 tokens side by side: scan_chunk and scan_combine give each its
 // first state and the gradient that reaches its last one.  A workgroup takes a
-// chunk of 128 channels, wave w states 4 w to 4 w + 3 of two channels a lane.
+// chunk of 64 channels, wave w states 4 w to 4 w + 3 with a channel a lane.
 // It first runs forward and leaves the state before every 8 tokens in LDS,
 // then takes the eights from the last to the first: forward with the states
 // and decays in registers, and back.  The sums over the channels (dB, dC) are
@@ -169,17 +169,18 @@ struct OneToken {
   }
 };
 
-template <int T, bool GATE, bool MULTI>
-__global__ void __launch_bounds__(256, NC == 1 ? 4 : 2) scan_grad(ScanArgs a) {
-  constexpr int NW = 4, SPL = 4 * NW;
+template <int T, int NW, bool GATE, bool MULTI>
+__global__ void __launch_bounds__(64 * NW, 4) scan_grad(ScanArgs a) {
+  constexpr int SPL = 16;                       // states of a line of bc
+  constexpr int NT = NW < kEight ? kEight / NW : 1;  // tokens of an eight that a wave shares
   __shared__ float of[kOf][kEight][kPair];
   __shared__ float sums[3][4][NW][kPair];     // over a wave's states
-  __shared__ float first[kSubs][NC * 4][256];  // states before the eights
+  __shared__ float first[kSubs][NC * 4][64 * NW];  // states before the eights
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int pairs = (a.dg + kPair - 1) / kPair;
   uint32_t i = blockIdx.x;
-  const int blk = MULTI ? (int)(i % (uint32_t)a.nblk) : 0;
-  if (MULTI) i /= (uint32_t)a.nblk;
+  const int blk = MULTI ? (int)(i % (uint32_t)a.gblk) : 0;
+  if (MULTI) i /= (uint32_t)a.gblk;
   const int block = (int)(i % (uint32_t)pairs);
   i /= (uint32_t)pairs;
   const int g = (int)(i % (uint32_t)a.g);
@@ -203,7 +204,7 @@ __global__ void __launch_bounds__(256, NC == 1 ? 4 : 2) scan_grad(ScanArgs a) {
     dskip[k] = dbias[k] = 0.f;
   }
   float a2[NC][4], da[NC][4], carry[NC][4], h[NC][4];
-  const int n0 = blk * SPL + 4 * wave;
+  const int n0 = 4 * (blk * NW + wave);
   // (all loads under way together, then what is not there made zero)
   {
     const auto states = [&](const float* p, float(&v)[NC][4]) {  // of d x n
@@ -245,50 +246,52 @@ __global__ void __launch_bounds__(256, NC == 1 ? 4 : 2) scan_grad(ScanArgs a) {
   }
   // B and C of the wave's states, tokens 2 SPL apart; rows up to whole chunks
   // are there
-  const int64_t lines = (((b * a.g + g) * a.nblk + blk) * a.lp + t0) * (2 * SPL);
-  const float* const bc = a.bc + lines + 8 * wave;
-  float* const bcpart = a.bcpart + block * (a.b * a.g * a.nblk * a.lp * 2 * SPL) + lines + 8 * wave;
+  const int64_t lines = (((b * a.g + g) * a.nblk + n0 / 16) * a.lp + t0) * (2 * SPL) + 8 * (wave % 4);
+  const float* const bc = a.bc + lines;
+  float* const bcpart = a.bcpart + block * (a.b * a.g * a.nblk * a.lp * 2 * SPL) + lines;
 
-  // a wave's own tokens of an eight, wave and 4 + wave; next[] is the address
+  // a wave's own tokens of an eight, wave and NW + wave; next[] is the address
   // of the first of them in the eight to be read.  Chunks cut short read a
   // token past the last one as the chunk's first.
   constexpr int N = GATE ? 4 : 3;
-  RawToken<T, NC, GATE> raw[2];
-  const bool whole = live == kGradChunk;
+  RawToken<T, NC, GATE> raw[NT];
+  const bool whole = live == kGradChunk, mine = wave < kEight;
   const char* next[N];
-  int64_t four[N];
-  addresses<T, N>(a, b, t0 + (whole ? wave : 0), g0, next, four);
+  int64_t eight[N];  // bytes of eight tokens
+  addresses<T, N>(a, b, t0 + (whole && mine ? wave : 0), g0, next, eight);
 #pragma unroll
-  for (int i = 0; i < N; ++i) four[i] *= 4;
+  for (int i = 0; i < N; ++i) eight[i] *= kEight;
   const auto fetch = [&](int sub, int turn) {
     const char* p[N];
     if (whole) {
-      raw[0].load(next, in);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        p[i] = next[i] + four[i];
-        next[i] += 2 * turn * four[i];
+      for (int j = 0; j < NT; ++j) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) p[i] = next[i] + j * (eight[i] / NT);
+        raw[j].load(p, in);
       }
-      raw[1].load(p, in);
+#pragma unroll
+      for (int i = 0; i < N; ++i) next[i] += turn * eight[i];
     } else {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int t = sub * kEight + 4 * j + wave;
+      for (int j = 0; j < NT; ++j) {
+        const int t = sub * kEight + NW * j + wave;
 #pragma unroll
-        for (int i = 0; i < N; ++i) p[i] = next[i] + (t < live ? t : 0) * (four[i] / 4);
+        for (int i = 0; i < N; ++i) p[i] = next[i] + (t < live ? t : 0) * (eight[i] / kEight);
         raw[j].load(p, in);
       }
     }
   };
   const auto share = [&](int sub, bool all) {
+    if (!mine) return;
     // (the bias is read again for each eight: registers are short)
     const float* pb = a.bias ? a.bias + g0 : nullptr;
     float bias[NC];
 #pragma unroll
     for (int k = 0; k < NC; ++k) bias[k] = pb ? pb[in[k]] : 0.f;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int at = 4 * j + wave;
+    for (int j = 0; j < NT; ++j) {
+      const int at = NW * j + wave;
 #pragma unroll
       for (int k = 0; k < NC; ++k) {
         const Token v = token_of(a, raw[j], k, bias[k], on[k] && sub * kEight + at < live);
@@ -416,19 +419,19 @@ __global__ void __launch_bounds__(256, NC == 1 ? 4 : 2) scan_grad(ScanArgs a) {
       }
       __syncthreads();
       FreshArgs& f = fresh_args();
-      const int j = 4 * half + wave;
+      const int j = 4 * half + (NW > 4 ? wave % 4 : wave);
       const int t = sub * kEight + j;
       const int64_t at = row_out + (int64_t)t * f.d;
 #pragma unroll
       for (int k = 0; k < NC; ++k) {
         float gb = 0.f, aq = 0.f, ch = 0.f;
-#pragma unroll
+#pragma unroll 4
         for (int m = 0; m < NW; ++m) {
-          gb += sums[0][wave][m][NC * lane + k];
-          aq += sums[1][wave][m][NC * lane + k];
-          ch += sums[2][wave][m][NC * lane + k];
+          gb += sums[0][j % 4][m][NC * lane + k];
+          aq += sums[1][j % 4][m][NC * lane + k];
+          ch += sums[2][j % 4][m][NC * lane + k];
         }
-        if (!on[k] || t >= tokens) continue;
+        if (!on[k] || t >= tokens || wave >= 4) continue;
         if constexpr (MULTI) {
           const int64_t all = f.b * f.l * f.d;
           float* out = f.sums + blk * 3 * all + at;
@@ -468,7 +471,7 @@ __global__ void __launch_bounds__(256, NC == 1 ? 4 : 2) scan_grad(ScanArgs a) {
 #pragma unroll
       for (int k = 0; k < NC; ++k) {
         float x = 0.f, y = 0.f;
-#pragma unroll
+#pragma unroll 4
         for (int m = 0; m < NW; ++m) {
           x += sums[0][0][m][NC * lane + k];
           y += sums[1][0][m][NC * lane + k];
@@ -505,7 +508,7 @@ __global__ void __launch_bounds__(256) scan_finish(ScanArgs a) {
       addresses<T, N>(a, b, t, 0, p, step);
       r.load(p, c);
       float gb = 0.f, aq = 0.f, ch = 0.f;
-      for (int k = 0; k < a.nblk; ++k) {
+      for (int k = 0; k < a.gblk; ++k) {
         gb += a.sums[3 * k * all + at + c[0]];
         aq += a.sums[(3 * k + 1) * all + at + c[0]];
         ch += a.sums[(3 * k + 2) * all + at + c[0]];
@@ -547,13 +550,17 @@ __global__ void __launch_bounds__(256) scan_bc_sum(ScanArgs a) {
 template <int T, bool GATE>
 void go_gate(const ScanArgs& a, hipStream_t st) {
   const int pairs = (a.dg + kPair - 1) / kPair;
-  const dim3 grid((uint32_t)(a.b * a.nc * a.g * pairs * a.nblk));
-  if (a.nblk > 1) {
-    hipLaunchKernelGGL((scan_grad<T, GATE, true>), grid, dim3(256), 0, st, a);
+  const dim3 grid((uint32_t)(a.b * a.nc * a.g * pairs * a.gblk));
+  if (a.gblk > 1) {
+    hipLaunchKernelGGL((scan_grad<T, 16, GATE, true>), grid, dim3(1024), 0, st, a);
     hipLaunchKernelGGL((scan_finish<T, GATE>), dim3((uint32_t)((a.b * a.nc * a.d + 255) / 256)),
                        dim3(256), 0, st, a);
+  } else if (a.nblk == 1) {
+    hipLaunchKernelGGL((scan_grad<T, 4, GATE, false>), grid, dim3(256), 0, st, a);
+  } else if (a.nblk == 2) {
+    hipLaunchKernelGGL((scan_grad<T, 8, GATE, false>), grid, dim3(512), 0, st, a);
   } else {
-    hipLaunchKernelGGL((scan_grad<T, GATE, false>), grid, dim3(256), 0, st, a);
+    hipLaunchKernelGGL((scan_grad<T, 16, GATE, false>), grid, dim3(1024), 0, st, a);
   }
 }
 

@@ -60,7 +60,8 @@ struct ScanArgs {
   // how the work is split: dg channels a group; spl states a lane in blocks of
   // that many, cblk blocks of 64 channels a group, nc chunks of tc tokens
   int dg, spl, nblk, cblk, tc, nc;
-  int one;  // one pass over all tokens, no chunks
+  int one;   // one pass over all tokens, no chunks
+  int gblk;  // blocks of states of the gradients' workgroups
   // workspace
   int64_t lp;      // l up to whole chunks of the gradients
   float* bc;       // [b][g][nblk][lp][2 spl]: B and C in fp32, zeros past n and past a length
@@ -70,7 +71,7 @@ struct ScanArgs {
   float* bcpart;   // [channel blocks a group][b][g][nblk][lp][2 spl]
   float* apart;    // [b nc][nblk spl][d]
   float* dpart;    // [b nc][2][d]
-  float* sums;     // [nblk][3][b l d]
+  float* sums;     // [gblk][3][b l d]
 };
 constexpr int kGradChannels = 64, kGradChunk = 32;  // of a workgroup of the gradients
 // Fills the split of the work.

@@ -196,7 +196,7 @@ int scan_layout(ScanArgs* a, bool bwd, char* base, size_t* bytes) {
     take(&a->bcpart, pairs * tokens * a->g * line);
     take(&a->apart, rows * np * a->d);
     take(&a->dpart, rows * 2 * a->d);
-    if (a->nblk > 1) take(&a->sums, 3 * a->nblk * tokens * a->d);
+    if (a->gblk > 1) take(&a->sums, 3 * a->gblk * tokens * a->d);
   }
   *bytes = at;
   return DWC_OK;
