@@ -437,18 +437,18 @@ void prepare_bwd(const ScanArgs& a, hipStream_t st) {
 }  // namespace scan
 
 // Whether one pass over all tokens is done before the chunks' three.  It takes
-// kOne a token while its workgroups (64 channels each) have SIMDs to themselves, then kMore a token and workgroup;
-// the chunks' three passes take kTwo a token and workgroup and kFixed besides,
-// for their launches and the states between them.  bf16, us: 256 tokens of
-// 2048 channels, 16 states: 34 and 51 in chunks; 1024 tokens: 110 and 56; 16
-// sequences of 2048 tokens: 326 and 501; 32 states, 4 sequences of 700 tokens
-// of 512 channels: 102 and 72, 16 such: 108 and 160.
+// kOne a token while its workgroups (64 channels each) have SIMDs to
+// themselves, then kMore a token and workgroup; the chunks take kTwo a token
+// and workgroup and kFixed besides, for their launches and the states between
+// them.  bf16, us: 256 tokens of 2048 channels, 16 states: 34 and 51 in chunks;
+// 1024 tokens: 110 and 54; 16 sequences of 2048 tokens: 361 and 501; 32 states,
+// 4 sequences of 700 tokens of 512 channels: 112 and 70, 16 such: 117 and 160.
 static bool one_pass(const ScanArgs& a) {
   if (a.n > 64) return false;
   const int blocks = (a.n + 15) / 16;
   const double groups = (double)(a.b * a.g * a.cblk);
-  const double kOne = a.n <= 16 ? 0.103 : (a.n <= 32 ? 0.146 : 0.22);
-  const double kMore = 0.00027 * blocks;
+  const double kOne = a.n <= 16 ? 0.106 : (a.n <= 32 ? 0.146 : 0.22);
+  const double kMore = 0.0003 * blocks;
   const double kTwo = 0.00043 * (blocks == 1 ? 1 : 1 + blocks), kFixed = 40.0;
   const double token = kMore * groups > kOne ? kMore * groups : kOne;
   return token * (double)a.l < kFixed + kTwo * groups * (double)a.l;
@@ -476,6 +476,8 @@ void scan_split(ScanArgs* a, bool bwd) {
     if (nc < 1) nc = 1;
     a->tc = (int)(((a->l + nc - 1) / nc + 7) / 8 * 8);
     if (a->tc < 8) a->tc = 8;
+    // inside a chunk each decay is rounded: no more of them than 128
+    if (a->tc > 128) a->tc = 128;
   }
   a->nc = (int)((a->l + a->tc - 1) / a->tc);
   if (a->nc < 1) a->nc = 1;

@@ -6,7 +6,13 @@
 // steps, inputs and gates (tokens w, w + NW, ...), all run the stage on their
 // own states, and join the parts of C . h in LDS, where each finishes its own
 // tokens.  B and C go through LDS too, a stage ahead: there are few waves to
-// wait for the scalar cache.  A state takes its exp and four
+// wait for the scalar cache.
+//
+// A decay near 1 loses what is below 2^-24, and a product of many loses that
+// much each time (16 states, 491 tokens: the last state off by 8e-7 of its
+// norm, now by 2e-7).  So a second state starts from zero every 64 tokens and the first one
+// is made again from it there, with one decay for the sum of their steps; that
+// is one of six instructions, and 5 to 10% of the time.  A state takes its exp and four
 // other instructions once, not twice as in chunks; bound: the vector units.
 #include "seq_scan.h"
 
@@ -14,7 +20,7 @@ namespace dwc {
 namespace seq {
 namespace scan {
 
-constexpr int kStage = 16;
+constexpr int kStage = 16, kAgain = 4;  // tokens; stages until the states are made again
 
 template <int T, int NW, int S, bool GATE>
 __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
@@ -35,7 +41,7 @@ __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
   const bool on = (int)c0 < a.dg;
   const uint32_t in = on ? c0 : 0;  // (lanes past the end repeat the first channel)
   const int n0 = S * wave;
-  float a2[S], h[S];
+  float a2[S], h[S], start[S], from[S], sum = 0.f;  // from: from zero, start: at that time
   const auto states = [&](const float* p, float(&v)[S]) {  // of d x n
 #pragma unroll
     for (int s = 0; s < S; ++s) v[s] = (p + (n0 + s < a.n ? n0 + s : 0))[in * (uint32_t)a.n];
@@ -49,6 +55,11 @@ __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
     h[s] = 0.f;
   }
   if (a.s0) states(a.s0 + (b * a.d + g0) * a.n, h);
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    start[s] = h[s];
+    from[s] = 0.f;
+  }
   const float bias = a.bias ? (a.bias + g0)[in] : 0.f, skip = a.skip ? (a.skip + g0)[in] : 0.f;
   // B and C of a stage: S / 2 values a thread; rows up to a multiple of the
   // stage are there, but for blocks of 16 states past the last
@@ -144,6 +155,7 @@ __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
     read(0);
     read(1);
     decays(0);
+    float steps = 0.f;
 #pragma unroll
     for (int j = 0; j < kStage; ++j) {
       __builtin_amdgcn_sched_barrier(0);
@@ -152,10 +164,27 @@ __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
       float y = 0.f;
 #pragma unroll
       for (int s = 0; s < S; ++s) {
-        h[s] = fmaf(k[j % 2][s], h[s], du[j % 3] * bb[j % 3][s]);
+        const float x = du[j % 3] * bb[j % 3][s];
+        h[s] = fmaf(k[j % 2][s], h[s], x);
+        from[s] = fmaf(k[j % 2][s], from[s], x);
         y = fmaf(cc[j % 3][s], h[s], y);
       }
+      steps += dt[j % 3];
+      // (nothing reads these before the end: without this all 16 steps of them
+      // are put off to there, their operands held in registers)
+#pragma unroll
+      for (int s = 0; s < S; ++s) asm volatile("" : "+v"(from[s]));
+      asm volatile("" : "+v"(steps));
       parts[j][wave][lane] = y;
+    }
+    sum += steps;
+    if (t0 / kStage % kAgain == kAgain - 1) {
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        h[s] = start[s] = fmaf(exp2_of(a2[s] * sum), start[s], from[s]);
+        from[s] = 0.f;
+      }
+      sum = 0.f;
     }
     if (t0 + kStage < len) keep(side ^ 1);
     __syncthreads();
@@ -182,7 +211,8 @@ __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
   float* const s1 = a.s1 + (b * a.d + g0) * a.n;
 #pragma unroll
   for (int s = 0; s < S; ++s)
-    if (on && n0 + s < a.n) (s1 + n0 + s)[in * (uint32_t)a.n] = h[s];
+    if (on && n0 + s < a.n)
+      (s1 + n0 + s)[in * (uint32_t)a.n] = fmaf(exp2_of(a2[s] * sum), start[s], from[s]);
 }
 
 template <int T, int NW, int S, bool GATE>
@@ -196,7 +226,7 @@ void go_wide(const ScanArgs& a, hipStream_t st) {
   if (a.n <= 8) return go_shape<T, 4, 2, GATE>(a, st);
   // two states a wave while that leaves no SIMD more than two waves (8 and 16
   // sequences of 2048 tokens of 2048 channels: 220 and 361 us, with four 249
-  // and 326)
+  // and 326, all four before the states were made again)
   if (a.n <= 16)
     return a.b * a.g * a.cblk <= 256 ? go_shape<T, 8, 2, GATE>(a, st)
                                      : go_shape<T, 4, 4, GATE>(a, st);
