@@ -50,8 +50,9 @@ hipError_t launch_column_sums(const ColumnSum (&jobs)[kColumnJobs], hipStream_t 
   for (const ColumnSum& s : jobs)
     if (s.out) cols += s.cols;
   if (cols == 0) return hipSuccess;
-  // whole lines of the rows where there are columns enough for the device
-  const int width = cols >= 16384 ? 64 : 16;
+  // whole lines of the rows where there are columns for 64 workgroups (6144
+  // columns of 1024 rows: 7 us, 11 by 16 columns)
+  const int width = cols >= 4096 ? 64 : 16;
   ColumnJobs a{};
   uint32_t blocks = 0;
   for (int i = 0; i < kColumnJobs; ++i) {

@@ -98,57 +98,77 @@ __device__ __forceinline__ void load_row(const void* p, int64_t row, int64_t str
   }
 }
 
+// Each group of LPR lanes walks rows; the weights stay in registers and the
+// next row is read while this one's sums are made (a workgroup a row with its
+// weights read again: 88 us for 16384 rows of 2048, so 74).
 template <int XT, int YT, int VEC, int LPR, int NV>
 __global__ void __launch_bounds__(LPR <= 64 ? kBlock : LPR) resnorm_fwd(ResNormArgs a) {
   constexpr int ROWS = LPR <= 64 ? kBlock / LPR : 1;
   __shared__ float lds[LPR <= 64 ? 1 : LPR / 64];
-  const int lane = threadIdx.x % LPR;
-  const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / LPR;
-  const bool live = row < a.rows;
-  float y[NV][VEC], x[NV][VEC], g[NV][VEC], scale[NV][VEC], post[NV][VEC], pre[NV][VEC];
-  load_row<YT, VEC, LPR, NV>(a.y, row, a.y_stride, live, a.c, lane, 0.f, y);
-  load_row<XT, VEC, LPR, NV>(a.x, row, a.x_stride, live, a.c, lane, 0.f, x);
-  load_row<YT, VEC, LPR, NV>(a.gate, row, a.gate_stride, live, a.c, lane, 1.f, g);
+  const int lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
+  float yn[NV][VEC], xn[NV][VEC], gn[NV][VEC], scale[NV][VEC], post[NV][VEC], pre[NV][VEC];
+  const auto fetch = [&](int64_t row) {
+    const bool live = row < a.rows;
+    load_row<YT, VEC, LPR, NV>(a.y, row, a.y_stride, live, a.c, lane, 0.f, yn);
+    load_row<XT, VEC, LPR, NV>(a.x, row, a.x_stride, live, a.c, lane, 0.f, xn);
+    load_row<YT, VEC, LPR, NV>(a.gate, row, a.gate_stride, live, a.c, lane, 1.f, gn);
+  };
+  const int64_t step = (int64_t)a.groups * ROWS, first = (int64_t)blockIdx.x * ROWS;
+  fetch(first + sub);
   weights<VEC, LPR, NV>(a, lane, scale, post, pre);
   const float c = (float)a.c;
-  float q1 = 1.f;
-  if (a.post) {
-    float s = 0.f;
+  const int act = a.gate ? a.act : A_NONE;
+  for (int64_t row0 = first; row0 < a.rows; row0 += step) {  // (the same in all waves)
+    const int64_t row = row0 + sub;
+    const bool live = row < a.rows;
+    float y[NV][VEC], x[NV][VEC], g[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) s = fmaf(y[i][j], y[i][j], s);
-    q1 = 1.f / sqrtf(row_sum<LPR>(s, lds) / c + a.eps);
-  }
-  const int act = a.gate ? a.act : A_NONE;
-  float s = 0.f;
+      for (int j = 0; j < VEC; ++j) {
+        y[i][j] = yn[i][j];
+        x[i][j] = xn[i][j];
+        g[i][j] = gn[i][j];
+      }
+    if (row0 + step < a.rows) fetch(row + step);
+    float q1 = 1.f;
+    if (a.post) {
+      float s = 0.f;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int64_t col = (int64_t)(i * LPR + lane) * VEC;
-    const bool in = col < a.c;
+      for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const float p = y[i][j] * q1 * post[i][j];
-      x[i][j] = fmaf(scale[i][j] * act_of(act, g[i][j])[0], p, x[i][j]);
-      if (in) s = fmaf(x[i][j], x[i][j], s);
+        for (int j = 0; j < VEC; ++j) s = fmaf(y[i][j], y[i][j], s);
+      q1 = 1.f / sqrtf(row_sum<LPR>(s, lds) / c + a.eps);
     }
-    if (live && in) store_vec<XT, VEC>(a.r, row * a.c + col, x[i]);
-  }
-  float q2 = 1.f;
-  if (a.pre) {
-    q2 = 1.f / sqrtf(row_sum<LPR>(s, lds) / c + a.eps);
+    float s = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int64_t col = (int64_t)(i * LPR + lane) * VEC;
-      if (!live || col >= a.c) continue;
+      const bool in = col < a.c;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) x[i][j] *= q2 * pre[i][j];
-      store_vec<YT, VEC>(a.h, row * a.c + col, x[i]);
+      for (int j = 0; j < VEC; ++j) {
+        const float p = y[i][j] * q1 * post[i][j];
+        x[i][j] = fmaf(scale[i][j] * act_of(act, g[i][j])[0], p, x[i][j]);
+        if (in) s = fmaf(x[i][j], x[i][j], s);
+      }
+      if (live && in) store_vec<XT, VEC>(a.r, row * a.c + col, x[i]);
     }
-  }
-  if (live && lane == 0) {
-    if (a.post_rstd) a.post_rstd[row] = q1;
-    if (a.pre_rstd) a.pre_rstd[row] = q2;
+    float q2 = 1.f;
+    if (a.pre) {
+      q2 = 1.f / sqrtf(row_sum<LPR>(s, lds) / c + a.eps);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int64_t col = (int64_t)(i * LPR + lane) * VEC;
+        if (!live || col >= a.c) continue;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) x[i][j] *= q2 * pre[i][j];
+        store_vec<YT, VEC>(a.h, row * a.c + col, x[i]);
+      }
+    }
+    if (live && lane == 0) {
+      if (a.post_rstd) a.post_rstd[row] = q1;
+      if (a.pre_rstd) a.pre_rstd[row] = q2;
+    }
   }
 }
 
@@ -382,9 +402,9 @@ __global__ void __launch_bounds__(kBlock) resnorm_cols_long(ResNormArgs a) {
 
 static bool aligned(const void* p) { return ((uintptr_t)p % 16) == 0; }
 
-// Values of a row that a lane holds: forward six registers a value, of 512
-// and of 128 in the 1024-lane form; backward eleven.
-constexpr int most(int lpr, bool bwd) { return bwd ? (lpr == 1024 ? 8 : 16) : (lpr == 1024 ? 8 : 32); }
+// Values of a row that a lane holds: nine registers a value forward, eleven
+// backward, of 512 and of 128 in the 1024-lane form.
+constexpr int most(int lpr) { return lpr == 1024 ? 8 : 16; }
 
 }  // namespace resnorm
 
@@ -406,15 +426,16 @@ ResNormShape resnorm_shape(const ResNormArgs& a, bool bwd) {
   for (int lpr : {64, 256, 1024}) {
     const int64_t nv = (n + lpr - 1) / lpr;
     for (int v : {1, 2, 4, 8})
-      if (nv <= v && v * vec <= most(lpr, bwd)) return {vec, lpr, v};
+      if (nv <= v && v * vec <= most(lpr)) return {vec, lpr, v};
   }
   return {1, 0, 0};
 }
 
-int resnorm_groups(const ResNormArgs& a, const ResNormShape& s) {
+int resnorm_groups(const ResNormArgs& a, const ResNormShape& s, bool bwd) {
   if (s.lpr == 0) return (int)(a.rows < 64 ? (a.rows > 0 ? a.rows : 1) : 64);
   const int64_t per = s.lpr <= 64 ? kBlock / s.lpr : 1;
-  const int64_t most = s.lpr <= 64 ? 1024 : (s.lpr == 256 ? 1024 : 256);
+  // (the backward pass leaves a row of partial sums each)
+  const int64_t most = (s.lpr <= 256 ? 1024 : 256) * (bwd ? 1 : 2);
   const int64_t need = (a.rows + per - 1) / per;
   return (int)(need < 1 ? 1 : (need < most ? need : most));
 }
@@ -423,15 +444,10 @@ namespace resnorm {
 
 template <int XT, int YT, int VEC, int LPR, int NV>
 void go(bool bwd, const ResNormArgs& a, hipStream_t st) {
-  constexpr int block = LPR <= 64 ? kBlock : LPR, rows = block / LPR;
-  if (bwd) {
-    if constexpr (NV * VEC <= most(LPR, true))
-      hipLaunchKernelGGL((resnorm_bwd<XT, YT, VEC, LPR, NV>), dim3(a.groups), dim3(block), 0, st,
-                         a);
-  } else {
-    if constexpr (NV * VEC <= most(LPR, false))
-      hipLaunchKernelGGL((resnorm_fwd<XT, YT, VEC, LPR, NV>),
-                         dim3((uint32_t)((a.rows + rows - 1) / rows)), dim3(block), 0, st, a);
+  constexpr int block = LPR <= 64 ? kBlock : LPR;
+  if constexpr (NV * VEC <= most(LPR)) {
+    auto* f = bwd ? &resnorm_bwd<XT, YT, VEC, LPR, NV> : &resnorm_fwd<XT, YT, VEC, LPR, NV>;
+    hipLaunchKernelGGL(f, dim3(a.groups), dim3(block), 0, st, a);
   }
 }
 
@@ -491,7 +507,8 @@ static hipError_t launch(bool bwd, const ResNormArgs& a, hipStream_t st) {
 
 }  // namespace resnorm
 
-hipError_t launch_resnorm_fwd(const ResNormArgs& a, hipStream_t st) {
+hipError_t launch_resnorm_fwd(ResNormArgs a, hipStream_t st) {
+  a.groups = resnorm_groups(a, resnorm_shape(a, false), false);
   return launch(false, a, st);
 }
 

@@ -108,8 +108,8 @@ struct ResNormShape {
   int vec, lpr, nv;
 };
 ResNormShape resnorm_shape(const ResNormArgs& a, bool bwd);
-int resnorm_groups(const ResNormArgs& a, const ResNormShape& s);
-hipError_t launch_resnorm_fwd(const ResNormArgs& a, hipStream_t st);
+int resnorm_groups(const ResNormArgs& a, const ResNormShape& s, bool bwd);
+hipError_t launch_resnorm_fwd(ResNormArgs a, hipStream_t st);
 hipError_t launch_resnorm_bwd(const ResNormArgs& a, float* dscale, float* dw_post, float* dw_pre,
                               hipStream_t st);
 

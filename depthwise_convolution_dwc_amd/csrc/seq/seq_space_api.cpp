@@ -493,7 +493,7 @@ int dwc_residual_norm_bwd_workspace_size(const dwc_resnorm_problem* p, size_t* b
     if (!wide) a.y = (const void*)1;  // no wide loads
     else a.y = nullptr;
     const ResNormShape s = resnorm_shape(a, true);
-    const size_t need = (size_t)resnorm_groups(a, s) * 3 * (size_t)p->c * 4 +
+    const size_t need = (size_t)resnorm_groups(a, s, true) * 3 * (size_t)p->c * 4 +
                         (s.lpr == 0 ? (size_t)p->rows * 4 : 0);
     if (need > most) most = need;
   }
@@ -552,7 +552,7 @@ int dwc_residual_norm_bwd(const dwc_resnorm_problem* p, const void* dr, const vo
   a.dy = dy;
   a.dgate = dgate;
   a.part = (float*)workspace;
-  a.groups = resnorm_groups(a, resnorm_shape(a, true));
+  a.groups = resnorm_groups(a, resnorm_shape(a, true), true);
   return hip_result(launch_resnorm_bwd(a, dscale, dw_post, dw_pre, (hipStream_t)stream),
                     "dwc_residual_norm_bwd launch");
 }
