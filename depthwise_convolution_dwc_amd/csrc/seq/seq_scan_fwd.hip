@@ -18,22 +18,38 @@ void launch_scan_wide(const ScanArgs& a, hipStream_t st);
 
 namespace scan {
 
+// B and C four values a thread, then A with its states' rows across: waves
+// read 64 channels of a state from one place.
 template <int T, bool FOURS>
 __global__ void __launch_bounds__(256) scan_prep(ScanArgs a) {
-  const int w = 2 * a.spl;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t line = i / w, row = line / a.lp, t = line - row * a.lp;  // row: of b g nblk
-  const int64_t gr = row / a.nblk, b = gr / a.g;
-  if (b >= a.b) return;
-  const int j = (int)(i - line * w), blk = (int)(row - gr * a.nblk), g = (int)(gr - b * a.g);
-  // states in order, or by fours with B and C in turn
-  const bool second = FOURS ? j & 4 : j >= a.spl;
-  const int s = blk * a.spl + (FOURS ? j / 8 * 4 + j % 4 : (second ? j - a.spl : j));
-  float v = 0.f;
-  if (s < a.n && t < length_of(a, b))
-    v = second ? load1<T>(a.cm, b * a.c_stride[0] + t * a.c_stride[1] + g * a.c_stride[2] + s)
-               : load1<T>(a.bm, b * a.b_stride[0] + t * a.b_stride[1] + g * a.b_stride[2] + s);
-  a.bc[i] = v;
+  const uint32_t w = (uint32_t)a.spl / 2;  // threads a line
+  const uint32_t rows = (uint32_t)(a.b * a.g * a.nblk), lp = (uint32_t)a.lp;
+  uint32_t i = blockIdx.x * 256 + threadIdx.x;
+  if (i < rows * lp * w) {
+    const uint32_t line = i / w, j = (i - line * w) * 4, row = line / lp;
+    const int64_t t = line - row * lp;
+    const uint32_t gr = row / (uint32_t)a.nblk, blk = row - gr * (uint32_t)a.nblk;
+    const int64_t b = gr / (uint32_t)a.g, g = gr - (uint32_t)b * (uint32_t)a.g;
+    // states in order, or by fours with B and C in turn
+    const bool second = FOURS ? j & 4 : j >= (uint32_t)a.spl;
+    const int s0 = (int)(blk * a.spl + (FOURS ? j / 8 * 4 : (second ? j - a.spl : j)));
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    if (t < length_of(a, b)) {
+      const int64_t at =
+          second ? b * a.c_stride[0] + t * a.c_stride[1] + g * a.c_stride[2] + s0
+                 : b * a.b_stride[0] + t * a.b_stride[1] + g * a.b_stride[2] + s0;
+      const void* p = second ? a.cm : a.bm;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (s0 + k < a.n) v[k] = load1<T>(p, at + k);
+    }
+    ((f32x4*)a.bc)[i] = v;
+    return;
+  }
+  i -= rows * lp * w;
+  const uint32_t s = i / (uint32_t)a.d, c = i - s * (uint32_t)a.d;
+  if (s < (uint32_t)(a.nblk * a.spl))
+    a.a2[i] = s < (uint32_t)a.n ? kLog2e * a.a[(int64_t)c * a.n + s] : 0.f;
 }
 
 // What a workgroup works on.
@@ -72,15 +88,9 @@ __device__ __forceinline__ Where where(const ScanArgs& a, int blk, uint32_t i, i
 
 template <int SPL>
 __device__ __forceinline__ void load_a(const ScanArgs& a, const Where& w, float (&v)[SPL]) {
-  const float* p = a.a + w.g0 * a.n;
-  const uint32_t at = w.in * (uint32_t)a.n;  // d n is below 2^32
+  const float* p = a.a2 + ((int64_t)w.blk * SPL * a.d + w.g0);
 #pragma unroll
-  for (int s = 0; s < SPL; ++s) {  // (loads of all states under way together)
-    const int i = w.blk * SPL + s;
-    v[s] = (p + (i < a.n ? i : 0))[at];
-  }
-#pragma unroll
-  for (int s = 0; s < SPL; ++s) v[s] = w.blk * SPL + s < a.n ? kLog2e * v[s] : 0.f;
+  for (int s = 0; s < SPL; ++s) v[s] = (p + (int64_t)s * a.d)[w.in];
 }
 
 // B and C of the chunk's first token.
@@ -213,7 +223,7 @@ __global__ void __launch_bounds__(64 * RUNS) scan_combine(ScanArgs a) {
   const int s = (int)(row - (uint32_t)b * np);
   const bool back = blockIdx.y == 1, in = s < a.n;
   const int64_t own = (b * a.d + c) * a.n + (in ? s : 0), step = (int64_t)np * a.d;
-  const float a2 = in ? kLog2e * a.a[(int64_t)c * a.n + s] : 0.f;
+  const float a2 = a.a2[(int64_t)s * a.d + c];
   const float* from = back ? a.ds1 : a.s0;
   float carry = from && in ? from[own] : 0.f;
   float* x = (back ? a.rstates : a.states) + (b * a.nc * np + s) * a.d + c;
@@ -380,10 +390,9 @@ __global__ void __launch_bounds__(MULTI ? 1024 : 64) scan_out(ScanArgs a) {
 
 template <int T, bool FOURS>
 void lay_out(const ScanArgs& a, hipStream_t st) {
-  const int64_t vals = a.b * a.lp * a.g * a.nblk * 2 * a.spl;
-  if (vals > 0)
-    hipLaunchKernelGGL((scan_prep<T, FOURS>), dim3((uint32_t)((vals + 255) / 256)), dim3(256), 0,
-                       st, a);
+  const int64_t lanes = a.b * a.lp * a.g * a.nblk * a.spl / 2 + (int64_t)a.nblk * a.spl * a.d;
+  hipLaunchKernelGGL((scan_prep<T, FOURS>), dim3((uint32_t)((lanes + 255) / 256)), dim3(256), 0, st,
+                     a);
 }
 
 template <int T, int SPL, bool BWD, bool GATE>

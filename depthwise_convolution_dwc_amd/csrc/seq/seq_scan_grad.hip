@@ -98,13 +98,13 @@ struct Token {
   float u, dt, slope, go, dz;
 };
 template <int T, int NC, bool GATE>
-__device__ __forceinline__ Token token_of(const ScanArgs& a, const RawToken<T, NC, GATE>& r, int k,
+__device__ __forceinline__ Token token_of(int soft, const RawToken<T, NC, GATE>& r, int k,
                                           float bias, bool live) {
   Token v;
   v.u = value<T>(r.v[0][k]);
   const float x = value<T>(r.v[1][k]) + bias, s = softplus(x);
-  v.dt = a.softplus ? s : x;  // (selects: branches would split the code)
-  v.slope = a.softplus ? sigmoid(x) : 1.f;
+  v.dt = soft ? s : x;  // (selects: branches would split the code)
+  v.slope = soft ? sigmoid(x) : 1.f;
   v.go = value<T>(r.v[2][k]);
   v.dz = 0.f;
   if constexpr (GATE) {
@@ -207,14 +207,10 @@ __global__ void __launch_bounds__(64 * NW, 4) scan_grad(ScanArgs a) {
   const int n0 = 4 * (blk * NW + wave);
   // (all loads under way together, then what is not there made zero)
   {
-    const auto states = [&](const float* p, float(&v)[NC][4]) {  // of d x n
 #pragma unroll
-      for (int k = 0; k < NC; ++k)
+    for (int k = 0; k < NC; ++k)
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
-          v[k][s] = (p + (n0 + s < a.n ? n0 + s : 0))[in[k] * (uint32_t)a.n];
-    };
-    states(a.a + g0 * a.n, a2);
+      for (int s = 0; s < 4; ++s) a2[k][s] = (a.a2 + ((int64_t)(n0 + s) * a.d + g0))[in[k]];
     if (a.nc > 1) {
       const int64_t at = (row * a.nblk * SPL + n0) * a.d + g0;
 #pragma unroll
@@ -229,18 +225,19 @@ __global__ void __launch_bounds__(64 * NW, 4) scan_grad(ScanArgs a) {
 #pragma unroll
       for (int k = 0; k < NC; ++k)
 #pragma unroll
-        for (int s = 0; s < 4; ++s) h[k][s] = carry[k][s] = 0.f;
-      if (a.s0) states(a.s0 + at, h);
-      if (a.ds1) states(a.ds1 + at, carry);
+        for (int s = 0; s < 4; ++s) {
+          const bool is = n0 + s < a.n;
+          const int64_t i = at + (int64_t)in[k] * a.n + (is ? n0 + s : 0);
+          h[k][s] = a.s0 && is ? a.s0[i] : 0.f;
+          carry[k][s] = a.ds1 && is ? a.ds1[i] : 0.f;
+        }
     }
 #pragma unroll
     for (int k = 0; k < NC; ++k)
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        const bool is = on[k] && n0 + s < a.n;
-        a2[k][s] = is ? kLog2e * a2[k][s] : 0.f;
-        h[k][s] = is ? h[k][s] : 0.f;
-        carry[k][s] = is ? carry[k][s] : 0.f;
+        h[k][s] = on[k] ? h[k][s] : 0.f;
+        carry[k][s] = on[k] ? carry[k][s] : 0.f;
         da[k][s] = 0.f;
       }
   }
@@ -248,7 +245,6 @@ __global__ void __launch_bounds__(64 * NW, 4) scan_grad(ScanArgs a) {
   // are there
   const int64_t lines = (((b * a.g + g) * a.nblk + n0 / 16) * a.lp + t0) * (2 * SPL) + 8 * (wave % 4);
   const float* const bc = a.bc + lines;
-  float* const bcpart = a.bcpart + block * (a.b * a.g * a.nblk * a.lp * 2 * SPL) + lines;
 
   // a wave's own tokens of an eight, wave and NW + wave; next[] is the address
   // of the first of them in the eight to be read.  Chunks cut short read a
@@ -285,7 +281,8 @@ __global__ void __launch_bounds__(64 * NW, 4) scan_grad(ScanArgs a) {
   const auto share = [&](int sub, bool all) {
     if (!mine) return;
     // (the bias is read again for each eight: registers are short)
-    const float* pb = a.bias ? a.bias + g0 : nullptr;
+    FreshArgs& f = fresh_args();
+    const float* pb = f.bias ? f.bias + g0 : nullptr;
     float bias[NC];
 #pragma unroll
     for (int k = 0; k < NC; ++k) bias[k] = pb ? pb[in[k]] : 0.f;
@@ -294,7 +291,7 @@ __global__ void __launch_bounds__(64 * NW, 4) scan_grad(ScanArgs a) {
       const int at = NW * j + wave;
 #pragma unroll
       for (int k = 0; k < NC; ++k) {
-        const Token v = token_of(a, raw[j], k, bias[k], on[k] && sub * kEight + at < live);
+        const Token v = token_of(f.softplus, raw[j], k, bias[k], on[k] && sub * kEight + at < live);
         of[DT][at][NC * lane + k] = v.dt;
         of[U][at][NC * lane + k] = v.u;
         if (all) {
@@ -346,7 +343,9 @@ __global__ void __launch_bounds__(64 * NW, 4) scan_grad(ScanArgs a) {
     share(sub, true);
     __syncthreads();
     const float* const rows = bc + sub * (kEight * 2 * SPL);
-    float* const rows_out = bcpart + sub * (kEight * 2 * SPL);
+    FreshArgs& o = fresh_args();
+    float* const rows_out = o.bcpart + block * (o.b * o.g * o.nblk * o.lp * 2 * SPL) + lines +
+                            sub * (kEight * 2 * SPL);
     float h[kEight + 1][NC][4], decay[kEight][NC][4];
 #pragma unroll
     for (int k = 0; k < NC; ++k)
@@ -450,14 +449,15 @@ __global__ void __launch_bounds__(64 * NW, 4) scan_grad(ScanArgs a) {
       __syncthreads();
     }
   }
+  FreshArgs& e = fresh_args();
 #pragma unroll
   for (int k = 0; k < NC; ++k)
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const int n = n0 + s;
-      if (on[k]) (a.apart + ((row * a.nblk * SPL + n) * a.d + g0))[in[k]] = da[k][s];
-      if (on[k] && n < a.n && chunk == 0 && a.ds0)
-        (a.ds0 + ((b * a.d + g0) * a.n + n))[in[k] * (uint32_t)a.n] = carry[k][s];
+      if (on[k]) (e.apart + ((row * e.nblk * SPL + n) * e.d + g0))[in[k]] = da[k][s];
+      if (on[k] && n < e.n && chunk == 0 && e.ds0)
+        (e.ds0 + ((b * e.d + g0) * e.n + n))[in[k] * (uint32_t)e.n] = carry[k][s];
     }
   if constexpr (!MULTI) {
     // dD and dbias over the waves' tokens
@@ -477,8 +477,8 @@ __global__ void __launch_bounds__(64 * NW, 4) scan_grad(ScanArgs a) {
           y += sums[1][0][m][NC * lane + k];
         }
         if (on[k]) {
-          (a.dpart + (row * 2 * a.d + g0))[in[k]] = x;
-          (a.dpart + ((row * 2 + 1) * a.d + g0))[in[k]] = y;
+          (e.dpart + (row * 2 * e.d + g0))[in[k]] = x;
+          (e.dpart + ((row * 2 + 1) * e.d + g0))[in[k]] = y;
         }
       }
     }
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(256) scan_finish(ScanArgs a) {
         aq += a.sums[(3 * k + 1) * all + at + c[0]];
         ch += a.sums[(3 * k + 2) * all + at + c[0]];
       }
-      finish<T, GATE>(a, at, c[0], gb, aq, ch, token_of(a, r, 0, bias, true), skip, dskip, dbias);
+      finish<T, GATE>(a, at, c[0], gb, aq, ch, token_of(a.softplus, r, 0, bias, true), skip, dskip, dbias);
     } else {
       finish_none<T, GATE>(a, at, c[0]);
     }

@@ -48,10 +48,10 @@ __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
 #pragma unroll
     for (int s = 0; s < S; ++s) v[s] = n0 + s < a.n ? v[s] : 0.f;
   };
-  states(a.a + g0 * a.n, a2);
 #pragma unroll
   for (int s = 0; s < S; ++s) {
-    a2[s] *= kLog2e;
+    // (waves past the last block of states have none)
+    a2[s] = n0 + s < a.nblk * SPL ? (a.a2 + ((int64_t)(n0 + s) * a.d + g0))[in] : 0.f;
     h[s] = 0.f;
   }
   if (a.s0) states(a.s0 + (b * a.d + g0) * a.n, h);

@@ -63,6 +63,7 @@ struct ScanArgs {
   int one;   // one pass over all tokens, no chunks
   int gblk;  // blocks of states of the gradients' workgroups
   // workspace
+  float* a2;       // [nblk spl][d]: A log2 e, zeros past n
   int64_t lp;      // l up to whole chunks of the gradients
   float* bc;       // [b][g][nblk][lp][2 spl]: B and C in fp32, zeros past n and past a length
   float* states;   // [b][nc][nblk spl][d]

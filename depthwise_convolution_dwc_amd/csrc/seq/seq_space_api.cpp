@@ -176,7 +176,7 @@ int scan_layout(ScanArgs* a, bool bwd, char* base, size_t* bytes) {
   const int64_t tokens = a->b * a->lp, rows = a->b * a->nc;
   const int64_t pairs = (a->dg + kGradChannels - 1) / kGradChannels;
   // threads of the widest launches, and the index range
-  if (tokens > kMost / (a->g * line) || tokens * a->g * line >= kLanes ||
+  if (tokens > kMost / (a->g * line) || tokens * a->g * line >= kLanes / 2 ||
       rows >= kLanes / 64 / ((int64_t)a->g * a->cblk * a->nblk) || a->b * np * ((a->d + 63) / 64) >= kLanes / 1024 ||
       (bwd && (rows >= kLanes / 256 / ((int64_t)a->g * pairs * a->nblk) ||
                (int64_t)a->n * a->d * 64 >= kLanes / 2 || rows >= kLanes / a->d)))
@@ -186,6 +186,7 @@ int scan_layout(ScanArgs* a, bool bwd, char* base, size_t* bytes) {
     *field = reinterpret_cast<float*>(base + at);
     at += ((size_t)floats * 4 + 255) & ~(size_t)255;
   };
+  take(&a->a2, np * a->d);
   take(&a->bc, tokens * a->g * line);
   if (a->nc > 1) {
     take(&a->states, rows * np * a->d);

@@ -85,6 +85,14 @@ def _token_strides(t, name):
     return s[:2]
 
 
+def _token_operand(t, name, dtypes, index, shape):
+    """Its strides, checked against the first operand."""
+    _device_tensor(t, name, dtypes, index)
+    if t.shape != shape:
+        raise ValueError(f"{name} and u disagree in shape")
+    return _token_strides(t, name)
+
+
 def _lengths(lengths, b, index):
     if lengths is not None:
         _device_tensor(lengths, "lengths", _I32, index)
@@ -209,41 +217,33 @@ def _scan(u, delta, A, B, C, D, z, delta_bias, s0, lengths, softplus, dy=None):
     if len(shape) != 3:
         raise ValueError("u must be b x l x d")
     b, n, d = shape
-    zs = ys = (0, 0)
-    for t, name in ((delta, "delta"), (z, "z"), (dy, "dy")):
-        if t is None and name != "delta":
-            continue
-        _device_tensor(t, name, dt, index)
-        if t.shape != shape:
-            raise ValueError(f"{name} and u disagree in shape")
+    ds = _token_operand(delta, "delta", dt, index, shape)
+    zs = _token_operand(z, "z", dt, index, shape) if z is not None else (0, 0)
+    ys = _token_operand(dy, "dy", dt, index, shape) if dy is not None else (0, 0)
     _device_tensor(A, "A", _F32, index)
     if A.dim() != 2:
         raise ValueError("A must be d x n")
     m = A.shape[1]
     _dense(A, "A", (d, m))
-    for t, name in ((B, "B"), (C, "C")):
-        _device_tensor(t, name, dt, index)
-        if t.dim() != 4:
-            raise ValueError(f"{name} must be b x l x g x n")
-    g = B.shape[2]
-    if B.shape != (b, n, g, m) or C.shape != B.shape:
+    _device_tensor(B, "B", dt, index)
+    _device_tensor(C, "C", dt, index)
+    bs = B.shape
+    if len(bs) != 4 or bs[0] != b or bs[1] != n or bs[3] != m or C.shape != bs:
         raise ValueError(f"B and C must be {(b, n, 'g', m)}")
-    for t, name in ((D, "D"), (delta_bias, "delta_bias")):
-        if t is not None:
-            _device_tensor(t, name, _F32, index)
-            _dense(t, name, (d,))
+    g = bs[2]
+    if D is not None:
+        _device_tensor(D, "D", _F32, index)
+        _dense(D, "D", (d,))
+    if delta_bias is not None:
+        _device_tensor(delta_bias, "delta_bias", _F32, index)
+        _dense(delta_bias, "delta_bias", (d,))
     states = (b, d, m)
     if s0 is not None:
         _device_tensor(s0, "s0", _F32, index)
         _dense(s0, "s0", states)
     _lengths(lengths, b, index)
-    if z is not None:
-        zs = _token_strides(z, "z")
-    if dy is not None:
-        ys = _token_strides(dy, "dy")
-    p = _SCAN(b, n, *_token_strides(u, "u"), *_token_strides(delta, "delta"), *zs, *ys,
-              *_strides(B, "B"), *_strides(C, "C"), d, m, g, _DTYPE_CODE[u.dtype],
-              int(bool(softplus)), 0)
+    p = _SCAN(b, n, *_token_strides(u, "u"), *ds, *zs, *ys, *_strides(B, "B"),
+              *_strides(C, "C"), d, m, g, _DTYPE_CODE[u.dtype], int(bool(softplus)), 0)
     return p, index, states
 
 
@@ -332,6 +332,14 @@ def selective_scan_bwd(dy: torch.Tensor, ds1: Optional[torch.Tensor], u: torch.T
 
 # ----------------------------------------------------------------- residual norm ----
 
+def _row_operand(t, name, dtypes, index, shape):
+    """Its row stride, checked against the block's output."""
+    _device_tensor(t, name, dtypes, index)
+    if t.shape != shape:
+        raise ValueError(f"{name} and y disagree in shape")
+    return _row_stride(t, name)
+
+
 def _resnorm(x, y, gate, scale, w_post, w_pre, post, pre, act, eps, dr=None, dh=None):
     """(the problem's bytes, device index)"""
     index = _device_tensor(y, "y", _TYPES)
@@ -342,16 +350,12 @@ def _resnorm(x, y, gate, scale, w_post, w_pre, post, pre, act, eps, dr=None, dh=
     xt = y.dtype if x is None else x.dtype
     if dr is not None and x is None:
         xt = dr.dtype
-    strides = []
-    for t, name, types in ((x, "x", (torch.float32, y.dtype)), (y, "y", _TYPES),
-                           (gate, "gate", (y.dtype,)), (dr, "dr", (xt,)), (dh, "dh", (y.dtype,))):
-        if t is None:
-            strides.append(c)
-            continue
-        _device_tensor(t, name, types, index)
-        if t.shape != shape:
-            raise ValueError(f"{name} and y disagree in shape")
-        strides.append(_row_stride(t, name))
+    yt = (y.dtype,)
+    strides = (_row_operand(x, "x", (torch.float32, y.dtype), index, shape) if x is not None else c,
+               _row_stride(y, "y"),
+               _row_operand(gate, "gate", yt, index, shape) if gate is not None else c,
+               _row_operand(dr, "dr", (xt,), index, shape) if dr is not None else c,
+               _row_operand(dh, "dh", yt, index, shape) if dh is not None else c)
     wt = None
     for t, name in ((scale, "scale"), (w_post, "w_post"), (w_pre, "w_pre")):
         if t is not None:
@@ -386,7 +390,9 @@ def residual_norm(x: Optional[torch.Tensor], y: torch.Tensor,
         r = torch.empty_like(y if x is None else x, memory_format=_DENSE)
         h = torch.empty_like(y, memory_format=_DENSE) if pre else None
         q1 = y.new_empty(y.shape[:-1], dtype=torch.float32) if post else None
-        q2 = y.new_empty(y.shape[:-1], dtype=torch.float32) if pre else None
+        q2 = None
+        if pre:
+            q2 = torch.empty_like(q1) if post else y.new_empty(y.shape[:-1], dtype=torch.float32)
         _raise(lib().dwc_residual_norm(p, _ptr(x), y.data_ptr(), _ptr(gate), _ptr(scale),
                                        _ptr(w_post), _ptr(w_pre), r.data_ptr(), _ptr(h), _ptr(q1),
                                        _ptr(q2), _raw(index)))
