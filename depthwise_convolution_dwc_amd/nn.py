@@ -638,7 +638,11 @@ class SelectiveScanMixer(torch.nn.Module):
         delta = self.w_dt(mixed[..., :self.rank])
         B = mixed[..., self.rank:self.rank + g * n].unflatten(-1, (g, n))
         C = mixed[..., self.rank + g * n:].unflatten(-1, (g, n))
-        return delta, -torch.exp(self.a), B, C
+        return delta, -torch.exp(self.a.float()), B, C
+
+    def _vectors(self):
+        """D and the steps' bias, fp32 also in a module converted as a whole."""
+        return self.D.float(), self.delta_bias.float()
 
     def forward(self, h: torch.Tensor, state: Optional[ScanState] = None,
                 lengths: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, ScanState]:
@@ -650,8 +654,9 @@ class SelectiveScanMixer(torch.nn.Module):
         taps, states = state if state is not None else (None, None)
         u, taps = causal_conv(xz[..., :self.inner], self.conv_weight, self.conv_bias, taps,
                               lengths, "silu")
-        y, states = selective_scan(u, *self._operands(u), self.D, xz[..., self.inner:],
-                                   self.delta_bias, states, lengths, softplus=True)
+        D, bias = self._vectors()
+        y, states = selective_scan(u, *self._operands(u), D, xz[..., self.inner:], bias, states,
+                                   lengths, softplus=True)
         return self.w_out(y), ScanState(taps, states)
 
     @torch.no_grad()
@@ -661,9 +666,9 @@ class SelectiveScanMixer(torch.nn.Module):
         xz = self.w_in(h)
         u, _ = space.causal_conv_step(xz[..., :self.inner], self.conv_weight, self.conv_bias,
                                       state.taps, act="silu", out_state=state.taps)
-        y, _ = space.selective_scan_step(u, *self._operands(u), self.D, xz[..., self.inner:],
-                                         self.delta_bias, state.states, softplus=True,
-                                         out_state=state.states)
+        D, bias = self._vectors()
+        y, _ = space.selective_scan_step(u, *self._operands(u), D, xz[..., self.inner:], bias,
+                                         state.states, softplus=True, out_state=state.states)
         return self.w_out(y)
 
     def extra_repr(self) -> str:
