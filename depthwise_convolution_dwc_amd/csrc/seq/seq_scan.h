@@ -57,6 +57,13 @@ constexpr int b_at(int s) { return BWD ? s / 4 * 8 + s % 4 : s; }
 template <int SPL, bool BWD>
 constexpr int c_at(int s) { return BWD ? s / 4 * 8 + 4 + s % 4 : SPL + s; }
 
+// A in units of the decays' exp2.  Infinities become the largest values: a
+// token that is not there has a step of 0, and 0 times infinity would be NaN.
+__device__ __forceinline__ float rate_of(float a) {
+  const float v = kLog2e * a;
+  return fabsf(v) == __builtin_inff() ? copysignf(__FLT_MAX__, v) : v;
+}
+
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
 __device__ __forceinline__ float sigmoid(float x) {

@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(256) scan_prep(ScanArgs a) {
   i -= rows * lp * w;
   const uint32_t s = i / (uint32_t)a.d, c = i - s * (uint32_t)a.d;
   if (s < (uint32_t)(a.nblk * a.spl))
-    a.a2[i] = s < (uint32_t)a.n ? kLog2e * a.a[(int64_t)c * a.n + s] : 0.f;
+    a.a2[i] = s < (uint32_t)a.n ? rate_of(a.a[(int64_t)c * a.n + s]) : 0.f;
 }
 
 // What a workgroup works on.

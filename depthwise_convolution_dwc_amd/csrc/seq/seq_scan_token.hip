@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(256) scan_token(ScanArgs a) {
   load_four<T_F32, WIDE>(a.a, (int64_t)c * a.n + s0, left, a2);
   const float bias = a.bias ? a.bias[c] : 0.f, skip = a.skip ? a.skip[c] : 0.f;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) a2[j] *= kLog2e;
+  for (int j = 0; j < 4; ++j) a2[j] = rate_of(a2[j]);
   for (int64_t t = 0; t < a.l; ++t) {
     float y = 0.f;
     if (t < len) {

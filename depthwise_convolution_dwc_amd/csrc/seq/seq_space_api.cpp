@@ -177,7 +177,9 @@ int scan_layout(ScanArgs* a, bool bwd, char* base, size_t* bytes) {
   const int64_t pairs = (a->dg + kGradChannels - 1) / kGradChannels;
   // threads of the widest launches, and the index range
   if (tokens > kMost / (a->g * line) || tokens * a->g * line >= kLanes / 2 ||
-      rows >= kLanes / 64 / ((int64_t)a->g * a->cblk * a->nblk) || a->b * np * ((a->d + 63) / 64) >= kLanes / 1024 ||
+      rows >= kLanes / 64 / ((int64_t)a->g * a->cblk * a->nblk) ||
+      (a->nc > 1 && a->b * np * ((a->d + 63) / 64) >= kLanes / 128) ||
+      (a->one && a->b * a->g * a->cblk >= kLanes / 1024) ||
       (bwd && (rows >= kLanes / 256 / ((int64_t)a->g * pairs * a->nblk) ||
                (int64_t)a->n * a->d * 64 >= kLanes / 2 || rows >= kLanes / a->d)))
     return fail(DWC_ERR_UNSUPPORTED, "scan sizes past the launch range");
@@ -553,6 +555,7 @@ int dwc_residual_norm_bwd(const dwc_resnorm_problem* p, const void* dr, const vo
   a.dy = dy;
   a.dgate = dgate;
   a.part = (float*)workspace;
+  a.pre = p->pre && dh;  // (else nothing of that norm is read)
   a.groups = resnorm_groups(a, resnorm_shape(a, true), true);
   return hip_result(launch_resnorm_bwd(a, dscale, dw_post, dw_pre, (hipStream_t)stream),
                     "dwc_residual_norm_bwd launch");

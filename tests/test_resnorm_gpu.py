@@ -230,3 +230,17 @@ def test_refusals():
             dwc.residual_norm_bwd(*args, **kw)
     with pytest.raises(TypeError):
         dwc.residual_norm_bwd(x, x, x, x, None, q2)
+
+
+@pytest.mark.parametrize("c", [64, 777, 9000])
+def test_gradients_of_the_sum_alone(c):
+    """Without a gradient of h its norm's values are not needed."""
+    log(f"case residual norm without dh, {c}")
+    x, y, dr = (randn(30 + i, 5, c) for i in range(3))
+    w = randn(33, c)
+    r, h, q1, q2 = dwc.residual_norm(x, y, w_post=w, w_pre=w)
+    want = dwc.residual_norm_bwd(dr, torch.zeros_like(dr), x, y, q1, q2, w_post=w, w_pre=w)
+    for q in (q2, None):
+        got = dwc.residual_norm_bwd(dr, None, x, y, q1, q, w_post=w, w_pre=w)
+        for s, t in zip(got, want):
+            assert s is t is None or (s == t).all()

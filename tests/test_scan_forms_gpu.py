@@ -87,3 +87,27 @@ def test_gradients_alone_of_broadcast_sequences():
     for name, s, t in zip(NAMES[2:], got, one):
         if t.dim() > 2 and name != "dA":
             assert (s == t).all(), name
+
+
+@pytest.mark.parametrize("b,l,d,n", [(2, 150, 70, 16), (1, 600, 20, 5), (3, 40, 66, 33), (1, 600, 9, 70)])
+def test_infinite_rates(b, l, d, n):
+    """States whose decay is 0 at every token, sequences that end inside a
+    stage, an eight and a chunk."""
+    log(f"case scan with infinite rates {b} {l} {d} {n}")
+    a = inputs(23, b, l, d, n, 1, F32)
+    lens = [l - 3 - 8 * i for i in range(b)]
+    lengths = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    dy, ds1 = randn(24, b, l, d), randn(25, b, d, n)
+    a[2][:, n // 2] = -1e30  # exp(dt A) is 0 in 64 bits too
+    ref = reference(a, lens, True)
+    large = dwc.selective_scan(*a, lengths=lengths, softplus=True)
+    for name, got in zip(("y", "s1"), large):
+        check(name, got, ref[name])
+    large += dwc.selective_scan_bwd(dy, ds1, *a, lengths=lengths, softplus=True)
+    large += dwc.selective_scan_step(*a, lengths=lengths, softplus=True)
+    a[2][:, n // 2] = -float("inf")
+    got = dwc.selective_scan(*a, lengths=lengths, softplus=True)
+    got += dwc.selective_scan_bwd(dy, ds1, *a, lengths=lengths, softplus=True)
+    got += dwc.selective_scan_step(*a, lengths=lengths, softplus=True)
+    for s, t in zip(got, large):
+        assert torch.isfinite(s).all() and (s == t).all()
