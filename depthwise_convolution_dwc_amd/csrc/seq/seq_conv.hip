@@ -10,7 +10,8 @@
 // Bound: memory (2 K + 8 operations an element).  A lane owns VEC channels of
 // a strip of tokens and keeps the K - 1 inputs behind the current one in
 // registers, so x is read once but for the K - 1 tokens before each strip
-// (from the caches: a neighbour reads them too).
+// (from the caches: a neighbour reads them too).  8 sequences of 2048 tokens of
+// 2048 channels, bf16, 4 taps: 31 us (4.3 TB/s), back 46 us (4.4 TB/s).
 #include "seq_device.h"
 #include "seq_space.h"
 
@@ -384,7 +385,9 @@ static void launch(bool bwd, const ConvArgs& a, hipStream_t st) {
 }  // namespace conv
 
 int conv_strip(const ConvArgs& a, bool bwd) {
-  // lanes for 8 waves a compute unit, in strips of 8 to 32 tokens
+  // lanes for 8 waves a compute unit, in strips of 8 to 32 tokens (8 sequences
+  // of 2048 tokens of 2048 channels, both ways: 82 us in strips of 32, 92 of 16,
+  // 89 of 64, 90 of 128)
   const int64_t per = (a.d + 3) / 4 * a.b;
   int strip = 32;
   while (strip > 8 && per * ((a.l + strip - 1) / strip) < (int64_t)256 * 8 * 64) strip /= 2;

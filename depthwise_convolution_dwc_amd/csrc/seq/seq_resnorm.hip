@@ -13,6 +13,9 @@
 // without its rounding.
 //
 // Bound: memory.  A row is read once into registers; LPR lanes share it.
+// 16384 rows of 2048, fp32 stream and bf16 blocks: 70 us (5.7 TB/s), back 120 us
+// (5.0 TB/s) and 6 for the sums over the rows.  (Back, the next row read while
+// this one is worked on: 225 us for both ways, then 203, for the registers.)
 #include "seq_device.h"
 #include "seq_space.h"
 

@@ -2,18 +2,24 @@
 // many sequences or channels and for short sequences.
 //
 // A workgroup takes 64 channels of a sequence, a wave two or four of the
-// states with a channel a lane.  Stages of 16 tokens: the waves share out the tokens'
-// steps, inputs and gates (tokens w, w + NW, ...), all run the stage on their
-// own states, and join the parts of C . h in LDS, where each finishes its own
-// tokens.  B and C go through LDS too, a stage ahead: there are few waves to
+// states with a channel a lane.  Stages of 16 tokens: the waves share out the
+// tokens' steps, inputs and gates (tokens w, w + NW, ...), all run the stage on
+// their own states, and join the parts of C . h in LDS, where each finishes its
+// own tokens.  B and C go through LDS too, a stage ahead: there are few waves to
 // wait for the scalar cache.
 //
 // A decay near 1 loses what is below 2^-24, and a product of many loses that
 // much each time (16 states, 491 tokens: the last state off by 8e-7 of its
-// norm, now by 2e-7).  So a second state starts from zero every 64 tokens and the first one
-// is made again from it there, with one decay for the sum of their steps; that
-// is one of six instructions, and 5 to 10% of the time.  A state takes its exp and four
-// other instructions once, not twice as in chunks; bound: the vector units.
+// norm).  So a second state starts from zero every 64 tokens and the first one
+// is made again from it there, with one decay for the sum of their steps: 1.4e-7,
+// for 5 to 10% of the time.
+//
+// Bound: the vector units, of which a state of a token takes an exp and five
+// other instructions once, not twice as in chunks.  8 sequences of 2048 tokens
+// of 2048 channels and 16 states: 250 us, the vector units 66% busy at the two
+// waves a SIMD that there are.  (One barrier a stage, with the outputs of the
+// stage before and the steps of the next one among the tokens: 1% less there,
+// 2 to 7% more for 32 sequences and up, where its LDS leaves fewer waves.)
 #include "seq_scan.h"
 
 namespace dwc {
