@@ -458,7 +458,7 @@ static bool one_pass(const ScanArgs& a) {
   if (a.n > 64) return false;
   const int blocks = (a.n + 15) / 16;
   const double groups = (double)(a.b * a.g * a.cblk);
-  const double kOne = a.n <= 16 ? 0.106 : (a.n <= 32 ? 0.146 : 0.22);
+  const double kOne = a.n <= 16 ? 0.106 : (a.n <= 24 ? 0.13 : (a.n <= 32 ? 0.146 : 0.22));
   const double kMore = 0.0003 * blocks;
   const double kTwo = 0.00043 * (blocks == 1 ? 1 : 1 + blocks), kFixed = 40.0;
   const double token = kMore * groups > kOne ? kMore * groups : kOne;

@@ -32,9 +32,9 @@ template <int T, int NW, int S, bool GATE>
 __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
   constexpr int NT = kStage / NW, SPL = 16;  // tokens a wave shares; states a line of bc
   constexpr int ROW = 2 * S * NW;            // B and C of all states
-  __shared__ float of[2][kStage][64];        // dt, u
+  __shared__ f32x2 of[kStage][64];           // dt, dt u
   __shared__ float parts[kStage][NW][64];    // of C . h
-  __shared__ __align__(16) float rows[2][kStage][ROW];  // four states' B and their C in turn
+  __shared__ __align__(16) float rows[2][kStage][ROW];  // a wave's B and its C in turn
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   uint32_t i = blockIdx.x;
   const int block = (int)(i % (uint32_t)a.cblk);
@@ -47,6 +47,7 @@ __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
   const bool on = (int)c0 < a.dg;
   const uint32_t in = on ? c0 : 0;  // (lanes past the end repeat the first channel)
   const int n0 = S * wave;
+  const bool mine = n0 < a.n;  // (the same in a wave; the others leave zeros)
   float a2[S], h[S], start[S], from[S], sum = 0.f;  // from: from zero, start: at that time
   const auto states = [&](const float* p, float(&v)[S]) {  // of d x n
 #pragma unroll
@@ -74,6 +75,9 @@ __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
   const bool some = of16 < a.nblk;
   const float* bc = a.bc + (((b * a.g + g) * a.nblk + (some ? of16 : 0)) * a.lp + row) * (2 * SPL) +
                     at_row % 32;
+  // in LDS a wave's B and C stand together
+  const int to_row = S == 4 ? at_row
+                            : at_row / 8 * 8 + at_row % 4 / 2 * 4 + at_row % 8 / 4 * 2 + at_row % 2;
   float bc_next[PER];
   // the wave's tokens of the next stage: next[] is the address of the first
   constexpr int N = GATE ? 3 : 2;
@@ -113,9 +117,13 @@ __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
   };
   const auto keep = [&](int side) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) rows[side][row][at_row + i] = some ? bc_next[i] : 0.f;
+    for (int i = 0; i < PER; ++i) rows[side][row][to_row + i] = some ? bc_next[i] : 0.f;
   };
   Elem<T>* const out = (Elem<T>*)a.y + (b * a.l * a.d + g0);
+  if (!mine) {
+#pragma unroll
+    for (int j = 0; j < kStage; ++j) parts[j][wave][lane] = 0.f;
+  }
   if (len > 0) {
     fetch_rows(0);
     fetch(0, even);
@@ -133,64 +141,65 @@ __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
       u[j] = value<T>(raw[0][j]);
       const float dt = step_of(a.softplus, value<T>(raw[1][j]) + bias);
       if constexpr (GATE) gate[j] = raw[GATE ? 2 : 0][j];
-      of[0][at][lane] = live ? dt : 0.f;
-      of[1][at][lane] = live ? u[j] : 0.f;
+      of[at][lane] = live ? f32x2{dt, dt * u[j]} : f32x2{0.f, 0.f};
     }
     __syncthreads();
     // (the rows first: they are waited for first, a stage before the rest)
     if (t0 + kStage < len) fetch_rows(t0 + kStage);
     fetch(t0 + 2 * kStage, raw);
-    // LDS is read two tokens ahead and the decays are made one ahead: a SIMD
-    // may have no other wave to fill the wait
-    float bb[3][S], cc[3][S], dt[3], du[3], k[2][S];
-    const int b_at = 8 * (n0 / 4) + n0 % 4, c_at = b_at + 4;
-    const auto read = [&](int j) {
+    if (mine) {
+      // LDS is read two tokens ahead and the decays are made one ahead: a SIMD
+      // may have no other wave to fill the wait
+      float bb[3][S], cc[3][S], dt[3], du[3], k[2][S];
+      const int b_at = 2 * n0, c_at = b_at + S;
+      const auto read = [&](int j) {
 #pragma unroll
-      for (int s = 0; s < S; ++s) {
-        bb[j % 3][s] = rows[side][j][b_at + s];
-        cc[j % 3][s] = rows[side][j][c_at + s];
+        for (int s = 0; s < S; ++s) {
+          bb[j % 3][s] = rows[side][j][b_at + s];
+          cc[j % 3][s] = rows[side][j][c_at + s];
+        }
+        const f32x2 x = of[j][lane];
+        dt[j % 3] = x[0];
+        du[j % 3] = x[1];
+      };
+      const auto decays = [&](int j) {
+#pragma unroll
+        for (int s = 0; s < S; ++s) k[j % 2][s] = exp2_of(dt[j % 3] * a2[s]);
+      };
+      read(0);
+      read(1);
+      decays(0);
+      float steps = 0.f;
+#pragma unroll
+      for (int j = 0; j < kStage; ++j) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (j + 2 < kStage) read(j + 2);
+        if (j + 1 < kStage) decays(j + 1);
+        float y = 0.f;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+          const float x = du[j % 3] * bb[j % 3][s];
+          h[s] = fmaf(k[j % 2][s], h[s], x);
+          from[s] = fmaf(k[j % 2][s], from[s], x);
+          y = fmaf(cc[j % 3][s], h[s], y);
+        }
+        steps += dt[j % 3];
+        // (nothing reads these before the end: without this all 16 steps of them
+        // are put off to there, their operands held in registers)
+#pragma unroll
+        for (int s = 0; s < S; ++s) asm volatile("" : "+v"(from[s]));
+        asm volatile("" : "+v"(steps));
+        parts[j][wave][lane] = y;
       }
-      dt[j % 3] = of[0][j][lane];
-      du[j % 3] = of[1][j][lane];
-    };
-    const auto decays = [&](int j) {
-      du[j % 3] *= dt[j % 3];
+      sum += steps;
+      if (t0 / kStage % kAgain == kAgain - 1) {
 #pragma unroll
-      for (int s = 0; s < S; ++s) k[j % 2][s] = exp2_of(dt[j % 3] * a2[s]);
-    };
-    read(0);
-    read(1);
-    decays(0);
-    float steps = 0.f;
-#pragma unroll
-    for (int j = 0; j < kStage; ++j) {
-      __builtin_amdgcn_sched_barrier(0);
-      if (j + 2 < kStage) read(j + 2);
-      if (j + 1 < kStage) decays(j + 1);
-      float y = 0.f;
-#pragma unroll
-      for (int s = 0; s < S; ++s) {
-        const float x = du[j % 3] * bb[j % 3][s];
-        h[s] = fmaf(k[j % 2][s], h[s], x);
-        from[s] = fmaf(k[j % 2][s], from[s], x);
-        y = fmaf(cc[j % 3][s], h[s], y);
+        for (int s = 0; s < S; ++s) {
+          h[s] = start[s] = fmaf(exp2_of(a2[s] * sum), start[s], from[s]);
+          from[s] = 0.f;
+        }
+        sum = 0.f;
       }
-      steps += dt[j % 3];
-      // (nothing reads these before the end: without this all 16 steps of them
-      // are put off to there, their operands held in registers)
-#pragma unroll
-      for (int s = 0; s < S; ++s) asm volatile("" : "+v"(from[s]));
-      asm volatile("" : "+v"(steps));
-      parts[j][wave][lane] = y;
-    }
-    sum += steps;
-    if (t0 / kStage % kAgain == kAgain - 1) {
-#pragma unroll
-      for (int s = 0; s < S; ++s) {
-        h[s] = start[s] = fmaf(exp2_of(a2[s] * sum), start[s], from[s]);
-        from[s] = 0.f;
-      }
-      sum = 0.f;
     }
     if (t0 + kStage < len) keep(side ^ 1);
     __syncthreads();
@@ -236,7 +245,11 @@ void go_wide(const ScanArgs& a, hipStream_t st) {
   if (a.n <= 16)
     return a.b * a.g * a.cblk <= 256 ? go_shape<T, 8, 2, GATE>(a, st)
                                      : go_shape<T, 4, 4, GATE>(a, st);
-  if (a.n <= 32) return go_shape<T, 8, 4, GATE>(a, st);
+  // (up to 24 states twos load the SIMDs more evenly: 5 sequences of 333 tokens
+  // of 600 channels, 20 states: 47 and 58 us, 28 states 62 and 59)
+  if (a.n <= 32)
+    return a.n <= 24 && a.b * a.g * a.cblk <= 256 ? go_shape<T, 16, 2, GATE>(a, st)
+                                                  : go_shape<T, 8, 4, GATE>(a, st);
   go_shape<T, 16, 4, GATE>(a, st);
 }
 
