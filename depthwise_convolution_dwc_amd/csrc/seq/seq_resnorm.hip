@@ -438,8 +438,15 @@ int resnorm_groups(const ResNormArgs& a, const ResNormShape& s, bool bwd) {
   if (s.lpr == 0) return (int)(a.rows < 64 ? (a.rows > 0 ? a.rows : 1) : 64);
   const int64_t per = s.lpr <= 64 ? kBlock / s.lpr : 1;
   // (the backward pass leaves a row of partial sums each)
-  const int64_t most = (s.lpr <= 256 ? 1024 : 256) * (bwd ? 1 : 2);
+  int64_t most = (s.lpr <= 256 ? 1024 : 256) * (bwd ? 1 : 2);
   const int64_t need = (a.rows + per - 1) / per;
+  if (s.vec == 1 && s.lpr == 256 && need > 0) {
+    // as many as are resident, with the same number of rows each (3333 rows of
+    // 771: 16 and 33 us, 18 and 37 by the rule above; a wave a row does not gain)
+    most = bwd ? 1280 : 1792;
+    const int64_t rounds = (need + most - 1) / most;
+    most = (need + rounds - 1) / rounds;
+  }
   return (int)(need < 1 ? 1 : (need < most ? need : most));
 }
 
