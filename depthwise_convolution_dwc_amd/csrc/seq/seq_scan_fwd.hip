@@ -448,17 +448,22 @@ void prepare_bwd(const ScanArgs& a, hipStream_t st) {
 }  // namespace scan
 
 // Whether one pass over all tokens is done before the chunks' three.  It takes
-// kOne a token while its workgroups (64 channels each) have SIMDs to
-// themselves, then kMore a token and workgroup; the chunks take kTwo a token
-// and workgroup and kFixed besides, for their launches and the states between
-// them.  bf16, us: 256 tokens of 2048 channels, 16 states: 34 and 51 in chunks;
-// 1024 tokens: 110 and 54; 16 sequences of 2048 tokens: 361 and 501; 32 states,
-// 4 sequences of 700 tokens of 512 channels: 112 and 70, 16 such: 117 and 160.
+// one token's time (by the shape of its workgroups, see go_wide) while these
+// have SIMDs to themselves, then kMore a token and 64 channels; the chunks take
+// kTwo a token and 64 channels and kFixed besides, for their launches and the
+// states between them.  bf16, us: 512 tokens of 2048 channels, 16 states: 51
+// and 48 in chunks, 1024 tokens: 96 and 50; 4 sequences of 1024 tokens: both
+// 100, 16 of 2048: 361 and 501; 32 states, 700 tokens of 512 channels, 4
+// sequences: 62 and 68, 16: 83 and 160; 64 states, 4 such: 86 and 82, one of 256
+// channels: 82 and 48.
 static bool one_pass(const ScanArgs& a) {
   if (a.n > 64) return false;
   const int blocks = (a.n + 15) / 16;
   const double groups = (double)(a.b * a.g * a.cblk);
-  const double kOne = a.n <= 16 ? 0.106 : (a.n <= 24 ? 0.13 : (a.n <= 32 ? 0.146 : 0.22));
+  const int size = groups <= 64 ? 0 : (groups <= 128 ? 1 : 2);
+  constexpr double kOnes[4][3] = {
+      {0.092, 0.092, 0.106}, {0.083, 0.107, 0.13}, {0.083, 0.107, 0.146}, {0.118, 0.157, 0.22}};
+  const double kOne = kOnes[a.n <= 16 ? 0 : (a.n <= 24 ? 1 : (a.n <= 32 ? 2 : 3))][size];
   const double kMore = 0.0003 * blocks;
   const double kTwo = 0.00043 * (blocks == 1 ? 1 : 1 + blocks), kFixed = 40.0;
   const double token = kMore * groups > kOne ? kMore * groups : kOne;

@@ -1,8 +1,8 @@
 // seq_scan_wide.hip -- the selective scan in one pass over the tokens, for
 // many sequences or channels and for short sequences.
 //
-// A workgroup takes 64 channels of a sequence, a wave two or four of the
-// states with a channel a lane.  Stages of 16 tokens: the waves share out the
+// A workgroup takes 64 / Q channels of a sequence, a wave Q times two or four of
+// the states with a channel a lane.  Stages of 16 tokens: the waves share out the
 // tokens' steps, inputs and gates (tokens w, w + NW, ...), all run the stage on
 // their own states, and join the parts of C . h in LDS, where each finishes its
 // own tokens.  B and C go through LDS too, a stage ahead: there are few waves to
@@ -28,26 +28,29 @@ namespace scan {
 
 constexpr int kStage = 16, kAgain = 4;  // tokens; stages until the states are made again
 
-template <int T, int NW, int S, bool GATE>
+template <int T, int NW, int S, bool GATE, int Q>
 __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
-  constexpr int NT = kStage / NW, SPL = 16;  // tokens a wave shares; states a line of bc
-  constexpr int ROW = 2 * S * NW;            // B and C of all states
-  __shared__ f32x2 of[kStage][64];           // dt, dt u
-  __shared__ float parts[kStage][NW][64];    // of C . h
+  constexpr int CH = 64 / Q, SPL = 16;  // channels; states a line of bc
+  constexpr int NT = kStage / (NW * Q);  // tokens a lane shares
+  constexpr int ROW = 2 * S * NW * Q;    // B and C of all states
+  __shared__ f32x2 of[kStage][CH];       // dt, dt u
+  __shared__ float parts[kStage][NW][64];  // of C . h
   __shared__ __align__(16) float rows[2][kStage][ROW];  // a wave's B and its C in turn
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   uint32_t i = blockIdx.x;
-  const int block = (int)(i % (uint32_t)a.cblk);
-  i /= (uint32_t)a.cblk;
+  const uint32_t blocks = Q == 1 ? (uint32_t)a.cblk : (uint32_t)((a.dg + CH - 1) / CH);
+  const int block = (int)(i % blocks);
+  i /= blocks;
   const int g = (int)(i % (uint32_t)a.g);
   const int64_t b = i / (uint32_t)a.g;
   const int len = (int)length_of(a, b);
   const int64_t g0 = (int64_t)g * a.dg;
-  const uint32_t c0 = (uint32_t)(block * 64 + lane);
+  const int ch = lane % CH, q = Q == 1 ? 0 : lane / CH;
+  const uint32_t c0 = (uint32_t)(block * CH + ch);
   const bool on = (int)c0 < a.dg;
   const uint32_t in = on ? c0 : 0;  // (lanes past the end repeat the first channel)
-  const int n0 = S * wave;
-  const bool mine = n0 < a.n;  // (the same in a wave; the others leave zeros)
+  const int n0 = S * (Q * wave + q);
+  const bool mine = S * Q * wave < a.n;  // (the same in a wave; the others leave zeros)
   float a2[S], h[S], start[S], from[S], sum = 0.f;  // from: from zero, start: at that time
   const auto states = [&](const float* p, float(&v)[S]) {  // of d x n
 #pragma unroll
@@ -68,24 +71,27 @@ __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
     from[s] = 0.f;
   }
   const float bias = a.bias ? (a.bias + g0)[in] : 0.f, skip = a.skip ? (a.skip + g0)[in] : 0.f;
-  // B and C of a stage: S / 2 values a thread; rows up to a multiple of the
+  // B and C of a stage: S Q / 2 values a thread; rows up to a multiple of the
   // stage are there, but for blocks of 16 states past the last
-  constexpr int PER = S / 2, ACROSS = ROW / PER;
+  constexpr int PER = S * Q / 2, ACROSS = ROW / PER;
   const int row = threadIdx.x / ACROSS, at_row = PER * (threadIdx.x % ACROSS), of16 = at_row / 32;
   const bool some = of16 < a.nblk;
   const float* bc = a.bc + (((b * a.g + g) * a.nblk + (some ? of16 : 0)) * a.lp + row) * (2 * SPL) +
                     at_row % 32;
   // in LDS a wave's B and C stand together
-  const int to_row = S == 4 ? at_row
-                            : at_row / 8 * 8 + at_row % 4 / 2 * 4 + at_row % 8 / 4 * 2 + at_row % 2;
+  const auto to_row = [](int i) {
+    return S == 4 ? i : i / 8 * 8 + i % 4 / 2 * 4 + i % 8 / 4 * 2 + i % 2;
+  };
   float bc_next[PER];
-  // the wave's tokens of the next stage: next[] is the address of the first
+  // the lane's tokens of a stage, and the address of the first of the next
+  // stage's, but for q tokens
+  const auto token = [&](int j) { return (j * NW + wave) * Q + q; };
   constexpr int N = GATE ? 3 : 2;
   const char* next[N];
-  int64_t step[N];  // NW tokens
+  int64_t one[N];  // bytes between tokens
   const auto set = [&](int k, const void* p, const int64_t(&stride)[2]) {
-    next[k] = (const char*)((const Elem<T>*)p + (b * stride[0] + wave * stride[1] + g0));
-    step[k] = NW * stride[1] * (int64_t)sizeof(Elem<T>);
+    next[k] = (const char*)((const Elem<T>*)p + (b * stride[0] + wave * Q * stride[1] + g0));
+    one[k] = stride[1] * (int64_t)sizeof(Elem<T>);
   };
   set(0, a.u, a.u_stride);
   set(1, a.delta, a.delta_stride);
@@ -98,16 +104,16 @@ __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-          raw[k][j] = ((const Elem<T>*)next[k])[in];
-          next[k] += step[k];
+          raw[k][j] = ((const Elem<T>*)(next[k] + q * one[k]))[in];
+          next[k] += NW * Q * one[k];
         }
     } else {  // a token past the last one is read as the last
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        const int t = t0 + j * NW + wave, back = t < len ? 0 : t - (len - 1);
+        const int t = t0 + token(j), back = t < len ? 0 : t - (len - 1);
 #pragma unroll
         for (int k = 0; k < N; ++k)
-          raw[k][j] = ((const Elem<T>*)(next[k] + j * step[k] - back * (step[k] / NW)))[in];
+          raw[k][j] = ((const Elem<T>*)(next[k] + (j * NW * Q + q - back) * one[k]))[in];
       }
     }
   };
@@ -117,7 +123,7 @@ __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
   };
   const auto keep = [&](int side) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) rows[side][row][to_row + i] = some ? bc_next[i] : 0.f;
+    for (int i = 0; i < PER; ++i) rows[side][row][to_row(at_row + i)] = some ? bc_next[i] : 0.f;
   };
   Elem<T>* const out = (Elem<T>*)a.y + (b * a.l * a.d + g0);
   if (!mine) {
@@ -136,12 +142,12 @@ __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
     float u[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      const int at = j * NW + wave;
+      const int at = token(j);
       const bool live = t0 + at < len;
       u[j] = value<T>(raw[0][j]);
       const float dt = step_of(a.softplus, value<T>(raw[1][j]) + bias);
       if constexpr (GATE) gate[j] = raw[GATE ? 2 : 0][j];
-      of[at][lane] = live ? f32x2{dt, dt * u[j]} : f32x2{0.f, 0.f};
+      of[at][ch] = live ? f32x2{dt, dt * u[j]} : f32x2{0.f, 0.f};
     }
     __syncthreads();
     // (the rows first: they are waited for first, a stage before the rest)
@@ -158,7 +164,7 @@ __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
           bb[j % 3][s] = rows[side][j][b_at + s];
           cc[j % 3][s] = rows[side][j][c_at + s];
         }
-        const f32x2 x = of[j][lane];
+        const f32x2 x = of[j][ch];
         dt[j % 3] = x[0];
         du[j % 3] = x[1];
       };
@@ -205,10 +211,12 @@ __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      const int at = j * NW + wave;
+      const int at = token(j);
       float y = 0.f;
 #pragma unroll
-      for (int k = 0; k < NW; ++k) y += parts[at][k][lane];
+      for (int k = 0; k < NW; ++k)
+#pragma unroll
+        for (int e = 0; e < Q; ++e) y += parts[at][k][e * CH + ch];
       y = fmaf(skip, u[j], y);
       if constexpr (GATE) {
         const float z = value<T>(gate[j]);
@@ -221,7 +229,7 @@ __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
     stage(t0, 0, even);
     if (t0 + kStage < len) stage(t0 + kStage, 1, odd);
   }
-  for (int64_t t = len + wave; t < a.l; t += NW)
+  for (int64_t t = len + token(0); t < a.l; t += NW * Q)
     if (on) store1<T>(out + t * a.d, in, 0.f);
   float* const s1 = a.s1 + (b * a.d + g0) * a.n;
 #pragma unroll
@@ -230,26 +238,36 @@ __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
       (s1 + n0 + s)[in * (uint32_t)a.n] = fmaf(exp2_of(a2[s] * sum), start[s], from[s]);
 }
 
-template <int T, int NW, int S, bool GATE>
+template <int T, int NW, int S, bool GATE, int Q = 1>
 void go_shape(const ScanArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((scan_wide<T, NW, S, GATE>), dim3((uint32_t)(a.b * a.g * a.cblk)),
+  const int64_t blocks = (a.dg + 64 / Q - 1) / (64 / Q);
+  hipLaunchKernelGGL((scan_wide<T, NW, S, GATE, Q>), dim3((uint32_t)(a.b * a.g * blocks)),
                      dim3(64 * NW), 0, st, a);
 }
 
 template <int T, bool GATE>
 void go_wide(const ScanArgs& a, hipStream_t st) {
+  const int64_t groups = a.b * a.g * a.cblk;
+  // Few channels are spread over as many SIMDs as there are by taking 32 or 16 of
+  // them a workgroup.  us, with 64 first: 256 tokens of 2048 channels, 16 states:
+  // 34 and 29; 5 sequences of 333 tokens of 600 channels, 32 states: 58, 40 and
+  // 33; 16 of 700 tokens of 512: 119 and 82, 64 states 173 (in chunks) and 116.
   if (a.n <= 8) return go_shape<T, 4, 2, GATE>(a, st);
+  if (a.n <= 16 && groups <= 128) return go_shape<T, 4, 2, GATE, 2>(a, st);
+  if (a.n <= 32 && groups <= 64) return go_shape<T, 4, 2, GATE, 4>(a, st);
+  if (a.n <= 32 && groups <= 128) return go_shape<T, 8, 2, GATE, 2>(a, st);
   // two states a wave while that leaves no SIMD more than two waves (8 and 16
   // sequences of 2048 tokens of 2048 channels: 220 and 361 us, with four 249
   // and 326, all four before the states were made again)
   if (a.n <= 16)
-    return a.b * a.g * a.cblk <= 256 ? go_shape<T, 8, 2, GATE>(a, st)
-                                     : go_shape<T, 4, 4, GATE>(a, st);
-  // (up to 24 states twos load the SIMDs more evenly: 5 sequences of 333 tokens
-  // of 600 channels, 20 states: 47 and 58 us, 28 states 62 and 59)
+    return groups <= 256 ? go_shape<T, 8, 2, GATE>(a, st) : go_shape<T, 4, 4, GATE>(a, st);
+  // (up to 24 states twos load the SIMDs more evenly: 16 sequences of 700 tokens
+  // of 512 channels, 24 states: 96 and 117 us, 28 states 123 and 116)
   if (a.n <= 32)
-    return a.n <= 24 && a.b * a.g * a.cblk <= 256 ? go_shape<T, 16, 2, GATE>(a, st)
-                                                  : go_shape<T, 8, 4, GATE>(a, st);
+    return a.n <= 24 && groups <= 256 ? go_shape<T, 16, 2, GATE>(a, st)
+                                      : go_shape<T, 8, 4, GATE>(a, st);
+  if (groups <= 64) return go_shape<T, 4, 4, GATE, 4>(a, st);
+  if (groups <= 128) return go_shape<T, 8, 4, GATE, 2>(a, st);
   go_shape<T, 16, 4, GATE>(a, st);
 }
 

@@ -34,6 +34,22 @@ def test_many_sequences(b, l, d, n, gate):
     run_case(b, l, d, n, 1, lens, gate, True, True, F16)
 
 
+# each count of workgroups and of states a wave
+@pytest.mark.parametrize("b", [9, 70, 130, 260])
+@pytest.mark.parametrize("n", [8, 12, 20, 28, 40])
+def test_counts_of_workgroups(b, n):
+    log(f"case scan of {b} sequences, {n} states")
+    lens = [(11 * i) % 40 for i in range(b)]
+    run_case(b, 37, 5, n, 1, lens, True, True, True, F16)
+
+
+@pytest.mark.parametrize("d,n", [(17, 20), (33, 16), (15, 40), (47, 32), (65, 12)])
+def test_channels_of_narrow_workgroups(d, n):
+    """Channels that end inside workgroups of 16 and 32 of them, two groups."""
+    log(f"case scan of {d} channels, {n} states")
+    run_case(2, 50, 2 * d, n, 2, [50, 21], True, True, False, F32)
+
+
 @pytest.mark.parametrize("l", [1, 7, 8, 9, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129])
 def test_lengths_at_the_ends(l):
     """One sequence of each length, beside a longer one."""
