@@ -17,8 +17,8 @@
 // all 64 lanes add; the sums over the states go through LDS, where wave w
 // finishes token w of each four.
 //
-// Bound: the vector units, 80% busy at the four waves a SIMD that the registers
-// leave (two exps and about 24 instructions a state and token).  8 sequences of
+// Bound: the vector units, 88% busy at the four waves a SIMD that the registers
+// leave (28 instructions a state and token, two of them exps).  8 sequences of
 // 2048 tokens of 2048 channels and 16 states: 517 us of 785 for the whole
 // gradient; the chunks' states before it 173, between the chunks 57.  (Two
 // channels a lane: half the waves, 711 and 560 us when both were tried.)

@@ -16,7 +16,7 @@
 //
 // Bound: the vector units, of which a state of a token takes an exp and five
 // other instructions once, not twice as in chunks.  8 sequences of 2048 tokens
-// of 2048 channels and 16 states: 250 us, the vector units 66% busy at the two
+// of 2048 channels and 16 states: 240 us, the vector units 66% busy at the two
 // waves a SIMD that there are.  (One barrier a stage, with the outputs of the
 // stage before and the steps of the next one among the tokens: 1% less there,
 // 2 to 7% more for 32 sequences and up, where its LDS leaves fewer waves.)
