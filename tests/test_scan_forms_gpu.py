@@ -127,3 +127,23 @@ def test_infinite_rates(b, l, d, n):
     got += dwc.selective_scan_step(*a, lengths=lengths, softplus=True)
     for s, t in zip(got, large):
         assert torch.isfinite(s).all() and (s == t).all()
+
+
+def test_two_streams_at_once():
+    """Calls that run side by side have workspaces of their own."""
+    cases = [inputs(26 + i, 2, 300, 96, n, 1, BF16) for i, n in enumerate((16, 40))]
+    dys = [randn(30 + i, 2, 300, 96, dtype=BF16) for i in range(2)]
+    want = [dwc.selective_scan(*a, softplus=True) + dwc.selective_scan_bwd(dy, None, *a, softplus=True)
+            for a, dy in zip(cases, dys)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    sync()
+    got = [[], []]
+    for _ in range(5):
+        for i, (s, a, dy) in enumerate(zip(streams, cases, dys)):
+            with torch.cuda.stream(s):
+                got[i].append(dwc.selective_scan(*a, softplus=True)
+                              + dwc.selective_scan_bwd(dy, None, *a, softplus=True))
+    sync()
+    for runs, ref in zip(got, want):
+        for run in runs:
+            assert all((s == t).all() for s, t in zip(run, ref))
