@@ -66,6 +66,22 @@ __device__ __forceinline__ float rate_of(float a) {
 
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// The decay 2^x of many tokens, m 2^e with m in (1/2, 1].  As one number it is
+// past fp32's range where decays grow long enough, and infinity times a state
+// of 0, or one that is small enough, is not what the tokens make of it one by
+// one.
+struct Decay {
+  float m, e;
+  __device__ __forceinline__ float of(float v) const {
+    return __builtin_ldexpf(m * v, (int)e);
+  }
+};
+__device__ __forceinline__ Decay decay_of(float x) {
+  // (e is held where sums of it stay exact; m takes the rest, and a NaN)
+  const float e = __builtin_ceilf(fminf(fmaxf(x, -1e6f), 1e6f));
+  return {exp2_of(x - e), e};
+}
+
 __device__ __forceinline__ float sigmoid(float x) {
   return __builtin_amdgcn_rcpf(1.f + exp2_of(-kLog2e * x));
 }
@@ -90,6 +106,15 @@ __device__ __forceinline__ int64_t length_of(const ScanArgs& a, int64_t b) {
   if (!a.lengths) return a.l;
   const int64_t n = a.lengths[b];
   return n < 0 ? 0 : (n < a.l ? n : a.l);
+}
+
+// The kernel's arguments, read again from their segment: held in registers
+// over the whole kernel they push others out to memory.
+typedef const __attribute__((address_space(4))) ScanArgs FreshArgs;
+__device__ __forceinline__ FreshArgs& fresh_args() {
+  FreshArgs* p = (FreshArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *p;
 }
 
 }  // namespace scan

@@ -129,6 +129,32 @@ __device__ __forceinline__ const char* from(const void* p, const int64_t (&strid
   return (const char*)((const Elem<T>*)p + (w.b * stride[0] + w.t0 * stride[1] + w.g0));
 }
 
+// The gradient that a chunk hands to the state before it, from zero at its
+// end: r_t = a_t (r_(t+1) + C_t do_t).
+template <int T, int SPL, bool GATE>
+__device__ __forceinline__ void from_the_end(const Where& w, int64_t end, const float (&a2)[SPL],
+                                             float (&r)[SPL]) {
+  FreshArgs& a = fresh_args();
+  const float bias = a.bias ? a.bias[w.c] : 0.f;
+  const float* bc = a.bc + ((w.b * a.g + w.g) * a.nblk + w.blk) * a.lp * (2 * SPL);
+  asm volatile("" : "+v"(bc));  // (vector loads: scalar registers are short)
+#pragma unroll
+  for (int s = 0; s < SPL; ++s) r[s] = 0.f;
+#pragma unroll 1
+  for (int64_t t = end - 1; t >= w.t0; --t) {
+    const float x = load1<T>(a.delta, w.b * a.delta_stride[0] + t * a.delta_stride[1] + w.c);
+    const float dt = step_of(a.softplus, x + bias);
+    float go = load1<T>(a.dy, w.b * a.dy_stride[0] + t * a.dy_stride[1] + w.c);
+    if constexpr (GATE) {
+      const float z = load1<T>(a.z, w.b * a.z_stride[0] + t * a.z_stride[1] + w.c);
+      go *= z * sigmoid(z);
+    }
+#pragma unroll
+    for (int s = 0; s < SPL; ++s)
+      r[s] = exp2_of(dt * a2[s]) * fmaf(bc[t * (2 * SPL) + c_at<SPL, true>(s)], go, r[s]);
+  }
+}
+
 // Each chunk's state from zero and the sum of its steps.  With BWD also, from
 // zero at its end, the gradient that it hands to the state before it:
 //   sum_t (a_t0 ... a_t) C_t do_t,  do = dy silu(z).
@@ -200,9 +226,15 @@ __global__ void __launch_bounds__(64) scan_chunk(ScanArgs a) {
   }
   const int64_t at = ((w.b * a.nc + w.chunk) * a.nblk + w.blk) * SPL * a.d + w.g0;
 #pragma unroll
-  for (int s = 0; s < SPL; ++s) {
-    (a.states + at + (int64_t)s * a.d)[w.in] = h[s];
-    if constexpr (BWD) (a.rstates + at + (int64_t)s * a.d)[w.in] = r[s];
+  for (int s = 0; s < SPL; ++s) (a.states + at + (int64_t)s * a.d)[w.in] = h[s];
+  if constexpr (BWD) {
+    // a product of decays past fp32's range: token by token from the end
+    bool past = false;
+#pragma unroll
+    for (int s = 0; s < SPL; ++s) past = past || !(p[s] <= __FLT_MAX__);
+    if (past) from_the_end<T, SPL, GATE>(w, end, a2, r);
+#pragma unroll
+    for (int s = 0; s < SPL; ++s) (a.rstates + at + (int64_t)s * a.d)[w.in] = r[s];
   }
   if (w.blk == 0) (a.dts + (w.b * a.nc + w.chunk) * a.d + w.g0)[w.in] = (float)sum;
 }
@@ -215,7 +247,7 @@ __global__ void __launch_bounds__(64) scan_chunk(ScanArgs a) {
 constexpr int kRun = 16;
 template <int RUNS>
 __global__ void __launch_bounds__(64 * RUNS) scan_combine(ScanArgs a) {
-  __shared__ float part[2][RUNS][2][64];
+  __shared__ float part[2][RUNS][3][64];
   const int np = a.nblk * a.spl, blocks = (a.d + 63) / 64;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t row = blockIdx.x / (uint32_t)blocks;  // of b np
@@ -234,38 +266,43 @@ __global__ void __launch_bounds__(64 * RUNS) scan_combine(ScanArgs a) {
   int side = 0;
   for (int k0 = 0; k0 < a.nc; k0 += run * RUNS, side ^= 1) {
     const int first = k0 + wave * run;
-    float v[kRun], p[kRun];
+    float v[kRun], dt[kRun];
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
       const int k = first + j, q = back ? a.nc - 1 - k : k;
-      v[j] = p[j] = 0.f;  // (a chunk that is not there changes nothing)
+      v[j] = dt[j] = 0.f;  // (a chunk that is not there changes nothing)
       if (j < run && k < a.nc) {
         v[j] = x[q * step];
-        p[j] = dts[(int64_t)q * a.d];
+        dt[j] = dts[(int64_t)q * a.d];
       }
     }
-    float sum = 0.f, keep = 1.f;
+    Decay p[kRun], keep = {1.f, 0.f};
+    float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
-      p[j] = exp2_of(a2 * p[j]);
-      sum = fmaf(p[j], sum, v[j]);
-      keep *= p[j];
+      p[j] = decay_of(a2 * dt[j]);
+      sum = p[j].of(sum) + v[j];
+      keep.m *= p[j].m;
+      keep.e += p[j].e;
     }
     part[side][wave][0][lane] = sum;
-    part[side][wave][1][lane] = keep;
+    // (16 factors above 1/2: the product is brought back there)
+    part[side][wave][1][lane] = __builtin_amdgcn_frexp_mantf(keep.m);
+    part[side][wave][2][lane] = keep.e + (float)__builtin_amdgcn_frexp_expf(keep.m);
     __syncthreads();  // (two sides: one barrier keeps readers and writers apart)
     float mine = carry;
 #pragma unroll
     for (int i = 0; i < RUNS; ++i) {
       if (i == wave) mine = carry;
-      carry = fmaf(part[side][i][1][lane], carry, part[side][i][0][lane]);
+      const Decay all = {part[side][i][1][lane], part[side][i][2][lane]};
+      carry = all.of(carry) + part[side][i][0][lane];
     }
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
       const int k = first + j, q = back ? a.nc - 1 - k : k;
       if (j < run && k < a.nc) {
         if (c0 < a.d) x[q * step] = mine;
-        mine = fmaf(p[j], mine, v[j]);
+        mine = p[j].of(mine) + v[j];
       }
     }
   }

@@ -148,15 +148,6 @@ __device__ __forceinline__ void finish_none(const Args& a, int64_t at, uint32_t 
   if constexpr (GATE) store1<T>((Elem<T>*)a.dz + at, in, 0.f);
 }
 
-// The kernel's arguments, read again from their segment: held in registers
-// over the whole kernel they push others out to memory.
-typedef const __attribute__((address_space(4))) ScanArgs FreshArgs;
-__device__ __forceinline__ FreshArgs& fresh_args() {
-  FreshArgs* p = (FreshArgs*)__builtin_amdgcn_kernarg_segment_ptr();
-  asm volatile("" : "+s"(p));
-  return *p;
-}
-
 enum { DT = 0, U, GO, SLOPE, DZ, kOf };  // of a token and channel, in LDS
 
 // What the way back needs of one token.

@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
       if (t0 / kStage % kAgain == kAgain - 1) {
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-          h[s] = start[s] = fmaf(exp2_of(a2[s] * sum), start[s], from[s]);
+          h[s] = start[s] = decay_of(a2[s] * sum).of(start[s]) + from[s];
           from[s] = 0.f;
         }
         sum = 0.f;
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(64 * NW) scan_wide(ScanArgs a) {
 #pragma unroll
   for (int s = 0; s < S; ++s)
     if (on && n0 + s < a.n)
-      (s1 + n0 + s)[in * (uint32_t)a.n] = fmaf(exp2_of(a2[s] * sum), start[s], from[s]);
+      (s1 + n0 + s)[in * (uint32_t)a.n] = decay_of(a2[s] * sum).of(start[s]) + from[s];
 }
 
 template <int T, int NW, int S, bool GATE, int Q = 1>

@@ -479,9 +479,9 @@ int dwc_causal_conv_bwd(const dwc_causal_conv_problem* p, const void* dy,
  *       not used, y there is 0, s1 is the state after the last token
  *   y : b x l x d of dtype, dense
  * Infinities and NaN act as arithmetic has it, but for an infinite A, which is
- * taken as fp32's largest value.  The decays of up to 128 tokens are joined as
- * exp(A sum dt): where A > 0 takes that past fp32's range, states are infinite
- * or NaN. */
+ * taken as fp32's largest value.  A decay exp(dt_t A) is infinite past fp32's
+ * range, and NaN times a state of 0; products of decays over tokens have no
+ * such limit. */
 typedef struct {
     int64_t b, l;           /* >= 0                                         */
     int64_t u_stride[2], delta_stride[2], z_stride[2],
