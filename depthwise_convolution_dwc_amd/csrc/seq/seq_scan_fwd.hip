@@ -518,12 +518,17 @@ void scan_split(ScanArgs* a, bool bwd) {
   if (bwd && a->nblk > 2) a->nblk = (a->nblk + 3) / 4 * 4;
   a->gblk = (a->nblk + 3) / 4;
   a->lp = (a->l + kGradChunk - 1) / kGradChunk * kGradChunk;
+  if (a->one) {
+    a->tc = (int)a->l;
+    a->nc = 1;
+    return;
+  }
   if (bwd) {
     a->tc = kGradChunk;
   } else {
     const int64_t waves = a->b * a->g * a->cblk * a->nblk;
     // chunks for 8 waves a SIMD (4 sequences of 2048 tokens: 169 us, 187 us for 4)
-    int64_t nc = waves >= 4096 || a->b == 0 || a->one ? 1 : 8192 / waves;
+    int64_t nc = waves >= 4096 || a->b == 0 ? 1 : 8192 / waves;
     const int64_t most = (a->l + 31) / 32;
     if (nc > most) nc = most;
     if (nc < 1) nc = 1;
