@@ -441,9 +441,13 @@ int resnorm_groups(const ResNormArgs& a, const ResNormShape& s, bool bwd) {
   int64_t most = (s.lpr <= 256 ? 1024 : 256) * (bwd ? 1 : 2);
   const int64_t need = (a.rows + per - 1) / per;
   if (s.vec == 1 && s.lpr == 256 && need > 0) {
-    // as many as are resident, with the same number of rows each (3333 rows of
-    // 771: 16 and 33 us, 18 and 37 by the rule above; a wave a row does not gain)
-    most = bwd ? 1280 : 1792;
+    // as many as are resident, with the same number of rows each: seven waves a
+    // SIMD forward and five back up to 1024 columns, four and three past them.
+    // fp16, gated, us forward and back, by the rule above and so: 3333 rows of
+    // 771: 17 and 39, 17 and 33; 16384 of 771: 78 and 123, 54 and 101; 3333 of
+    // 1500: 33 and 86, 34 and 67; 16384 of 1500: 120 and 488, 118 and 358 (with
+    // 1792 and 1280 there 142 and 419).  A wave a row does not gain.
+    most = s.nv <= 4 ? (bwd ? 1280 : 1792) : (bwd ? 768 : 1024);
     const int64_t rounds = (need + most - 1) / most;
     most = (need + rounds - 1) / rounds;
   }

@@ -1,12 +1,13 @@
-"""What the selective scan asks for as workspace, and which sizes it takes,
-without a GPU."""
+"""What the selective scan and the residual norm ask for as workspace, and
+which sizes they take, without a GPU."""
 
+import ctypes
 import os
 
 import pytest
 
 import depthwise_convolution_dwc_amd as dwc
-from test_space_cpu import scan, scan_need
+from test_space_cpu import norm, scan, scan_need
 
 pytestmark = pytest.mark.skipif(not os.path.exists(dwc.LIB_PATH), reason="libdwc.so not built")
 
@@ -26,3 +27,16 @@ def test_chunks_hold_their_states():
 def test_limits_of_chunks_are_not_those_of_one_pass():
     """More sequences times channels than the chunks' launches take."""
     assert scan_need(scan(b=65535, l=129, d=2112, n=16, g=1), 0)[0] == 0
+
+
+@pytest.mark.parametrize("c,resident", [(771, 1280), (1023, 1280), (1031, 768), (1500, 768),
+                                        (2047, 768)])
+@pytest.mark.parametrize("rows", [700, 3333, 16384])
+def test_odd_rows_of_the_norm_are_spread_over_resident_workgroups(rows, c, resident):
+    """Five waves a SIMD hold four values a lane, three hold eight; a workgroup
+    leaves a row of three partial sums."""
+    need = ctypes.c_size_t()
+    p = norm(rows=rows, c=c, x=2, y=2)
+    assert dwc.lib().dwc_residual_norm_bwd_workspace_size(ctypes.byref(p), ctypes.byref(need)) == 0
+    rounds = -(-rows // resident)
+    assert need.value == -(-rows // rounds) * 3 * c * 4
