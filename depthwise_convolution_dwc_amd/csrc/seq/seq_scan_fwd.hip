@@ -10,8 +10,8 @@
 //
 // Bound: the vector units.  A state of a token takes an exp (two instructions'
 // time) and four other instructions: 4096 tokens of 2048 channels and 16 states
-// take 35 us for the chunks' states (three of the four), 10 between the chunks
-// and 43 for the outputs; 5 for the layout before them.
+// take 33 us for the chunks' states (three of the four), 10 between the chunks
+// and 40 for the outputs; 5 for the layout before them.
 #include "seq_scan.h"
 
 namespace dwc {
@@ -488,11 +488,11 @@ void prepare_bwd(const ScanArgs& a, hipStream_t st) {
 // one token's time (by the shape of its workgroups, see go_wide) while these
 // have SIMDs to themselves, then kMore a token and 64 channels; the chunks take
 // kTwo a token and 64 channels and kFixed besides, for their launches and the
-// states between them.  bf16, us: 512 tokens of 2048 channels, 16 states: 51
-// and 48 in chunks, 1024 tokens: 96 and 50; 4 sequences of 1024 tokens: both
-// 100, 16 of 2048: 361 and 501; 32 states, 700 tokens of 512 channels, 4
-// sequences: 62 and 68, 16: 83 and 160; 64 states, 4 such: 86 and 82, one of 256
-// channels: 82 and 48.
+// states between them.  bf16, us: 512 tokens of 2048 channels, 16 states: 50
+// and 48 in chunks, 1024 tokens: 95 and 50; 4 sequences of 1024 tokens: 97 and
+// 100, 16 of 2048: 359 and 499; 32 states, 700 tokens of 512 channels, 4
+// sequences: 61 and 68, 16: 77 and 147; 64 states, 4 such: 83 and 84, one of 256
+// channels: 80 and 49.
 static bool one_pass(const ScanArgs& a) {
   if (a.n > 64) return false;
   const int blocks = (a.n + 15) / 16;
@@ -527,7 +527,8 @@ void scan_split(ScanArgs* a, bool bwd) {
     a->tc = kGradChunk;
   } else {
     const int64_t waves = a->b * a->g * a->cblk * a->nblk;
-    // chunks for 8 waves a SIMD (4 sequences of 2048 tokens: 169 us, 187 us for 4)
+    // chunks for 8 waves a SIMD (2 sequences of 4096 tokens of 2048 channels: 147
+    // us, 164 for 4)
     int64_t nc = waves >= 4096 || a->b == 0 ? 1 : 8192 / waves;
     const int64_t most = (a->l + 31) / 32;
     if (nc > most) nc = most;

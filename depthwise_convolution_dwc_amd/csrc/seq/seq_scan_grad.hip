@@ -19,8 +19,8 @@
 //
 // Bound: the vector units, 88% busy at the four waves a SIMD that the registers
 // leave (28 instructions a state and token, two of them exps).  8 sequences of
-// 2048 tokens of 2048 channels and 16 states: 517 us of 785 for the whole
-// gradient; the chunks' states before it 173, between the chunks 57.  (Two
+// 2048 tokens of 2048 channels and 16 states: 473 us of 724 for the whole
+// gradient; the chunks' states before it 158, between the chunks 58.  (Two
 // channels a lane: half the waves, 711 and 560 us when both were tried.)
 #include "seq_scan.h"
 

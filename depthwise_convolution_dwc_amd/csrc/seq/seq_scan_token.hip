@@ -4,8 +4,8 @@
 // A lane owns four states of a channel, LPC lanes a channel, for all tokens:
 // a wave reads and writes 1 KB of states in one instruction each.  Bound for
 // many sequences: memory, the states read and written once (128 sequences of
-// 4096 channels, 16 states: 19 us, 3.8 TB/s; two or four channels a lane 21 and
-// 23); for one sequence the latency of its loads.
+// 4096 channels, 16 states: 17.5 us, 4.1 TB/s; two or four channels a lane took
+// 21 and 23 where one took 19); for one sequence the latency of its loads.
 #include "seq_scan.h"
 
 namespace dwc {

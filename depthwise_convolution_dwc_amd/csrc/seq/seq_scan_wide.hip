@@ -16,7 +16,7 @@
 //
 // Bound: the vector units, of which a state of a token takes an exp and five
 // other instructions once, not twice as in chunks.  8 sequences of 2048 tokens
-// of 2048 channels and 16 states: 240 us, the vector units 66% busy at the two
+// of 2048 channels and 16 states: 219 us, the vector units 65% busy at the two
 // waves a SIMD that there are.  (One barrier a stage, with the outputs of the
 // stage before and the steps of the next one among the tokens: 1% less there,
 // 2 to 7% more for 32 sequences and up, where its LDS leaves fewer waves.)
@@ -250,19 +250,20 @@ void go_wide(const ScanArgs& a, hipStream_t st) {
   const int64_t groups = a.b * a.g * a.cblk;
   // Few channels are spread over as many SIMDs as there are by taking 32 or 16 of
   // them a workgroup.  us, with 64 first: 256 tokens of 2048 channels, 16 states:
-  // 34 and 29; 5 sequences of 333 tokens of 600 channels, 32 states: 58, 40 and
-  // 33; 16 of 700 tokens of 512: 119 and 82, 64 states 173 (in chunks) and 116.
+  // 33 and 28; 5 sequences of 333 tokens of 600 channels, 32 states: 57, 40 and
+  // 33; 16 of 700 tokens of 512: 115 and 78, 64 states 176 and 114.
   if (a.n <= 8) return go_shape<T, 4, 2, GATE>(a, st);
   if (a.n <= 16 && groups <= 128) return go_shape<T, 4, 2, GATE, 2>(a, st);
   if (a.n <= 32 && groups <= 64) return go_shape<T, 4, 2, GATE, 4>(a, st);
   if (a.n <= 32 && groups <= 128) return go_shape<T, 8, 2, GATE, 2>(a, st);
   // two states a wave while that leaves no SIMD more than two waves (8 and 16
-  // sequences of 2048 tokens of 2048 channels: 220 and 361 us, with four 249
-  // and 326, all four before the states were made again)
+  // sequences of 2048 tokens of 2048 channels: 224 and 350 us, with four 280
+  // and 357; 32 of 1024 tokens, 128 of 256: 328 and 321, with four 306 and 290)
   if (a.n <= 16)
     return groups <= 256 ? go_shape<T, 8, 2, GATE>(a, st) : go_shape<T, 4, 4, GATE>(a, st);
-  // (up to 24 states twos load the SIMDs more evenly: 16 sequences of 700 tokens
-  // of 512 channels, 24 states: 96 and 117 us, 28 states 123 and 116)
+  // (up to 24 states twos load the SIMDs more evenly: 32 sequences of 700 tokens
+  // of 512 channels, 24 states: 99 and 116 us, 28 states 113 and 118; 48
+  // sequences, 24 states: 185 and 177)
   if (a.n <= 32)
     return a.n <= 24 && groups <= 256 ? go_shape<T, 16, 2, GATE>(a, st)
                                       : go_shape<T, 8, 4, GATE>(a, st);

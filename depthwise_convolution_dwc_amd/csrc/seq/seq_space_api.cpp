@@ -247,7 +247,8 @@ int check_resnorm(const dwc_resnorm_problem* p, bool bwd) {
   for (const int64_t s : stride)
     if (s > kMost >> 8 || p->rows > kMost / s)
       return fail(DWC_ERR_UNSUPPORTED, "residual norm sizes past the index range");
-  // the widest rows take 1024 threads each, the columns' sums 64 a column
+  // rows past 8192 values take 1024 threads each (the limit holds from 513 on),
+  // the columns' sums 64 a column
   if (p->rows >= (p->c > 512 ? (int64_t)1 << 22 : (int64_t)1 << 26) ||
       p->c >= (bwd ? (int64_t)1 << 24 : (int64_t)1 << 31))
     return fail(DWC_ERR_UNSUPPORTED, "residual norm sizes past the launch range");
